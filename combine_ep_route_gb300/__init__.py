@@ -6,4 +6,7 @@ for PyTorch tensors. See ``ep.EpContext``.
 """
 from .ep import (EpConfig, EpContext, DispatchOut, AgrsBuffers, agrs, alloc_agrs_buffers,  # noqa: F401
                  capacities, workspace_bytes)
+from .product import (act_grad, experts_product, experts_product_dgrad, experts_product_wgrad,  # noqa: F401
+                      linear, linear_dgrad, linear_wgrad)
+from .router import route_topk, route_topk_backward  # noqa: F401
 from ._lib import EpError  # noqa: F401

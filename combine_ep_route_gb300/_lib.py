@@ -34,6 +34,9 @@ EP_F32 = 2
 EP_FP8 = 3
 EP_FP4X2 = 4
 
+EP_ACT_NONE, EP_ACT_RELU, EP_ACT_SILU, EP_ACT_GELU, EP_ACT_GELU_TANH, EP_ACT_SWIGLU = range(6)
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = range(2)
+
 EP_PATH_FUSED = 0
 EP_PATH_SENDBUF = 1
 
@@ -92,6 +95,17 @@ class EpAgrsBuffersC(C.Structure):
                 ("status", C.c_void_p)]
 
 
+class EpProductC(C.Structure):
+    _fields_ = [("groups", C.c_int32), ("rows", C.c_int32), ("k", C.c_int32), ("n", C.c_int32),
+                ("act", C.c_int32), ("out_dtype", C.c_int32), ("counts", C.c_void_p),
+                ("status", C.c_void_p)]
+
+
+class EpTopkC(C.Structure):
+    _fields_ = [("tokens", C.c_int32), ("E", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32),
+                ("renormalize", C.c_int32), ("logits_dtype", C.c_int32), ("scale", C.c_float)]
+
+
 # name -> (restype, argtypes); mirrors include/ep.h one to one
 SIGNATURES = {
     "ep_capacities": (C.c_int, [C.POINTER(EpConfigC), C.POINTER(C.c_int32), C.POINTER(C.c_int32),
@@ -115,6 +129,13 @@ SIGNATURES = {
                                   C.POINTER(EpRouteOutputsC), C.c_void_p]),
     "ep_agrs": (C.c_int, [C.POINTER(EpConfigC), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                           C.POINTER(EpAgrsBuffersC), C.c_int32, C.c_void_p, C.c_void_p]),
+    "ep_product": (C.c_int, [C.POINTER(EpProductC)] + [C.c_void_p] * 7),
+    "ep_product_dgrad": (C.c_int, [C.POINTER(EpProductC)] + [C.c_void_p] * 5),
+    "ep_product_wgrad": (C.c_int, [C.POINTER(EpProductC), C.c_void_p, C.c_void_p, C.c_int32,
+                                   C.c_void_p, C.c_void_p, C.c_void_p]),
+    "ep_act_grad": (C.c_int, [C.POINTER(EpProductC)] + [C.c_void_p] * 4),
+    "ep_topk_route": (C.c_int, [C.POINTER(EpTopkC)] + [C.c_void_p] * 5),
+    "ep_topk_route_backward": (C.c_int, [C.POINTER(EpTopkC)] + [C.c_void_p] * 5),
 }
 
 _lib = None

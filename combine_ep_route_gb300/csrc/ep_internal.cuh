@@ -365,5 +365,8 @@ cudaError_t launch_scale_move(const ScaleMoveParams &p, int grid, cudaStream_t s
 // both stages as one-wave grids over num_sms SMs
 cudaError_t launch_combine_two_stage(const PartialParams &a, const GatherParams &b, bool out_f32,
                                      int num_sms, cudaStream_t st);
+// out[g][c] (+)= the sum over group g's rows in use of src[g][row][c] (bf16), n columns
+cudaError_t launch_row_sums(const void *src, const int32_t *counts, int groups, int rows, int n,
+                            bool out_f32, bool accumulate, void *out, cudaStream_t st);
 
 }  // namespace ep

@@ -1,0 +1,37 @@
+// product.cuh -- parameters of the tensor-core products (product.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "tcgen05.cuh"
+
+namespace ep {
+
+enum ProductMode { PRODUCT_FORWARD = 0, PRODUCT_DGRAD = 1, PRODUCT_WGRAD = 2 };
+
+constexpr int kBoxes = 4;   // token-row boxes of the column operand: 128, 64, 32, 16 rows
+
+// One product, seen by the kernel as D[col][lane] = sum_r A[lane][r] B[col][r]:
+//   forward  lanes = output features n, columns = tokens, r = k
+//   dgrad    lanes = input features k,  columns = tokens, r = n
+//   wgrad    lanes = k, columns = n, r = tokens in use
+struct ProductParams {
+    CUtensorMap a;            // lane operand
+    CUtensorMap b[kBoxes];    // column operand (wgrad: b[0] only)
+    const int32_t *counts;    // rows in use per group, or null (= rows)
+    int groups, rows;
+    int lanes;                // output features (gated forward: of the activation's output)
+    int cols;                 // wgrad: n
+    int red;                  // forward: k, dgrad: n (wgrad: the group's rows in use)
+    int lane_tiles, col_max;  // lane tiles per group; widest column tile
+    int act, interleave;      // gated forward: 8 or 16 gate rows, then as many up rows
+    int out_f32, accumulate;
+    const __nv_bfloat16 *bias, *residual;
+    const __nv_bfloat16 *z;   // dgrad: pre-activation of the product's input
+    __nv_bfloat16 *preact;    // forward: pre-activation kept for the backward pass
+    void *out;
+    int32_t *status;
+    uint64_t wait_limit_ns;
+};
+
+}  // namespace ep

@@ -1,0 +1,178 @@
+// rowops.cu -- row-wise companions of the products: the bias gradient (a sum of
+// rows per group) and the gradient through an activation that no product follows.
+// Both read each byte once and are bound by HBM.
+#include "ep_internal.cuh"
+
+#include <cooperative_groups.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include "act.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVecs = 8;             // 16-byte vectors of a row one CTA covers (64 columns)
+constexpr int kRowLanes = kThreads / kVecs;
+constexpr int kSplit = 8;            // CTAs of a cluster that share a group's rows
+
+// Sums over rows, fp32, in a fixed order: each thread walks rows r, r + 32 * split,
+// ..., then the CTA's 32 row threads and the cluster's CTAs are added in order.
+template <bool OUT_F32>
+__global__ void __launch_bounds__(kThreads) row_sums_kernel(const uint4 *src, const int32_t *counts, int rows,
+                                                            int n, int split, int accumulate, void *out) {
+    __shared__ float part[kRowLanes][kVecs * 8 + 1];
+    __shared__ float sums[kVecs * 8];
+    const int g = blockIdx.z, v = blockIdx.y * kVecs + threadIdx.x % kVecs, r0 = threadIdx.x / kVecs;
+    const int nvec = n / 8;
+    const int count = counts ? max(0, min(counts[g], rows)) : rows;
+    float a[8] = {};
+    if (v < nvec) {
+        const uint4 *p = src + (size_t)g * rows * nvec + v;
+        const int step = kRowLanes * split;
+        int r = blockIdx.x * kRowLanes + r0;
+        for (; r + 3 * step < count; r += 4 * step) {
+            uint4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __ldg(p + (size_t)(r + i * step) * nvec);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 f = unpack_bf16x2(w[q]);
+                    a[2 * q] += f.x, a[2 * q + 1] += f.y;
+                }
+            }
+        }
+        for (; r < count; r += step) {
+            const uint4 x = __ldg(p + (size_t)r * nvec);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 f = unpack_bf16x2(w[q]);
+                a[2 * q] += f.x, a[2 * q + 1] += f.y;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[r0][(threadIdx.x % kVecs) * 8 + i] = a[i];
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c < kVecs * 8) {
+        float s = 0.f;
+        for (int r = 0; r < kRowLanes; ++r) s += part[r][c];
+        sums[c] = s;
+    }
+    if (split > 1) {
+        namespace cg = cooperative_groups;
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        if (blockIdx.x == 0 && c < kVecs * 8) {
+            float s = 0.f;
+            for (int i = 0; i < split; ++i) s += *cluster.map_shared_rank(&sums[c], i);
+            sums[c] = s;
+        }
+        cluster.sync();
+        if (blockIdx.x != 0) return;
+    }
+    const int col = blockIdx.y * kVecs * 8 + c;
+    if (c < kVecs * 8 && col < n) {
+        const size_t at = (size_t)g * n + col;
+        if (OUT_F32) {
+            float *o = static_cast<float *>(out);
+            o[at] = accumulate ? o[at] + sums[c] : sums[c];
+        } else {
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(out);
+            o[at] = __float2bfloat16_rn(accumulate ? __bfloat162float(o[at]) + sums[c] : sums[c]);
+        }
+    }
+}
+
+// One thread per 16-byte vector of dy, rows in use only.
+__global__ void __launch_bounds__(kThreads) act_grad_kernel(const uint4 *dy, const uint4 *z, uint4 *dz,
+                                                            const int32_t *counts, int groups, int rows,
+                                                            int nvec, int act) {
+    const bool gated = act == EP_ACT_SWIGLU;
+    for (int g = blockIdx.y; g < groups; g += gridDim.y) {
+        const int count = counts ? max(0, min(counts[g], rows)) : rows;
+        const long long items = (long long)count * nvec;
+        for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < items;
+             i += (long long)gridDim.x * kThreads) {
+            const size_t row = (size_t)g * rows + (size_t)(i / nvec);
+            const int v = (int)(i % nvec);
+            const size_t zi = row * nvec * (gated ? 2 : 1) + v;
+            const uint4 d4 = __ldg(dy + row * nvec + v), a4 = __ldg(z + zi);
+            const uint4 b4 = gated ? __ldg(z + zi + nvec) : make_uint4(0, 0, 0, 0);
+            const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w}, a[4] = {a4.x, a4.y, a4.z, a4.w},
+                           b[4] = {b4.x, b4.y, b4.z, b4.w};
+            uint32_t oa[4], ob[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 dv = unpack_bf16x2(d[q]), zv = unpack_bf16x2(a[q]), uv = unpack_bf16x2(b[q]);
+                if (gated) {
+                    oa[q] = pack_bf16x2_rn(dv.x * uv.x * act_slope(zv.x, EP_ACT_SILU),
+                                           dv.y * uv.y * act_slope(zv.y, EP_ACT_SILU));
+                    ob[q] = pack_bf16x2_rn(dv.x * act_value(zv.x, EP_ACT_SILU),
+                                           dv.y * act_value(zv.y, EP_ACT_SILU));
+                } else {
+                    oa[q] = pack_bf16x2_rn(dv.x * act_slope(zv.x, act), dv.y * act_slope(zv.y, act));
+                    ob[q] = 0;
+                }
+            }
+            dz[zi] = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+            if (gated) dz[zi + nvec] = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_row_sums(const void *src, const int32_t *counts, int groups, int rows, int n, bool out_f32,
+                            bool accumulate, void *out, cudaStream_t st) {
+    const int tiles = (n + kVecs * 8 - 1) / (kVecs * 8);
+    if (tiles > 65535) return cudaErrorInvalidValue;
+    // few column tiles with many rows: a cluster's CTAs share the rows
+    const int split = (long long)tiles * groups < 512 && rows > 4 * kRowLanes ? kSplit : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split, tiles, groups);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const uint4 *s = static_cast<const uint4 *>(src);
+    return out_f32 ? cudaLaunchKernelEx(&cfg, row_sums_kernel<true>, s, counts, rows, n, split, (int)accumulate, out)
+                   : cudaLaunchKernelEx(&cfg, row_sums_kernel<false>, s, counts, rows, n, split, (int)accumulate, out);
+}
+
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int ep_act_grad(const ep_product_t *a, const void *dy, const void *preact, void *dz, void *stream) {
+    if (!a || a->groups < 1 || a->groups > EP_MAX_E || a->rows < 0 || a->n < 8 || a->n % 8 || a->n > (1 << 24) ||
+        (long long)a->groups * a->rows >= (1LL << 31) || a->act <= EP_ACT_NONE || a->act > EP_ACT_SWIGLU ||
+        a->out_dtype != EP_BF16)
+        return EP_ERR_INVALID_ARG;
+    if (a->rows == 0) return EP_OK;
+    if (!dy || !preact || !dz || reinterpret_cast<uintptr_t>(a->counts) % 4)
+        return EP_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(preact) | reinterpret_cast<uintptr_t>(dz)) % 16)
+        return EP_ERR_INVALID_ARG;
+    const long long per_group = ((long long)a->rows * (a->n / 8) + kThreads - 1) / kThreads;
+    // about sixteen CTAs per SM in all, however many groups share them
+    const long long want = a->groups >= 2048 ? 1 : 2432 / a->groups + 1;
+    const dim3 grid((unsigned)(per_group < want ? per_group : want), (unsigned)a->groups);
+    nvtxRangePushA("ep:act_grad");
+    act_grad_kernel<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        static_cast<const uint4 *>(dy), static_cast<const uint4 *>(preact), static_cast<uint4 *>(dz), a->counts,
+        a->groups, a->rows, a->n / 8, a->act);
+    nvtxRangePop();
+    return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}

@@ -1,0 +1,71 @@
+"""The top-k router: logits to the expert ids and weights that dispatch takes, and
+the logits' gradient (``ep_topk_route``, ``ep_topk_route_backward`` in include/ep.h)."""
+from __future__ import annotations
+
+import ctypes as C
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib as L
+from .ep import _need, _stream_ptr
+
+_SCORES = {"softmax": L.EP_SCORE_SOFTMAX, "sigmoid": L.EP_SCORE_SIGMOID}
+_TYPES = {torch.bfloat16: L.EP_BF16, torch.float32: L.EP_F32}
+
+
+def _args(logits: torch.Tensor, top_k: int, score: str, renormalize: bool, scale: float) -> L.EpTopkC:
+    if score not in _SCORES:
+        raise ValueError(f"score: want one of {sorted(_SCORES)}, got {score!r}")
+    if logits.dtype not in _TYPES or logits.dim() < 1 or not logits.is_contiguous() or logits.device.type != "cuda":
+        raise ValueError(f"logits: want contiguous bfloat16 or float32 [..., E] on a CUDA device, got {logits.dtype} "
+                         f"{tuple(logits.shape)} on {logits.device} (contiguous={logits.is_contiguous()})")
+    E = logits.shape[-1]
+    if not 1 <= E <= L.EP_MAX_E or not 1 <= top_k <= min(E, L.EP_MAX_TOPK):
+        raise ValueError(f"want 1..{L.EP_MAX_E} experts and top_k in 1..min(E, {L.EP_MAX_TOPK}), got E={E}, top_k={top_k}")
+    return L.EpTopkC(logits.numel() // E, E, top_k, _SCORES[score], 1 if renormalize else 0,
+                     _TYPES[logits.dtype], scale)
+
+
+def route_topk(logits: torch.Tensor, top_k: int, *, score: str = "softmax", renormalize: bool = True,
+               bias: Optional[torch.Tensor] = None, scale: float = 1.0,
+               out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``(topk_ids int32, topk_weights float32)``, both ``[..., top_k]``, for ``logits`` ``[..., E]``.
+
+    Experts are chosen by ``logits + bias``, largest first, ties to the lowest id; weights are
+    ``scale`` times the score of the unbiased logit, divided by the chosen scores' sum with
+    ``renormalize``. A logit of minus infinity (or NaN) masks its expert; a row with fewer than
+    ``top_k`` experts left ends in ids of -1, which dispatch drops.
+    """
+    a = _args(logits, top_k, score, renormalize, scale)
+    dev, shape = logits.device, tuple(logits.shape[:-1]) + (top_k,)
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (a.E,), dev)
+    if out is None:
+        out = (torch.empty(shape, dtype=torch.int32, device=dev), torch.empty(shape, dtype=torch.float32, device=dev))
+    ids, weights = out
+    _need(ids, "topk_ids", torch.int32, shape, dev)
+    _need(weights, "topk_weights", torch.float32, shape, dev)
+    L.check(L.lib().ep_topk_route(C.byref(a), logits.data_ptr(), None if bias is None else bias.data_ptr(),
+                                  ids.data_ptr(), weights.data_ptr(), _stream_ptr(stream, dev)), "ep_topk_route")
+    return ids, weights
+
+
+def route_topk_backward(dweights: torch.Tensor, logits: torch.Tensor, topk_ids: torch.Tensor, *,
+                        score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                        out: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The logits' gradient (of the logits' type) for the gradient of ``route_topk``'s weights."""
+    if topk_ids.dim() < 1:
+        raise ValueError("topk_ids: want [..., top_k]")
+    a = _args(logits, topk_ids.shape[-1], score, renormalize, scale)
+    dev, shape = logits.device, tuple(logits.shape[:-1]) + (a.top_k,)
+    _need(topk_ids, "topk_ids", torch.int32, shape, dev)
+    _need(dweights, "dweights", torch.float32, shape, dev)
+    if out is None:
+        out = torch.empty_like(logits)
+    _need(out, "out", logits.dtype, tuple(logits.shape), dev)
+    L.check(L.lib().ep_topk_route_backward(C.byref(a), dweights.data_ptr(), logits.data_ptr(), topk_ids.data_ptr(),
+                                           out.data_ptr(), _stream_ptr(stream, dev)), "ep_topk_route_backward")
+    return out

@@ -479,6 +479,121 @@ int ep_agrs(const ep_config_t *cfg, const int32_t *num_tokens, const void *a1,
             const int32_t *topk_ids, const float *topk_weights, const ep_agrs_buffers_t *buf,
             int32_t out_dtype, void *out, void *stream);
 
+/* --------------------------------------------------------- the layer's products
+ *
+ * The matrix products of the layers around dispatch and combine: the experts'
+ * (one weight per expert, over the batched-experts layout that ep_dispatch
+ * writes, with expert_num_tokens read on the device) and dense ones (one
+ * group). Operands are bf16, sums are fp32, and each output is rounded once.
+ * No context and no workspace; each call enqueues its kernels on `stream` and
+ * can be captured in a graph. Every matrix is dense and row-major, 16-byte
+ * aligned, with n and k multiples of 8.
+ */
+#define EP_ACT_NONE 0
+#define EP_ACT_RELU 1
+#define EP_ACT_SILU 2      /* z * sigmoid(z) */
+#define EP_ACT_GELU 3      /* z * Phi(z), by the error function */
+#define EP_ACT_GELU_TANH 4 /* its tanh approximation */
+#define EP_ACT_SWIGLU 5    /* silu(gate) * up: the pre-activation holds n gate, then n up columns */
+
+typedef struct ep_product {
+    int32_t groups;    /* weights (experts), 1..EP_MAX_E; 1 for a dense product */
+    int32_t rows;      /* row slots per group (expert_cap), >= 0; groups * rows < 2^31 */
+    int32_t k, n;      /* columns of x, columns of the product; multiples of 8, <= 2^24 */
+    int32_t act;       /* EP_ACT_*; EP_ACT_NONE for ep_product_wgrad */
+    int32_t out_dtype; /* EP_BF16 or EP_F32: the type of out / dx / dw and dbias */
+    const int32_t *counts; /* device [groups]: rows in use per group (clamped to 0..rows), or
+                              NULL: all */
+    int32_t *status;   /* device [1] or NULL: set to EP_ERR_TIMEOUT if a bounded wait of the
+                          kernel ran out (its outputs are then invalid); never cleared here */
+} ep_product_t;
+
+/*
+ * ep_product -- per group g and row r in use: z = x[g][r] . w[g]^T + bias[g],
+ * out[g][r] = act(z) + residual[g][r]. Rows not in use are neither read into a
+ * result nor written; they may hold anything.
+ *   x        [groups][rows][k] bf16
+ *   w        [groups][n][k] bf16; EP_ACT_SWIGLU: [groups][2n][k], gate rows first
+ *   bias     [groups][n] ([groups][2n]) bf16, or NULL
+ *   residual [groups][rows][n] bf16, or NULL
+ *   out      [groups][rows][n] out_dtype
+ *   preact   [groups][rows][n] ([groups][rows][2n]) bf16 or NULL: z, for the backward pass
+ * out may be residual itself; no other buffers may overlap.
+ */
+int ep_product(const ep_product_t *args, const void *x, const void *w, const void *bias,
+               const void *residual, void *out, void *preact, void *stream);
+
+/*
+ * ep_product_dgrad -- the gradient of a product's input, taken on through the
+ * activation that made that input: dh = dy[g][r] . w[g], dx = dh * act'(preact).
+ *   dy     [groups][rows][n] bf16
+ *   w      [groups][n][k] bf16 (for a gated product n counts gate and up rows)
+ *   preact [groups][rows][k] bf16, EP_ACT_SWIGLU: [groups][rows][2k]; NULL if and only if
+ *          act is EP_ACT_NONE
+ *   dx     like preact ([groups][rows][k] for EP_ACT_NONE), out_dtype
+ */
+int ep_product_dgrad(const ep_product_t *args, const void *dy, const void *w, const void *preact,
+                     void *dx, void *stream);
+
+/*
+ * ep_product_wgrad -- the gradients of a product's weight and bias, over the rows
+ * in use: dw[g] = sum_r dy[g][r]^T x[g][r], dbias[g] = sum_r dy[g][r]; zeros for a
+ * group with no rows. With accumulate 1 they are added to what dw and dbias hold.
+ *   dy [groups][rows][n], x [groups][rows][k] bf16; dw [groups][n][k] out_dtype;
+ *   dbias [groups][n] out_dtype or NULL
+ */
+int ep_product_wgrad(const ep_product_t *args, const void *dy, const void *x, int32_t accumulate,
+                     void *dw, void *dbias, void *stream);
+
+/*
+ * ep_act_grad -- dz = dy * act'(preact) on the rows in use, for an activation whose
+ * output gradient is at hand (one that no product follows). args->k is not read.
+ *   dy [groups][rows][n] bf16; preact, dz [groups][rows][n] ([groups][rows][2n] for
+ *   EP_ACT_SWIGLU) bf16 (out_dtype must be EP_BF16, act not EP_ACT_NONE)
+ */
+int ep_act_grad(const ep_product_t *args, const void *dy, const void *preact, void *dz,
+                void *stream);
+
+/* Host-side errors of the four: EP_ERR_INVALID_ARG, EP_ERR_CUDA. */
+
+/* ------------------------------------------------------------------ the router */
+#define EP_SCORE_SOFTMAX 0 /* over the E logits of a token */
+#define EP_SCORE_SIGMOID 1 /* of each logit */
+
+typedef struct ep_topk {
+    int32_t tokens;       /* rows, >= 0 */
+    int32_t E;            /* experts, 1..EP_MAX_E */
+    int32_t top_k;        /* 1..min(E, EP_MAX_TOPK) */
+    int32_t score;        /* EP_SCORE_* */
+    int32_t renormalize;  /* 1: the chosen experts' scores are divided by their sum */
+    int32_t logits_dtype; /* EP_BF16 or EP_F32 */
+    float scale;          /* factor on the weights */
+} ep_topk_t;
+
+/*
+ * ep_topk_route -- each token's top_k experts and weights, as ep_dispatch takes
+ * them. Experts are chosen by logit + bias (rounded to fp32), largest first, ties
+ * to the lowest id; weights are scale * score of the unbiased logit. An expert
+ * whose logit (or logit + bias) is NaN or minus infinity is never chosen, and a NaN
+ * logit takes no part in the softmax; a row with fewer than top_k experts left
+ * ends in ids -1 with weight 0.
+ *   logits [tokens][E] logits_dtype; bias [E] float or NULL
+ *   topk_ids [tokens][top_k] int32; topk_weights [tokens][top_k] float
+ */
+int ep_topk_route(const ep_topk_t *args, const void *logits, const float *bias, int32_t *topk_ids,
+                  float *topk_weights, void *stream);
+
+/*
+ * ep_topk_route_backward -- the logits' gradient for the weights' gradient, the
+ * choice of experts held fixed (the bias has no gradient). Ids outside 0..E-1 take no
+ * part; the ids of a row must differ.
+ *   dweights [tokens][top_k] float; logits, topk_ids as above; dlogits like logits
+ */
+int ep_topk_route_backward(const ep_topk_t *args, const float *dweights, const void *logits,
+                           const int32_t *topk_ids, void *dlogits, void *stream);
+
+/* Both: pointers aligned to their element. Host-side errors: EP_ERR_INVALID_ARG, EP_ERR_CUDA. */
+
 #ifdef __cplusplus
 }
 #endif
