@@ -29,20 +29,22 @@ namespace ep {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kLanes = 128;          // accumulator lanes of a tile
-constexpr int kColMax = 256;         // accumulator columns of a tile, at most
-constexpr int kBlockRed = 64;        // reduction elements per stage: one 128-byte swizzled line
-constexpr int kStages = 4;
-constexpr int kABytes = kLanes * kBlockRed * 2;
-constexpr int kBBytes = kColMax * kBlockRed * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kChunkBytes = kBlockRed * 128;   // MN-major: 64 reduction lines of 64 elements
+constexpr int kEpilogueWarps = 8;    // two per quarter of the accumulator lanes
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;
+constexpr int kLanes = 128;          // accumulator lanes of a CTA
+constexpr int kColMax = 256;         // accumulator columns, at most
+constexpr int kSubRed = 64;          // reduction elements of a sub-block: one 128-byte swizzled line
+constexpr int kMaxStages = 12;
+constexpr int kABytes = kLanes * kSubRed * 2;
+constexpr int kChunkBytes = kSubRed * 128;   // MN-major: 64 reduction lines of 64 elements
 constexpr int kTmemCols = 512;       // two accumulators of 256 columns
+constexpr int kMaxSplit = 8;
+constexpr int kBand = 8;              // lane tiles of a band (see find_tile)
+constexpr uint32_t kSleepNs = 1000000;       // of one attempt at a wait
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages], tail[kStages];
+    uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
@@ -50,16 +52,27 @@ struct Shared {
     int first[EP_MAX_E + 1];         // column tiles before each group
 };
 
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + sizeof(Shared);
+constexpr size_t kSmemMax = 227 * 1024;
+constexpr size_t kStageSpace = kSmemMax - 1024 - sizeof(Shared);
+// a split tile's partial sums take the place of the stages
+static_assert((size_t)kLanes * kColMax * 4 <= kStageSpace, "partial sums fit");
+
+// A position in the ring of stages: stage and phase parity.
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == stages) s = 0, phase ^= 1;
+    }
+};
 
 // A wait of one of the kernel's roles: bounded, and cut short once any role of
 // the CTA has given up.
-__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Shared *sh,
-                                          const ProductParams &p) {
-    if (mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Shared *sh, const ProductParams &p) {
+    if (mbar_try_wait_ns(bar, parity, kSleepNs)) return true;
     const uint64_t t0 = global_ns();
     volatile int *abort = &sh->abort;
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_try_wait_ns(bar, parity, kSleepNs)) {
         if (*abort) return false;
         if (global_ns() - t0 > p.wait_limit_ns) {
             *abort = 1;
@@ -71,19 +84,21 @@ __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Shared
 }
 
 struct Tile {
-    int g, lane0, col0, cols, n_mma, red, blocks;
+    int g, lane0;            // group; this CTA's first output feature
+    int col0, cols, n_mma;   // first column, columns in use, columns of the MMA
+    int red, blocks;         // reduction length and blocks
 };
 
-// Column tiles of a group are of equal width (a multiple of 16), so 260 rows
-// make two tiles of 144 and 116 and not of 256 and 4.
+// Column tiles of a group are of equal width (a multiple of 16 per CTA), so 260
+// rows make two tiles of 144 and 116 and not of 256 and 4.
 template <int MODE>
 __device__ __forceinline__ int col_tiles(const ProductParams &p, int count) {
     const int cols = MODE == PRODUCT_WGRAD ? p.cols : count;
     return (cols + p.col_max - 1) / p.col_max;
 }
 
-template <int MODE, bool GATED>
-__device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *sh, int t) {
+template <int MODE, bool GATED, int CG>
+__device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *sh, int t, uint32_t rank) {
     int lo = 0, hi = p.groups;       // first[lo] * lane_tiles <= t < first[hi] * lane_tiles
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -98,15 +113,30 @@ __device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *
     const int ct = sh->first[lo + 1] - sh->first[lo];
     const int count = sh->count[lo];
     const int all = MODE == PRODUCT_WGRAD ? p.cols : count;
-    const int lt = r / ct;
-    const int width = ((all + ct - 1) / ct + 15) & ~15;
-    x.lane0 = lt * (GATED && MODE == PRODUCT_FORWARD ? kLanes / 2 : kLanes);
-    x.col0 = (r - lt * ct) * width;
+    // bands of kBand lane tiles, lane tiles innermost: the tiles in flight at a time form
+    // a square rather than a strip, so each operand block is fetched by several of them
+    const int band = r / (kBand * ct), in_band = r - band * kBand * ct;
+    const int high = min(kBand, p.lane_tiles - band * kBand);
+    const int lt = band * kBand + in_band % high, c = in_band / high;
+    constexpr int kUnit = 16 * CG;
+    constexpr int kPer = GATED && MODE == PRODUCT_FORWARD ? kLanes / 2 : kLanes;
+    const int width = ((all + ct - 1) / ct + kUnit - 1) / kUnit * kUnit;
+    x.lane0 = (CG == 1 ? lt : lt * 2 + (int)rank) * kPer;
+    x.col0 = c * width;
     x.cols = min(width, all - x.col0);
-    x.n_mma = (x.cols + 15) & ~15;
+    x.n_mma = (x.cols + kUnit - 1) / kUnit * kUnit;
     x.red = MODE == PRODUCT_WGRAD ? count : p.red;
-    x.blocks = (x.red + kBlockRed - 1) / kBlockRed;
+    x.blocks = (x.red + p.block_red - 1) / p.block_red;
     return x;
+}
+
+// The blocks [lo, hi) of a tile's reduction that this CTA sums.
+__device__ __forceinline__ void my_blocks(const ProductParams &p, const Tile &x, uint32_t rank, int &lo, int &hi) {
+    lo = 0, hi = x.blocks;
+    if (p.split > 1) {
+        lo = (int)((long long)x.blocks * rank / p.split);
+        hi = (int)((long long)x.blocks * (rank + 1) / p.split);
+    }
 }
 
 // Two output features (f, f + 1) of token column j or j + 1: lanes trade with
@@ -123,12 +153,6 @@ __device__ __forceinline__ uint32_t ld_pair(const __nv_bfloat16 *ptr) {
 __device__ __forceinline__ void st_pair(__nv_bfloat16 *ptr, uint32_t v) {
     *reinterpret_cast<uint32_t *>(ptr) = v;
 }
-__device__ __forceinline__ void st_out(const ProductParams &p, size_t at, float2 v) {
-    if (p.out_f32)
-        *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at) = v;
-    else
-        st_pair(static_cast<__nv_bfloat16 *>(p.out) + at, pack_bf16x2_rn(v.x, v.y));
-}
 
 // What the epilogue of one chunk reads from memory (residual, pre-activations or
 // the output added to), fetched before the accumulators are waited for.
@@ -137,7 +161,7 @@ struct Side {
 };
 
 // Where a lane's pairs of a chunk of 32 columns lie: its first feature, and the
-// column of its i-th pair (see trade_pair; a gated forward chunk has 8 pairs).
+// column of its i-th pair (see trade_pair; a gated forward chunk ends in 8 pairs).
 template <int MODE, bool GATED>
 struct Place {
     int f;
@@ -160,11 +184,12 @@ struct Place {
 };
 
 template <int MODE, bool GATED>
-__device__ __forceinline__ void load_side(const ProductParams &p, size_t row0, int n,
-                                          const Place<MODE, GATED> &at, Side &side) {
+__device__ __forceinline__ void load_side(const ProductParams &p, size_t row0, int n, const Place<MODE, GATED> &at,
+                                          Side &side) {
     constexpr int kPairs = MODE == PRODUCT_FORWARD && GATED ? 8 : 16;
     const bool want = MODE == PRODUCT_FORWARD ? p.residual != nullptr
-                                              : MODE == PRODUCT_DGRAD ? GATED || p.act != EP_ACT_NONE : p.accumulate;
+                      : MODE == PRODUCT_DGRAD ? GATED || p.act != EP_ACT_NONE
+                                              : p.accumulate;
     if (!want || !at.ok) return;
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
@@ -186,101 +211,143 @@ __device__ __forceinline__ void load_side(const ProductParams &p, size_t row0, i
     }
 }
 
+template <int ACT, int N>
+__device__ __forceinline__ void act_pairs(float2 (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float2(act_value(v[i].x, ACT), act_value(v[i].y, ACT));
+}
+template <int ACT, int N>
+__device__ __forceinline__ void slope_pairs(float2 (&v)[N], const uint32_t (&z)[16]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float2 s = unpack_bf16x2(z[i]);
+        v[i].x *= act_slope(s.x, ACT), v[i].y *= act_slope(s.y, ACT);
+    }
+}
+
+// Pairs i of v to output rows row0 + column(i), `wide` elements apart, at `off`.
+template <int MODE, bool GATED, int N>
+__device__ __forceinline__ void store_pairs(const ProductParams &p, const float2 (&v)[N], size_t row0, int n,
+                                            const Place<MODE, GATED> &at, size_t wide, size_t off) {
+    if (!at.ok) return;
+    if (p.out_f32) {
+        float *o = static_cast<float *>(p.out) + row0 * wide + off;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (at.column(i) < n) *reinterpret_cast<float2 *>(o + at.column(i) * wide) = v[i];
+    } else {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + row0 * wide + off;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (at.column(i) < n) st_pair(o + at.column(i) * wide, pack_bf16x2_rn(v[i].x, v[i].y));
+    }
+}
+
 // The epilogue of 32 accumulator columns of one warp's 32 lanes, of which n are
-// output rows row0 .. row0 + n - 1.
+// output rows row0 .. row0 + n - 1. Straight-line over the 16 pairs, so that
+// their arithmetic and stores overlap.
 template <int MODE, bool GATED>
-__device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const float (&acc)[32], size_t row0,
-                                               int n, const Place<MODE, GATED> &at, float2 bias,
-                                               const Side &side) {
+__device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const float (&acc)[32], size_t row0, int n,
+                                               const Place<MODE, GATED> &at, float2 bias, const Side &side) {
+    const size_t L = (size_t)p.lanes;
+    float2 v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = trade_pair(acc[2 * i], acc[2 * i + 1], at.odd);
+    if constexpr (MODE == PRODUCT_FORWARD) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i].x += bias.x, v[i].y += bias.y;
+        if (p.preact && at.ok) {
+            const size_t wide = GATED ? 2 * L : L;
+            __nv_bfloat16 *z = p.preact + row0 * wide + (GATED && at.up ? L : 0) + at.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (2 * i + at.odd < n) st_pair(z + (2 * i + at.odd) * wide, pack_bf16x2_rn(v[i].x, v[i].y));
+        }
+    }
     if constexpr (MODE == PRODUCT_FORWARD && GATED) {
+        float2 y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (4 * i >= n) break;
-            float2 a = trade_pair(acc[4 * i], acc[4 * i + 1], at.odd);
-            float2 b = trade_pair(acc[4 * i + 2], acc[4 * i + 3], at.odd);
-            a.x += bias.x, a.y += bias.y, b.x += bias.x, b.y += bias.y;
-            if (p.preact && at.ok) {
-                const int ja = 4 * i + at.odd, jb = ja + 2;
-                __nv_bfloat16 *z = p.preact + (at.up ? p.lanes : 0) + at.f;
-                if (ja < n) st_pair(z + (row0 + ja) * 2 * p.lanes, pack_bf16x2_rn(a.x, a.y));
-                if (jb < n) st_pair(z + (row0 + jb) * 2 * p.lanes, pack_bf16x2_rn(b.x, b.y));
-            }
-            // gate lanes give their second token's pair for the up pair of the first
-            const float2 give = at.up ? a : b;
+            // of two pairs, gate lanes give their second for the up pair of the first
+            const float2 a = v[2 * i], b = v[2 * i + 1], give = at.up ? a : b;
             float2 got;
             got.x = __shfl_xor_sync(0xFFFFFFFFu, give.x, p.interleave);
             got.y = __shfl_xor_sync(0xFFFFFFFFu, give.y, p.interleave);
             const float2 gate = at.up ? got : a, up = at.up ? b : got;
-            const int j = at.column(i);
-            if (at.ok && j < n) {
-                float2 y = make_float2(act_value(gate.x, EP_ACT_SILU) * up.x,
-                                       act_value(gate.y, EP_ACT_SILU) * up.y);
-                if (p.residual) {
-                    const float2 r = unpack_bf16x2(side.a[i]);
-                    y.x += r.x, y.y += r.y;
-                }
-                st_out(p, (row0 + j) * p.lanes + at.f, y);
+            y[i] = make_float2(act_value(gate.x, EP_ACT_SILU) * up.x, act_value(gate.y, EP_ACT_SILU) * up.y);
+        }
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 r = unpack_bf16x2(side.a[i]);
+                y[i].x += r.x, y[i].y += r.y;
             }
         }
-    } else {
+        store_pairs(p, y, row0, n, at, L, at.f);
+    } else if constexpr (MODE == PRODUCT_DGRAD && GATED) {
+        float2 d[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            if (2 * i >= n) break;
-            float2 v = trade_pair(acc[2 * i], acc[2 * i + 1], at.odd);
-            const int j = at.column(i);
-            if (!at.ok || j >= n) continue;
-            if (MODE == PRODUCT_DGRAD && GATED) {
-                const float2 zg = unpack_bf16x2(side.a[i]), zu = unpack_bf16x2(side.b[i]);
-                const size_t o = (row0 + j) * 2 * p.lanes + at.f;
-                st_out(p, o, make_float2(v.x * zu.x * act_slope(zg.x, EP_ACT_SILU),
-                                         v.y * zu.y * act_slope(zg.y, EP_ACT_SILU)));
-                st_out(p, o + p.lanes, make_float2(v.x * act_value(zg.x, EP_ACT_SILU),
-                                                   v.y * act_value(zg.y, EP_ACT_SILU)));
-                continue;
-            }
-            const size_t o = (row0 + j) * p.lanes + at.f;
-            if (MODE == PRODUCT_FORWARD) {
-                v.x += bias.x, v.y += bias.y;
-                if (p.preact) st_pair(p.preact + o, pack_bf16x2_rn(v.x, v.y));
-                v = make_float2(act_value(v.x, p.act), act_value(v.y, p.act));
-                if (p.residual) {
-                    const float2 r = unpack_bf16x2(side.a[i]);
-                    v.x += r.x, v.y += r.y;
-                }
-            } else if (MODE == PRODUCT_DGRAD) {
-                if (p.act != EP_ACT_NONE) {
-                    const float2 z = unpack_bf16x2(side.a[i]);
-                    v.x *= act_slope(z.x, p.act), v.y *= act_slope(z.y, p.act);
-                }
-            } else if (p.accumulate) {
-                const float2 was = p.out_f32 ? make_float2(__uint_as_float(side.a[i]), __uint_as_float(side.b[i]))
-                                             : unpack_bf16x2(side.a[i]);
-                v.x += was.x, v.y += was.y;
-            }
-            st_out(p, o, v);
+            const float2 g = unpack_bf16x2(side.a[i]), u = unpack_bf16x2(side.b[i]);
+            d[i] = make_float2(v[i].x * u.x * act_slope(g.x, EP_ACT_SILU), v[i].y * u.y * act_slope(g.y, EP_ACT_SILU));
+            v[i].x *= act_value(g.x, EP_ACT_SILU), v[i].y *= act_value(g.y, EP_ACT_SILU);
         }
+        store_pairs(p, d, row0, n, at, 2 * L, at.f);
+        store_pairs(p, v, row0, n, at, 2 * L, L + at.f);
+    } else {
+        if (MODE == PRODUCT_FORWARD) {
+            switch (p.act) {
+                case EP_ACT_RELU: act_pairs<EP_ACT_RELU>(v); break;
+                case EP_ACT_SILU: act_pairs<EP_ACT_SILU>(v); break;
+                case EP_ACT_GELU: act_pairs<EP_ACT_GELU>(v); break;
+                case EP_ACT_GELU_TANH: act_pairs<EP_ACT_GELU_TANH>(v); break;
+                default: break;
+            }
+        } else if (MODE == PRODUCT_DGRAD) {
+            switch (p.act) {
+                case EP_ACT_RELU: slope_pairs<EP_ACT_RELU>(v, side.a); break;
+                case EP_ACT_SILU: slope_pairs<EP_ACT_SILU>(v, side.a); break;
+                case EP_ACT_GELU: slope_pairs<EP_ACT_GELU>(v, side.a); break;
+                case EP_ACT_GELU_TANH: slope_pairs<EP_ACT_GELU_TANH>(v, side.a); break;
+                default: break;
+            }
+        }
+        if ((MODE == PRODUCT_FORWARD && p.residual) || (MODE == PRODUCT_WGRAD && p.accumulate)) {
+            const bool wide = MODE == PRODUCT_WGRAD && p.out_f32;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float2 r = wide ? make_float2(__uint_as_float(side.a[i]), __uint_as_float(side.b[i]))
+                                      : unpack_bf16x2(side.a[i]);
+                v[i].x += r.x, v[i].y += r.y;
+            }
+        }
+        store_pairs(p, v, row0, n, at, L, at.f);
     }
 }
 
-template <int MODE, bool GATED>
+template <int MODE, bool GATED, int CG>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductParams p) {
     constexpr bool kMnA = MODE != PRODUCT_FORWARD, kMnB = MODE == PRODUCT_WGRAD;
     extern __shared__ uint8_t raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    Shared *sh = reinterpret_cast<Shared *>(stages + (size_t)kStages * kStageBytes);
+    Shared *sh = reinterpret_cast<Shared *>(stages + kStageSpace / 1024 * 1024);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const bool clustered = CG == 2 || p.split > 1;
+    const uint32_t rank = clustered ? cluster_rank() : 0;
+    const int per_cluster = CG == 2 ? 2 : p.split;
+    const int t0 = blockIdx.x / per_cluster, t_step = gridDim.x / per_cluster;
 
     for (int g = threadIdx.x; g < p.groups; g += kThreads)
         sh->count[g] = p.counts ? max(0, min(p.counts[g], p.rows)) : p.rows;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sh->full[s], 1);
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&sh->full[s], 2 * CG);   // an arrival per operand and CTA
             mbar_init(&sh->empty[s], 1);
-            mbar_init(&sh->tail[s], 1);
+            mbar_init(&sh->tail[s], 2);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh->acc_full[a], 1);
-            mbar_init(&sh->acc_empty[a], 4);
+            mbar_init(&sh->acc_empty[a], kEpilogueWarps * CG);
         }
         mbar_init(&sh->drain, 1);
         sh->abort = 0;
@@ -288,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         tma_prefetch_map(&p.a);
         tma_prefetch_map(&p.b[0]);
     }
-    if (warp == 3) tmem_alloc(&sh->tmem, kTmemCols);
+    if (warp == 3) tmem_alloc<CG>(&sh->tmem, kTmemCols);
     __syncthreads();
     if (warp == 0) {   // exclusive prefix of the groups' column tiles
         int base = 0;
@@ -307,91 +374,128 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();   // both CTAs' barriers are ready before either signals the other's
     tc_fence_after();
     const int total = sh->first[p.groups] * p.lane_tiles;
     const uint32_t tmem = sh->tmem;
 
-    uint32_t it = 0;       // reduction blocks so far: stage it % kStages, phase (it / kStages) & 1
-    uint32_t n_acc = 0;    // accumulators so far
+    Ring ring;
+    uint32_t n_acc = 0;                     // accumulators so far
+    int issued = 0;                         // producer: blocks so far
     uint32_t on_tail = 0, tail_phase = 0;   // producer, a bit per stage: last load signals tail[], and its phase
-    if (warp == 0) {
-        // ---- TMA: both operands of every block into the next free stage
-        if (lane == 0) {
-            bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                const Tile x = find_tile<MODE, GATED>(p, sh, t);
-                for (int kb = 0; kb < x.blocks; ++kb, ++it) {
-                    const int s = it % kStages;
-                    ok = role_wait(&sh->empty[s], ((it / kStages) & 1) ^ 1, sh, p);
-                    if (!ok) break;
-                    uint8_t *sa = stages + (size_t)s * kStageBytes, *sb = sa + kABytes;
-                    const int r0 = kb * kBlockRed;
-                    const int chunks = (x.n_mma + 63) / 64;
-                    const uint32_t bytes = kABytes + (kMnB ? chunks * kChunkBytes : x.n_mma * 128);
-                    // a weight gradient's block that ends past the count goes through the
-                    // zeroing warp before the MMA warp sees it
-                    const bool tail = kMnB && x.red - r0 < kBlockRed;
-                    uint64_t *bar = tail ? &sh->tail[s] : &sh->full[s];
-                    if (kMnB) {
-                        // phase bit of the next use: flipped by each use
-                        if (tail) tail_phase ^= 1u << s;
-                        on_tail = (on_tail & ~(1u << s)) | (tail ? 1u << s : 0u);
-                    }
-                    mbar_arrive_expect_tx(bar, bytes);
-                    if (MODE == PRODUCT_FORWARD) {
-                        if (GATED)
-                            tma_load_5d(sa, &p.a, r0, 0, 0, x.lane0 / p.interleave, x.g, bar);
-                        else
-                            tma_load_3d(sa, &p.a, r0, x.lane0, x.g, bar);
+    if (warp == 0 || warp == 3) {
+        // ---- TMA: this CTA's part of one operand (warp 0: lanes, warp 3: columns) of every
+        // block into the next free stage. One warp for both took as long to issue a block's
+        // loads as the tensor cores to use them.
+        const bool lanes = warp == 0;
+        bool ok = true;
+        for (int t = t0; t < total && ok; t += t_step) {
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank);
+            const int own_cols = x.n_mma / CG;
+            const int col0 = x.col0 + (CG == 2 ? (int)rank * own_cols : 0);
+            const int chunks = (own_cols + 63) / 64;
+            const uint32_t sub_bytes = lanes ? kABytes : kMnB ? chunks * kChunkBytes : own_cols * 128;
+            const int lane_block = x.lane0 / (GATED && MODE == PRODUCT_FORWARD ? p.interleave : 1);
+            int lo, hi;
+            my_blocks(p, x, rank, lo, hi);
+            for (int kb = lo; kb < hi; ++kb, ++issued, ring.next(p.stages)) {
+                const int s = ring.s;
+                ok = role_wait(&sh->empty[s], ring.phase ^ 1, sh, p);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const int r0 = kb * p.block_red, left = x.red - r0;
+                const int subs = min(p.subs, (left + kSubRed - 1) / kSubRed);
+                // a weight gradient's block that ends past the count goes through the
+                // zeroing warp before the MMA warp sees it
+                const bool tail = kMnB && left < p.block_red && left % kSubRed != 0;
+                if (kMnB) {
+                    if (tail) tail_phase ^= 1u << s;   // phase of the stage's next tail
+                    on_tail = (on_tail & ~(1u << s)) | (tail ? 1u << s : 0u);
+                }
+                if (elect_one()) {
+                    uint64_t *local = tail ? &sh->tail[s] : &sh->full[s];
+                    uint32_t bar;
+                    if (CG == 2 && !tail) {
+                        bar = map_rank(local, 0);
+                        mbar_arrive_expect_tx_cluster(bar, sub_bytes * subs);
                     } else {
-                        tma_load_3d(sa, &p.a, x.lane0, r0, x.g, bar);
-                        tma_load_3d(sa + kChunkBytes, &p.a, x.lane0 + 64, r0, x.g, bar);
+                        bar = smem_u32(local);
+                        mbar_arrive_expect_tx(local, sub_bytes * subs);
                     }
-                    if (kMnB) {
-                        for (int c = 0; c < chunks; ++c)
-                            tma_load_3d(sb + c * kChunkBytes, &p.b[0], x.col0 + 64 * c, r0, x.g, bar);
-                    } else {
-                        int done = 0;
-                        for (int b = 0; b < kBoxes; ++b)
-                            for (const int box = 128 >> b; x.n_mma - done >= box; done += box)
-                                tma_load_3d(sb + done * 128, &p.b[b], r0, x.col0 + done, x.g, bar);
+                    uint8_t *dst = stages + (size_t)s * p.stage_bytes + (lanes ? 0 : kABytes);
+                    for (int sub = 0; sub < subs; ++sub, dst += p.sub_bytes) {
+                        const int r = r0 + sub * kSubRed;
+                        if (lanes) {
+                            if (MODE == PRODUCT_FORWARD) {
+                                if (GATED)
+                                    tma_load_5d<CG>(dst, &p.a, r, 0, 0, lane_block, x.g, bar);
+                                else
+                                    tma_load_3d<CG>(dst, &p.a, r, lane_block, x.g, bar);
+                            } else {
+                                tma_load_3d<CG>(dst, &p.a, x.lane0, r, x.g, bar);
+                                tma_load_3d<CG>(dst + kChunkBytes, &p.a, x.lane0 + 64, r, x.g, bar);
+                            }
+                        } else if (kMnB) {
+                            for (int c = 0; c < chunks; ++c)
+                                tma_load_3d<CG>(dst + c * kChunkBytes, &p.b[0], col0 + 64 * c, r, x.g, bar);
+                        } else {
+                            int done = own_cols & ~127;
+                            if (done) tma_load_3d<CG>(dst, &p.b[0], r, col0, x.g, bar);
+                            if (done > 128) tma_load_3d<CG>(dst + 128 * 128, &p.b[0], r, col0 + 128, x.g, bar);
+                            if (done < own_cols) {
+#pragma unroll
+                                for (int b = 1; b < kBoxes; ++b)
+                                    if (own_cols & (128 >> b)) {
+                                        tma_load_3d<CG>(dst + done * 128, &p.b[b], r, col0 + done, x.g, bar);
+                                        done += 128 >> b;
+                                    }
+                            }
+                        }
                     }
                 }
+                __syncwarp();
             }
         }
-    } else if (warp == 1) {
-        // ---- MMA: one thread issues four steps of 16 per block
+    } else if (warp == 1 && (CG == 1 || rank == 0)) {
+        // ---- MMA: one thread issues the steps of 16 of each block
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const Tile x = find_tile<MODE, GATED>(p, sh, t);
-            if (x.blocks == 0) continue;
+        for (int t = t0; t < total && ok; t += t_step) {
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank);
+            int lo, hi;
+            my_blocks(p, x, rank, lo, hi);
+            if (lo == hi) continue;
             const int a = n_acc & 1;
             ok = role_wait(&sh->acc_empty[a], ((n_acc / 2) & 1) ^ 1, sh, p);
+            ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t idesc = mma_idesc(kLanes, x.n_mma, kMnA, kMnB);
+            const uint32_t idesc = mma_idesc(kLanes * CG, x.n_mma, kMnA, kMnB);
             const uint32_t d = tmem + a * kColMax;
-            for (int kb = 0; kb < x.blocks; ++kb, ++it) {
-                const int s = it % kStages;
-                ok = role_wait(&sh->full[s], (it / kStages) & 1, sh, p);
+            for (int kb = lo; kb < hi; ++kb, ring.next(p.stages)) {
+                const int s = ring.s;
+                ok = role_wait(&sh->full[s], ring.phase, sh, p);
+                ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t sa = smem_u32(stages + (size_t)s * kStageBytes), sb = sa + kABytes;
-                    const int steps = min(4, (x.red - kb * kBlockRed + 15) / 16);
-                    for (int i = 0; i < steps; ++i) {
-                        const uint64_t da = kMnA ? smem_desc(sa + i * 2048, kChunkBytes, 1024)
-                                                 : smem_desc(sa + i * 32, 16, 1024);
-                        const uint64_t db = kMnB ? smem_desc(sb + i * 2048, kChunkBytes, 1024)
-                                                 : smem_desc(sb + i * 32, 16, 1024);
-                        mma_bf16(d, da, db, idesc, kb > 0 || i > 0);
+                if (elect_one()) {
+                    uint32_t sa = smem_u32(stages + (size_t)s * p.stage_bytes);
+                    int left = x.red - kb * p.block_red;
+                    for (int sub = 0; sub < p.subs && left > 0; ++sub, sa += p.sub_bytes, left -= kSubRed) {
+                        const uint64_t da = kMnA ? smem_desc(sa, kChunkBytes, 1024) : smem_desc(sa, 16, 1024);
+                        const uint64_t db = kMnB ? smem_desc(sa + kABytes, kChunkBytes, 1024)
+                                                 : smem_desc(sa + kABytes, 16, 1024);
+                        constexpr uint32_t kStepA = (kMnA ? 2048 : 32) / 16, kStepB = (kMnB ? 2048 : 32) / 16;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (left > 16 * i)
+                                mma_bf16<CG>(d, da + kStepA * i, db + kStepB * i, idesc, kb > lo || sub > 0 || i > 0);
                     }
-                    mma_commit(&sh->empty[s]);
+                    mma_commit<CG>(&sh->empty[s]);
                 }
                 __syncwarp();
             }
             if (!ok) break;
-            if (lane == 0) mma_commit(&sh->acc_full[a]);
+            if (elect_one()) mma_commit<CG>(&sh->acc_full[a]);
             __syncwarp();
             ++n_acc;
         }
@@ -399,35 +503,47 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         // ---- rows at or past the count, in the last block: zero in both operands
         uint32_t used = 0;   // a bit per stage: parity of its next use here
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const Tile x = find_tile<MODE, GATED>(p, sh, t);
-            it += x.blocks;
-            const int left = x.red % kBlockRed;
-            if (left == 0) continue;
-            const int s = (it - 1) % kStages;
-            ok = role_wait(&sh->tail[s], (used >> s) & 1, sh, p);
-            used ^= 1u << s;
-            if (!ok) break;
-            // rows up to the MMA's last step of 16
-            const int rows = ((left + 15) & ~15) - left;
-            const int chunks = 2 + (x.n_mma + 63) / 64;
-            uint8_t *sa = stages + (size_t)s * kStageBytes;
-            for (int i = lane; i < rows * chunks * 8; i += 32) {
-                const int c = i / (rows * 8), r = i % (rows * 8) / 8, v = i % 8;
-                *reinterpret_cast<uint4 *>(sa + c * kChunkBytes + (left + r) * 128 + v * 16) =
-                    make_uint4(0, 0, 0, 0);
+        for (int t = t0; t < total && ok; t += t_step) {
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank);
+            int lo, hi;
+            my_blocks(p, x, rank, lo, hi);
+            const int left = x.red % kSubRed;
+            for (int kb = lo; kb < hi; ++kb, ring.next(p.stages)) {
+                if (left == 0 || kb + 1 < x.blocks) continue;
+                const int s = ring.s;
+                ok = role_wait(&sh->tail[s], (used >> s) & 1, sh, p);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                used ^= 1u << s;
+                if (!ok) break;
+                // rows up to the MMA's last step of 16
+                const int rows = ((left + 15) & ~15) - left;
+                const int chunks = 2 + (x.n_mma / CG + 63) / 64;
+                const int sub = (x.red - kb * p.block_red) / kSubRed;
+                uint8_t *sa = stages + (size_t)s * p.stage_bytes + sub * p.sub_bytes;
+                for (int i = lane; i < rows * chunks * 8; i += 32) {
+                    const int c = i / (rows * 8), r = i % (rows * 8) / 8, v = i % 8;
+                    *reinterpret_cast<uint4 *>(sa + c * kChunkBytes + (left + r) * 128 + v * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_async();
+                __syncwarp();
+                if (lane < 2) {   // for both operands' loads
+                    if (CG == 2)
+                        mbar_arrive_cluster(map_rank(&sh->full[s], 0));
+                    else
+                        mbar_arrive(&sh->full[s]);
+                }
             }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->full[s]);
         }
     } else if (warp >= 4) {
-        // ---- epilogue: this warp's 32 lanes of every accumulator
-        const int quad = warp - 4;
+        // ---- epilogue: 32 lanes and every other 32 columns of each accumulator
+        const int quad = warp % 4, half = (warp - 4) / 4;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const Tile x = find_tile<MODE, GATED>(p, sh, t);
-            if (x.blocks == 0 && MODE == PRODUCT_WGRAD && p.accumulate) continue;
+        for (int t = t0; t < total && ok; t += t_step) {
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank);
+            int lo, hi;
+            my_blocks(p, x, rank, lo, hi);
+            if (p.split == 1 && lo == hi && MODE == PRODUCT_WGRAD && p.accumulate) continue;
             const Place<MODE, GATED> at(p, x, quad, lane);
             const size_t row0 = (size_t)x.g * (MODE == PRODUCT_WGRAD ? p.cols : p.rows) + x.col0;
             float2 bias = make_float2(0.f, 0.f);
@@ -435,18 +551,18 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 bias = unpack_bf16x2(ld_pair(p.bias + (size_t)x.g * (GATED ? 2 : 1) * p.lanes +
                                              (at.up ? p.lanes : 0) + at.f));
             const int a = n_acc & 1;
-            if (x.blocks > 0) {
+            Side side;
+            if (p.split == 1 && half * 32 < x.cols)
+                load_side(p, row0 + half * 32, min(32, x.cols - half * 32), at, side);
+            if (lo < hi) {
                 ok = role_wait(&sh->acc_full[a], (n_acc / 2) & 1, sh, p);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
             }
-            for (int c = 0; c < x.cols; c += 32) {
+            for (int c = half * 32; c < x.cols; c += 64) {
                 float acc[32];
-                Side side;
-                const int n = min(32, x.cols - c);
-                load_side(p, row0 + c, n, at, side);
-                if (x.blocks > 0) {
+                if (lo < hi) {
                     uint32_t r[32];
                     tmem_ld32(tmem + a * kColMax + c + ((uint32_t)(quad * 32) << 16), r);
                     tmem_ld_wait();
@@ -456,12 +572,25 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
                     for (int j = 0; j < 32; ++j) acc[j] = 0.f;
                 }
-                epilogue_chunk(p, acc, row0 + c, n, at, bias, side);
+                if (p.split > 1) {   // to shared memory, [column][lane]; joined below
+                    float *part = reinterpret_cast<float *>(stages) + quad * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j < x.cols) part[(c + j) * kLanes] = acc[j];
+                } else {
+                    epilogue_chunk(p, acc, row0 + c, min(32, x.cols - c), at, bias, side);
+                    if (c + 64 < x.cols) load_side(p, row0 + c + 64, min(32, x.cols - c - 64), at, side);
+                }
             }
-            if (x.blocks > 0) {
+            if (lo < hi) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->acc_empty[a]);
+                if (lane == 0) {
+                    if (CG == 2)
+                        mbar_arrive_cluster(map_rank(&sh->acc_empty[a], 0));
+                    else
+                        mbar_arrive(&sh->acc_empty[a]);
+                }
                 ++n_acc;
             }
         }
@@ -471,24 +600,61 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         // a wait ran out: let the copies and MMAs in flight finish (bounded) before
         // shared and tensor memory are given up
         const uint64_t t0 = global_ns();
-        if (threadIdx.x == 0) {
-            for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
-                const int s = i % kStages;
-                uint64_t *bar = (on_tail >> s) & 1 ? &sh->tail[s] : &sh->full[s];
-                const uint32_t phase = (on_tail >> s) & 1 ? ((tail_phase >> s) & 1) ^ 1 : (i / kStages) & 1;
-                while (!mbar_try_wait(bar, phase) && global_ns() - t0 < 100000000ull)
+        if (threadIdx.x == 0 && (CG == 1 || rank == 0)) {
+            for (int i = max(0, issued - p.stages); i < issued; ++i) {
+                const int s = i % p.stages;
+                const bool tail = (on_tail >> s) & 1;
+                const uint32_t phase = tail ? ((tail_phase >> s) & 1) ^ 1 : (uint32_t)(i / p.stages) & 1;
+                while (!mbar_try_wait(tail ? &sh->tail[s] : &sh->full[s], phase) &&
+                       global_ns() - t0 < 100000000ull)
                     ;
             }
-        } else if (threadIdx.x == 32) {
-            mma_commit(&sh->drain);
+        } else if (threadIdx.x == 32 && (CG == 1 || rank == 0)) {
+            mma_commit<CG>(&sh->drain);
             while (!mbar_try_wait(&sh->drain, 0) && global_ns() - t0 < 100000000ull)
                 ;
         }
+        while (global_ns() - t0 < 1000000ull)   // the other CTA's copies, which it cannot see end
+            ;
     }
     tc_fence_before();
     __syncthreads();
+    if (CG == 1 && p.split > 1) {
+        // ---- the split tile: every CTA has its partial sums in shared memory; each adds up
+        // its share of the columns, in rank order, and finishes them
+        cluster_sync();
+        if (t0 < total && warp >= 4) {
+            const int quad = warp % 4, half = (warp - 4) / 4;
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t0, rank);
+            const Place<MODE, GATED> at(p, x, quad, lane);
+            const size_t row0 = (size_t)x.g * (MODE == PRODUCT_WGRAD ? p.cols : p.rows) + x.col0;
+            float2 bias = make_float2(0.f, 0.f);
+            if (MODE == PRODUCT_FORWARD && p.bias && at.ok)
+                bias = unpack_bf16x2(ld_pair(p.bias + (size_t)x.g * (GATED ? 2 : 1) * p.lanes +
+                                             (at.up ? p.lanes : 0) + at.f));
+            const int share = (x.cols + p.split - 1) / p.split;
+            const int c1 = min(x.cols, ((int)rank + 1) * share);
+            for (int c = (int)rank * share + half * 32; c < c1; c += 64) {
+                const int n = min(32, c1 - c);
+                Side side;
+                load_side(p, row0 + c, n, at, side);
+                float acc[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+                for (int i = 0; i < p.split; ++i) {
+                    const uint32_t part = map_rank(reinterpret_cast<float *>(stages) + quad * 32 + lane, i);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < n) acc[j] += ld_cluster_f32(part + (uint32_t)(c + j) * kLanes * 4);
+                }
+                epilogue_chunk(p, acc, row0 + c, n, at, bias, side);
+            }
+        }
+        cluster_sync();   // no CTA leaves while another reads its shared memory
+    }
+    if (CG == 2) cluster_sync();
     tc_fence_after();
-    if (warp == 3) tmem_free(tmem, kTmemCols);
+    if (warp == 3) tmem_free<CG>(tmem, kTmemCols);
 }
 
 // ------------------------------------------------------------------ host side
@@ -554,31 +720,67 @@ cudaError_t sm_count(int *out) {
     return e;
 }
 
-template <int MODE, bool GATED>
-int launch(const ProductParams &p, int grid, cudaStream_t st) {
-    const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, GATED>);
-    if (ensure_dyn_smem(fn, kSmemBytes) != cudaSuccess) return EP_ERR_CUDA;
-    product_kernel<MODE, GATED><<<grid, kThreads, kSmemBytes, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+template <int MODE, bool GATED, int CG>
+int launch(const ProductParams &p, int clusters, cudaStream_t st) {
+    const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, GATED, CG>);
+    if (ensure_dyn_smem(fn, kSmemMax) != cudaSuccess) return EP_ERR_CUDA;
+    const int size = CG == 2 ? 2 : p.split;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * size));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemMax;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, product_kernel<MODE, GATED, CG>, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 
 template <int MODE>
 int launch(ProductParams &p, cudaStream_t st) {
     const bool gated = p.act == EP_ACT_SWIGLU;
     const int per_tile = gated && MODE == PRODUCT_FORWARD ? kLanes / 2 : kLanes;
-    p.lane_tiles = (p.lanes + per_tile - 1) / per_tile;
-    p.col_max = kColMax;
-    p.wait_limit_ns = kWaitLimitNs;
     const long long cols = MODE == PRODUCT_WGRAD ? p.cols : p.rows;
-    const long long most = (long long)p.lane_tiles * p.groups * ((cols + p.col_max - 1) / p.col_max);
-    if (most >= (1LL << 31)) return EP_ERR_INVALID_ARG;
     int sms = 0;
     if (sm_count(&sms) != cudaSuccess) return EP_ERR_CUDA;
-    const int grid = (int)(most < sms ? most : sms);
-    if constexpr (MODE != PRODUCT_WGRAD) {
-        if (gated) return launch<MODE, true>(p, grid, st);
+    p.wait_limit_ns = kWaitLimitNs;
+    const int lane_tiles = (p.lanes + per_tile - 1) / per_tile;
+    auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };
+    // pairs of CTAs where they fill the GPU; otherwise single CTAs, which cut the work finer
+    p.col_max = kColMax;
+    const long long pairs = ceil_div(lane_tiles, 2) * p.groups * ceil_div(cols, kColMax);
+    const int cg = lane_tiles > 1 && 2 * pairs >= sms ? 2 : 1;
+    p.split = 1;
+    if (cg == 1 && !p.counts) {
+        // few tiles: narrower ones, then CTAs that share a tile's reduction
+        const long long blocks = ceil_div(MODE == PRODUCT_WGRAD ? p.rows : p.red, kSubRed);
+        while (p.col_max > 64 && 16 * (long long)lane_tiles * p.groups * ceil_div(cols, p.col_max) <= sms)
+            p.col_max /= 2;
+        const long long tiles = (long long)lane_tiles * p.groups * ceil_div(cols, p.col_max);
+        while (p.split < kMaxSplit && 2 * p.split * tiles <= sms && blocks >= 8 * p.split) p.split *= 2;
     }
-    return launch<MODE, false>(p, grid, st);
+    p.subs = cg;
+    p.block_red = p.subs * kSubRed;
+    p.lane_tiles = (int)ceil_div(lane_tiles, cg);
+    const int unit = 16 * cg;
+    const int widest = (int)(cols < p.col_max ? ceil_div(cols, unit) * unit : p.col_max);
+    p.sub_bytes = kABytes + (MODE == PRODUCT_WGRAD ? (widest / cg + 63) / 64 * kChunkBytes
+                                                   : (widest / cg * 128 + 1023) / 1024 * 1024);
+    p.stage_bytes = p.subs * p.sub_bytes;
+    p.stages = (int)(kStageSpace / 1024 * 1024 / p.stage_bytes);
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    const long long most = (long long)p.lane_tiles * p.groups * ceil_div(cols, p.col_max);
+    if (most >= (1LL << 31)) return EP_ERR_INVALID_ARG;
+    const long long room = p.split > 1 ? most : sms / cg;
+    const int clusters = (int)(most < room ? most : room);
+    if constexpr (MODE != PRODUCT_WGRAD) {
+        if (gated)
+            return cg == 2 ? launch<MODE, true, 2>(p, clusters, st) : launch<MODE, true, 1>(p, clusters, st);
+    }
+    return cg == 2 ? launch<MODE, false, 2>(p, clusters, st) : launch<MODE, false, 1>(p, clusters, st);
 }
 
 bool aligned16(const void *q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
@@ -660,7 +862,7 @@ extern "C" int ep_product_dgrad(const ep_product_t *a, const void *dy, const voi
     p.z = static_cast<const __nv_bfloat16 *>(preact);
     p.out = dx;
     const uint64_t K = a->k, N = a->n, G = a->groups;
-    bool ok = make_map3(&p.a, w, K, N, G, kBlockRed);
+    bool ok = make_map3(&p.a, w, K, N, G, kSubRed);
     for (int b = 0; b < kBoxes && ok; ++b) ok = make_map3(&p.b[b], dy, N, a->rows, G, 128u >> b);
     if (!ok) return EP_ERR_CUDA;
     Range range("ep:product_dgrad");
@@ -687,7 +889,7 @@ extern "C" int ep_product_wgrad(const ep_product_t *a, const void *dy, const voi
     p.cols = a->n;
     p.accumulate = accumulate;
     p.out = dw;
-    if (!make_map3(&p.a, x, K, a->rows, G, kBlockRed) || !make_map3(&p.b[0], dy, N, a->rows, G, kBlockRed))
+    if (!make_map3(&p.a, x, K, a->rows, G, kSubRed) || !make_map3(&p.b[0], dy, N, a->rows, G, kSubRed))
         return EP_ERR_CUDA;
     const int rc = launch<PRODUCT_WGRAD>(p, st);
     if (rc != EP_OK || !dbias) return rc;

@@ -24,6 +24,10 @@ struct ProductParams {
     int cols;                 // wgrad: n
     int red;                  // forward: k, dgrad: n (wgrad: the group's rows in use)
     int lane_tiles, col_max;  // lane tiles per group; widest column tile
+    int stages, stage_bytes;  // ring of operand blocks in shared memory,
+    int subs, sub_bytes;      // each of this many sub-blocks of 64 reduction elements
+    int block_red;            // subs * 64
+    int split;                // CTAs of a cluster that share one tile's reduction (1 = none)
     int act, interleave;      // gated forward: 8 or 16 gate rows, then as many up rows
     int out_f32, accumulate;
     const __nv_bfloat16 *bias, *residual;

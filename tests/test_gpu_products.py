@@ -72,6 +72,49 @@ def test_experts_forward_wide_tiles(act):
     check_forward(7, 600, 136, 144, act, [255, 256, 257, 300, 513, 600, 0])
 
 
+# enough tiles for pairs of CTAs to share each (two lane tiles, more than the GPU's pairs in all)
+PAIRED = [0, 1, 15, 16, 17, 31, 32, 33, 64, 100, 255, 256, 257, 300] * 3
+
+
+@pytest.mark.parametrize("act", ("none", "gelu", "swiglu"))
+@pytest.mark.parametrize("k,n", [(136, 264), (72, 392)])
+def test_experts_forward_paired(act, k, n):
+    check_forward(len(PAIRED), 300, k, n, act, PAIRED, bias=True, residual=True, keep=True)
+
+
+@pytest.mark.parametrize("rows", [1, 7, 64, 130, 300])
+@pytest.mark.parametrize("k,n", [(4104, 136), (7168, 16), (1000, 3080)])
+def test_linear_long_reduction_few_tiles(rows, k, n):
+    """Few tiles: the CTAs of a cluster share a tile's reduction."""
+    g = gen(rows + k)
+    for act, dtype in (("none", F32), ("swiglu", BF16)):
+        wn = 2 * n if act == "swiglu" else n
+        x, w, b, r = normal(g, rows, k), normal(g, wn, k, std=k ** -0.5), normal(g, wn), normal(g, rows, n)
+        z = torch.empty(rows, wn, dtype=BF16, device="cuda")
+        got = ep.linear(x, w, bias=b, act=act, residual=r, out_dtype=dtype, preact=z)
+        y, ey, zz, ez = R.forward(x, w, b, act, r, dtype)
+        close(got, y, ey, act)
+        close(z, zz, ez, act)
+        dy, w2, zin = normal(g, rows, k), normal(g, k, n, std=k ** -0.5), normal(g, rows, 2 * n)
+        d, ed = R.dgrad(dy, w2, "swiglu", zin, dtype)
+        close(ep.linear_dgrad(dy, w2, act="swiglu", preact=zin, out_dtype=dtype), d, ed)
+
+
+@pytest.mark.parametrize("rows,k,n", [(4097, 72, 40), (2000, 264, 136), (3001, 1032, 2056), (700, 5000, 4104)])
+def test_linear_gradients_large(rows, k, n):
+    """Weight gradients split over the rows, and paired tiles."""
+    g = gen(rows)
+    dy, x, w, z = normal(g, rows, n), normal(g, rows, k), normal(g, n, k, std=n ** -0.5), normal(g, rows, k)
+    before = normal(g, n, k, dtype=F32), normal(g, n, dtype=F32)
+    dw, db = before[0].clone(), before[1].clone()
+    ep.linear_wgrad(dy, x, out=dw, bias_grad=db, accumulate=True)
+    w64, ew, b64, eb = R.wgrad(dy, x, F32, before)
+    close(dw, w64, ew)
+    close(db, b64, eb)
+    d, ed = R.dgrad(dy, w, "gelu", z, BF16)
+    close(ep.linear_dgrad(dy, w, act="gelu", preact=z), d, ed)
+
+
 def test_experts_forward_residual_and_f32():
     check_forward(3, 70, 96, 72, "silu", [70, 0, 33], bias=True, residual=True)
     check_forward(3, 70, 96, 72, "swiglu", [70, 0, 33], bias=True, residual=True)
@@ -169,6 +212,29 @@ def test_experts_dgrad(act, k, n):
         d, ed = R.dgrad(dy[e, :c], w[e], act, z[e, :c], BF16)
         close(out[e, :c], d, ed, f"expert {e}")
         assert (out[e, c:] == 7.0).all()
+
+
+@pytest.mark.parametrize("act", ("none", "silu", "swiglu"))
+def test_experts_gradients_paired(act):
+    g = gen(21)
+    E, rows, n, k, two = len(PAIRED), 300, 136, 264, 2 if act == "swiglu" else 1
+    dy, w, x = normal(g, E, rows, n), normal(g, E, n, k, std=n ** -0.5), normal(g, E, rows, k)
+    z = normal(g, E, rows, two * k)
+    for e, c in enumerate(PAIRED):
+        dy[e, c:] = float("nan")
+        z[e, c:] = float("nan")
+        x[e, c:] = float("-inf")
+    cnt = torch.tensor(PAIRED, dtype=torch.int32, device="cuda")
+    out = torch.full((E, rows, two * k), 7.0, dtype=BF16, device="cuda")
+    ep.experts_product_dgrad(dy, w, cnt, act=act, preact=None if act == "none" else z, out=out)
+    dw, db = ep.experts_product_wgrad(dy, x, cnt, out_dtype=F32, bias_grad=True)
+    for e, c in enumerate(PAIRED):
+        d, ed = R.dgrad(dy[e, :c], w[e], act, z[e, :c], BF16)
+        close(out[e, :c], d, ed, f"expert {e}")
+        assert (out[e, c:] == 7.0).all()
+        w64, ew, b64, eb = R.wgrad(dy[e, :c], x[e, :c], F32)
+        close(dw[e], w64, ew, f"expert {e}")
+        close(db[e], b64, eb, f"bias of expert {e}")
 
 
 @pytest.mark.parametrize("act", ("none", "gelu", "swiglu"))
