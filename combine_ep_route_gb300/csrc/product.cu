@@ -55,7 +55,7 @@ struct Shared {
 constexpr size_t kSmemMax = 227 * 1024;
 constexpr size_t kStageSpace = kSmemMax - 1024 - sizeof(Shared);
 // a split tile's partial sums take the place of the stages
-static_assert((size_t)kLanes * kColMax * 4 <= kStageSpace, "partial sums fit");
+static_assert((size_t)kLanes * kColMax * 4 + kEpilogueWarps * 4096 <= kStageSpace, "partial sums fit");
 
 // A position in the ring of stages: stage and phase parity.
 struct Ring {
@@ -97,36 +97,44 @@ __device__ __forceinline__ int col_tiles(const ProductParams &p, int count) {
     return (cols + p.col_max - 1) / p.col_max;
 }
 
+// a / b for 0 <= a, 0 < b: by reciprocal and correction where fp32 holds a exactly (an
+// integer division takes several times as long, and short tiles wait for it).
+__device__ __forceinline__ int quotient(int a, int b) {
+    if (a >= 1 << 22) return a / b;
+    int q = (int)__fdividef((float)a, (float)b);
+    const int r = a - q * b;
+    if (r < 0) --q;
+    if (r >= b) ++q;
+    return q;
+}
+
+// Tile t of the launch. Tiles are visited in rising order, so the group is found by
+// walking on from the last one's (g).
 template <int MODE, bool GATED, int CG>
-__device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *sh, int t, uint32_t rank) {
-    int lo = 0, hi = p.groups;       // first[lo] * lane_tiles <= t < first[hi] * lane_tiles
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sh->first[mid] * p.lane_tiles <= t)
-            lo = mid;
-        else
-            hi = mid;
-    }
+__device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *sh, int t, uint32_t rank, int &g) {
+    while (t >= sh->first[g + 1] * p.lane_tiles) ++g;
     Tile x;
-    x.g = lo;
-    const int r = t - sh->first[lo] * p.lane_tiles;
-    const int ct = sh->first[lo + 1] - sh->first[lo];
-    const int count = sh->count[lo];
+    x.g = g;
+    const int first = sh->first[g];
+    const int r = t - first * p.lane_tiles;
+    const int ct = sh->first[g + 1] - first;
+    const int count = sh->count[g];
     const int all = MODE == PRODUCT_WGRAD ? p.cols : count;
     // bands of kBand lane tiles, lane tiles innermost: the tiles in flight at a time form
     // a square rather than a strip, so each operand block is fetched by several of them
-    const int band = r / (kBand * ct), in_band = r - band * kBand * ct;
+    const int band = ct == 1 ? r / kBand : quotient(r, kBand * ct), in_band = r - band * kBand * ct;
     const int high = min(kBand, p.lane_tiles - band * kBand);
-    const int lt = band * kBand + in_band % high, c = in_band / high;
+    const int c = ct == 1 ? 0 : high == kBand ? in_band / kBand : quotient(in_band, high);
+    const int lt = band * kBand + in_band - c * high;
     constexpr int kUnit = 16 * CG;
     constexpr int kPer = GATED && MODE == PRODUCT_FORWARD ? kLanes / 2 : kLanes;
-    const int width = ((all + ct - 1) / ct + kUnit - 1) / kUnit * kUnit;
+    const int width = ((ct == 1 ? all : quotient(all + ct - 1, ct)) + kUnit - 1) / kUnit * kUnit;
     x.lane0 = (CG == 1 ? lt : lt * 2 + (int)rank) * kPer;
     x.col0 = c * width;
     x.cols = min(width, all - x.col0);
     x.n_mma = (x.cols + kUnit - 1) / kUnit * kUnit;
     x.red = MODE == PRODUCT_WGRAD ? count : p.red;
-    x.blocks = (x.red + p.block_red - 1) / p.block_red;
+    x.blocks = (x.red + p.block_red - 1) >> p.block_shift;
     return x;
 }
 
@@ -243,13 +251,68 @@ __device__ __forceinline__ void store_pairs(const ProductParams &p, const float2
     }
 }
 
+// Where a warp's 32 x 32 output tile is staged, and its place in the output.
+struct OutTile {
+    uint8_t *smem;
+    int lane, row, group;
+};
+
+// Full tiles leave through shared memory and a TMA store: as stores of each lane they
+// kept the epilogue warps waiting on the memory pipe, and with the short reductions of
+// a weight gradient the epilogue sets the pace (0.88 -> 0.68 ms on 32 experts of 4096 x
+// 7168 with 256 rows each, in fp32). Lanes past the last feature are cut by the map.
+template <int MODE, bool GATED>
+__device__ __forceinline__ void tile_pairs(const ProductParams &p, const float2 (&v)[16], const Place<MODE, GATED> &at,
+                                           const OutTile &tile, int half) {
+    if (elect_one()) bulk_wait_read<0>();   // the tile's last contents are on their way
+    __syncwarp();
+    const int pair = (threadIdx.x % 32) / 2;
+    if (p.out_f32) {
+        float2 *o = reinterpret_cast<float2 *>(tile.smem) + pair;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[(2 * i + at.odd) * 16] = v[i];
+    } else {
+        uint32_t *o = reinterpret_cast<uint32_t *>(tile.smem) + pair;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[(2 * i + at.odd) * 16] = pack_bf16x2_rn(v[i].x, v[i].y);
+    }
+    fence_async();
+    __syncwarp();
+    if (elect_one()) {
+        tma_store_4d(&p.o, tile.smem, tile.lane, half, tile.row, tile.group);
+        bulk_commit();
+    }
+}
+
+// The accumulators as they are, in fp32.
+__device__ __forceinline__ void tile_lanes(const ProductParams &p, const float (&acc)[32], const OutTile &tile) {
+    if (elect_one()) bulk_wait_read<0>();
+    __syncwarp();
+    float *o = reinterpret_cast<float *>(tile.smem) + threadIdx.x % 32;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) o[j * 32] = acc[j];
+    fence_async();
+    __syncwarp();
+    if (elect_one()) {
+        tma_store_4d(&p.o, tile.smem, tile.lane, 0, tile.row, tile.group);
+        bulk_commit();
+    }
+}
+
 // The epilogue of 32 accumulator columns of one warp's 32 lanes, of which n are
 // output rows row0 .. row0 + n - 1. Straight-line over the 16 pairs, so that
 // their arithmetic and stores overlap.
 template <int MODE, bool GATED>
 __device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const float (&acc)[32], size_t row0, int n,
-                                               const Place<MODE, GATED> &at, float2 bias, const Side &side) {
+                                               const Place<MODE, GATED> &at, float2 bias, const Side &side,
+                                               const OutTile &tile) {
     const size_t L = (size_t)p.lanes;
+    if constexpr (MODE == PRODUCT_WGRAD) {
+        if (n == 32 && p.out_f32 && !p.accumulate) {   // nothing to pair up: lanes side by side already
+            tile_lanes(p, acc, tile);
+            return;
+        }
+    }
     float2 v[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = trade_pair(acc[2 * i], acc[2 * i + 1], at.odd);
@@ -292,8 +355,13 @@ __device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const flo
             d[i] = make_float2(v[i].x * u.x * act_slope(g.x, EP_ACT_SILU), v[i].y * u.y * act_slope(g.y, EP_ACT_SILU));
             v[i].x *= act_value(g.x, EP_ACT_SILU), v[i].y *= act_value(g.y, EP_ACT_SILU);
         }
-        store_pairs(p, d, row0, n, at, 2 * L, at.f);
-        store_pairs(p, v, row0, n, at, 2 * L, L + at.f);
+        if (n == 32) {
+            tile_pairs(p, d, at, tile, 0);
+            tile_pairs(p, v, at, tile, 1);
+        } else {
+            store_pairs(p, d, row0, n, at, 2 * L, at.f);
+            store_pairs(p, v, row0, n, at, 2 * L, L + at.f);
+        }
     } else {
         if (MODE == PRODUCT_FORWARD) {
             switch (p.act) {
@@ -321,7 +389,10 @@ __device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const flo
                 v[i].x += r.x, v[i].y += r.y;
             }
         }
-        store_pairs(p, v, row0, n, at, L, at.f);
+        if (n == 32)
+            tile_pairs(p, v, at, tile, 0);
+        else
+            store_pairs(p, v, row0, n, at, L, at.f);
     }
 }
 
@@ -380,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const uint32_t tmem = sh->tmem;
 
     Ring ring;
+    int group = 0;                          // of the current tile
     uint32_t n_acc = 0;                     // accumulators so far
     int issued = 0;                         // producer: blocks so far
     uint32_t on_tail = 0, tail_phase = 0;   // producer, a bit per stage: last load signals tail[], and its phase
@@ -390,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const bool lanes = warp == 0;
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank);
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, group);
             const int own_cols = x.n_mma / CG;
             const int col0 = x.col0 + (CG == 2 ? (int)rank * own_cols : 0);
             const int chunks = (own_cols + 63) / 64;
@@ -460,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         // ---- MMA: one thread issues the steps of 16 of each block
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank);
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, group);
             int lo, hi;
             my_blocks(p, x, rank, lo, hi);
             if (lo == hi) continue;
@@ -504,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         uint32_t used = 0;   // a bit per stage: parity of its next use here
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank);
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, group);
             int lo, hi;
             my_blocks(p, x, rank, lo, hi);
             const int left = x.red % kSubRed;
@@ -538,9 +610,23 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     } else if (warp >= 4) {
         // ---- epilogue: 32 lanes and every other 32 columns of each accumulator
         const int quad = warp % 4, half = (warp - 4) / 4;
+        OutTile tile;
+        tile.smem = stages + p.out_at + (warp - 4) * (p.out_f32 ? 4096 : 2048);
+        // accumulator a may be overwritten: this warp's part is in registers (nothing in
+        // memory is handed over)
+        auto free_acc = [&](int a) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2)
+                    mbar_arrive_cluster_relaxed(map_rank(&sh->acc_empty[a], 0));
+                else
+                    mbar_arrive(&sh->acc_empty[a]);
+            }
+        };
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank);
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, group);
             int lo, hi;
             my_blocks(p, x, rank, lo, hi);
             if (p.split == 1 && lo == hi && MODE == PRODUCT_WGRAD && p.accumulate) continue;
@@ -550,6 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             if (MODE == PRODUCT_FORWARD && p.bias && at.ok)
                 bias = unpack_bf16x2(ld_pair(p.bias + (size_t)x.g * (GATED ? 2 : 1) * p.lanes +
                                              (at.up ? p.lanes : 0) + at.f));
+            tile.lane = x.lane0 + quad * 32, tile.group = x.g;
             const int a = n_acc & 1;
             Side side;
             if (p.split == 1 && half * 32 < x.cols)
@@ -568,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) acc[j] = __uint_as_float(r[j]);
+                    if (c + 64 >= x.cols) free_acc(a);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) acc[j] = 0.f;
@@ -578,22 +666,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     for (int j = 0; j < 32; ++j)
                         if (c + j < x.cols) part[(c + j) * kLanes] = acc[j];
                 } else {
-                    epilogue_chunk(p, acc, row0 + c, min(32, x.cols - c), at, bias, side);
+                    tile.row = x.col0 + c;
+                    epilogue_chunk(p, acc, row0 + c, min(32, x.cols - c), at, bias, side, tile);
                     if (c + 64 < x.cols) load_side(p, row0 + c + 64, min(32, x.cols - c - 64), at, side);
                 }
             }
             if (lo < hi) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (CG == 2)
-                        mbar_arrive_cluster(map_rank(&sh->acc_empty[a], 0));
-                    else
-                        mbar_arrive(&sh->acc_empty[a]);
-                }
+                if (half * 32 >= x.cols) free_acc(a);   // a warp with no columns here
                 ++n_acc;
             }
         }
+        if (elect_one()) bulk_wait_all();
     }
     __syncthreads();
     if (sh->abort && threadIdx.x < 64) {
@@ -625,13 +708,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         cluster_sync();
         if (t0 < total && warp >= 4) {
             const int quad = warp % 4, half = (warp - 4) / 4;
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t0, rank);
+            group = 0;
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t0, rank, group);
             const Place<MODE, GATED> at(p, x, quad, lane);
             const size_t row0 = (size_t)x.g * (MODE == PRODUCT_WGRAD ? p.cols : p.rows) + x.col0;
             float2 bias = make_float2(0.f, 0.f);
             if (MODE == PRODUCT_FORWARD && p.bias && at.ok)
                 bias = unpack_bf16x2(ld_pair(p.bias + (size_t)x.g * (GATED ? 2 : 1) * p.lanes +
                                              (at.up ? p.lanes : 0) + at.f));
+            OutTile tile;
+            tile.smem = stages + p.out_at + (warp - 4) * (p.out_f32 ? 4096 : 2048);
+            tile.lane = x.lane0 + quad * 32, tile.group = x.g;
             const int share = (x.cols + p.split - 1) / p.split;
             const int c1 = min(x.cols, ((int)rank + 1) * share);
             for (int c = (int)rank * share + half * 32; c < c1; c += 64) {
@@ -647,8 +734,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     for (int j = 0; j < 32; ++j)
                         if (j < n) acc[j] += ld_cluster_f32(part + (uint32_t)(c + j) * kLanes * 4);
                 }
-                epilogue_chunk(p, acc, row0 + c, n, at, bias, side);
+                tile.row = x.col0 + c;
+                epilogue_chunk(p, acc, row0 + c, n, at, bias, side, tile);
             }
+            if (elect_one()) bulk_wait_all();
         }
         cluster_sync();   // no CTA leaves while another reads its shared memory
     }
@@ -707,6 +796,20 @@ bool make_map3(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, u
     return make_map(m, base, 3, dims, strides, box);
 }
 
+// The output [groups][rows][halves][lanes], written in boxes of 32 lanes and 32 rows.
+bool make_out_map(CUtensorMap *m, void *out, bool f32, uint64_t halves, uint64_t lanes, uint64_t rows,
+                  uint64_t groups) {
+    EncodeTiled enc = encoder();
+    if (!enc) return false;
+    const uint64_t size = f32 ? 4 : 2;
+    const cuuint64_t dims[4] = {lanes, halves, rows, groups};
+    const cuuint64_t strides[3] = {lanes * size, lanes * halves * size, lanes * halves * rows * size};
+    const cuuint32_t box[4] = {32, 1, 32, 1}, one[4] = {1, 1, 1, 1};
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, out, dims, strides, box,
+               one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The multiprocessor count of the current device.
 cudaError_t sm_count(int *out) {
     constexpr int kMaxDevices = 64;
@@ -762,16 +865,21 @@ int launch(ProductParams &p, cudaStream_t st) {
         const long long tiles = (long long)lane_tiles * p.groups * ceil_div(cols, p.col_max);
         while (p.split < kMaxSplit && 2 * p.split * tiles <= sms && blocks >= 8 * p.split) p.split *= 2;
     }
-    p.subs = cg;
+    p.subs = cg == 2 && !p.out_f32 ? 2 : 1;
     p.block_red = p.subs * kSubRed;
+    p.block_shift = p.subs == 2 ? 7 : 6;
     p.lane_tiles = (int)ceil_div(lane_tiles, cg);
     const int unit = 16 * cg;
     const int widest = (int)(cols < p.col_max ? ceil_div(cols, unit) * unit : p.col_max);
     p.sub_bytes = kABytes + (MODE == PRODUCT_WGRAD ? (widest / cg + 63) / 64 * kChunkBytes
                                                    : (widest / cg * 128 + 1023) / 1024 * 1024);
     p.stage_bytes = p.subs * p.sub_bytes;
-    p.stages = (int)(kStageSpace / 1024 * 1024 / p.stage_bytes);
+    const int out_bytes = kEpilogueWarps * (p.out_f32 ? 4096 : 2048);
+    p.stages = (int)((kStageSpace / 1024 * 1024 - out_bytes) / p.stage_bytes);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
+    p.out_at = (int)(kStageSpace / 1024 * 1024) - out_bytes;
+    if (!make_out_map(&p.o, p.out, p.out_f32, MODE == PRODUCT_DGRAD && gated ? 2 : 1, p.lanes, cols, p.groups))
+        return EP_ERR_CUDA;
     const long long most = (long long)p.lane_tiles * p.groups * ceil_div(cols, p.col_max);
     if (most >= (1LL << 31)) return EP_ERR_INVALID_ARG;
     const long long room = p.split > 1 ? most : sms / cg;

@@ -18,6 +18,7 @@ constexpr int kBoxes = 4;   // token-row boxes of the column operand: 128, 64, 3
 struct ProductParams {
     CUtensorMap a;            // lane operand
     CUtensorMap b[kBoxes];    // column operand (wgrad: b[0] only)
+    CUtensorMap o;            // output as {lanes, halves, rows, groups}, boxes of 32 lanes x 32 rows
     const int32_t *counts;    // rows in use per group, or null (= rows)
     int groups, rows;
     int lanes;                // output features (gated forward: of the activation's output)
@@ -26,7 +27,8 @@ struct ProductParams {
     int lane_tiles, col_max;  // lane tiles per group; widest column tile
     int stages, stage_bytes;  // ring of operand blocks in shared memory,
     int subs, sub_bytes;      // each of this many sub-blocks of 64 reduction elements
-    int block_red;            // subs * 64
+    int block_red, block_shift;   // subs * 64, and its logarithm
+    int out_at;               // offset of the epilogue warps' output tiles, after the stages
     int split;                // CTAs of a cluster that share one tile's reduction (1 = none)
     int act, interleave;      // gated forward: 8 or 16 gate rows, then as many up rows
     int out_f32, accumulate;
