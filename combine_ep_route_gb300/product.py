@@ -8,6 +8,7 @@ Operands are contiguous bf16; ``k`` and ``n`` are multiples of 8.
 from __future__ import annotations
 
 import ctypes as C
+from math import prod
 from typing import Optional, Tuple, Union
 
 import torch
@@ -20,22 +21,38 @@ ACTS = {"none": L.EP_ACT_NONE, "relu": L.EP_ACT_RELU, "silu": L.EP_ACT_SILU, "ge
         "gelu_tanh": L.EP_ACT_GELU_TANH, "swiglu": L.EP_ACT_SWIGLU}
 _OUT = {BF16: L.EP_BF16, F32: L.EP_F32}
 
+# The current stream's handle without a Stream object: building one costs as much as
+# the rest of a small call. (device index) -> cudaStream_t
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def stream_of(stream: Optional[torch.cuda.Stream], dev: torch.device) -> int:
+    """ep._stream_ptr, by the short way for the current stream."""
+    if stream is None and _raw_stream is not None and dev.index == torch.cuda.current_device():
+        return _raw_stream(dev.index)
+    return _stream_ptr(stream, dev)
+
 
 def _act(act: str) -> int:
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"act: want one of {sorted(ACTS)}, got {act!r}")
-    return ACTS[act]
+    return code
 
 
 def _want(t: torch.Tensor, name: str, shape: Tuple[int, ...], dev, dtype=BF16) -> None:
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"{name}: want contiguous {dtype} {shape} on {dev}, got "
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
 
 
 def _operands(a: torch.Tensor, b: torch.Tensor, names: Tuple[str, str]) -> None:
+    dev = a.device
+    if (a.dtype == BF16 and b.dtype == BF16 and a.is_cuda and b.device == dev and a.is_contiguous()
+            and b.is_contiguous()):
+        return
     for t, name in ((a, names[0]), (b, names[1])):
-        if t.dtype != BF16 or not t.is_contiguous() or t.device.type != "cuda" or t.device != a.device:
+        if t.dtype != BF16 or not t.is_contiguous() or not t.is_cuda or t.device != dev:
             raise ValueError(f"{name}: want contiguous {BF16} on one CUDA device, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
 
@@ -43,8 +60,10 @@ def _operands(a: torch.Tensor, b: torch.Tensor, names: Tuple[str, str]) -> None:
 def _out(out: Optional[torch.Tensor], shape: Tuple[int, ...], dtype: Optional[torch.dtype], dev,
          name: str = "out") -> torch.Tensor:
     if out is None:
-        out = torch.empty(shape, dtype=dtype or BF16, device=dev)
-    elif dtype is not None and out.dtype != dtype:
+        if dtype is not None and dtype not in _OUT:
+            raise ValueError(f"{name}: want bfloat16 or float32, got {dtype}")
+        return torch.empty(shape, dtype=dtype or BF16, device=dev)
+    if dtype is not None and out.dtype != dtype:
         raise ValueError(f"{name}: want {dtype}, got {out.dtype}")
     if out.dtype not in _OUT:
         raise ValueError(f"{name}: want bfloat16 or float32, got {out.dtype}")
@@ -70,28 +89,21 @@ def _args(groups: int, rows: int, k: int, n: int, act: int, out: torch.Tensor,
 
 def _split(t: torch.Tensor, name: str, grouped: bool) -> Tuple[int, int, int]:
     """(groups, rows, columns) of a row operand; leading dimensions of the experts' form are groups."""
-    if t.dim() < (3 if grouped else 2):
+    shape = t.shape
+    if len(shape) < (3 if grouped else 2):
         raise ValueError(f"{name}: want {'[groups, rows, columns]' if grouped else '[rows, columns]'}, "
-                         f"got {tuple(t.shape)}")
+                         f"got {tuple(shape)}")
     if grouped:
-        g = 1
-        for d in t.shape[:-2]:
-            g *= d
-        return g, t.shape[-2], t.shape[-1]
-    r = 1
-    for d in t.shape[:-1]:
-        r *= d
-    return 1, r, t.shape[-1]
+        return prod(shape[:-2]), shape[-2], shape[-1]
+    return 1, prod(shape[:-1]), shape[-1]
 
 
 def _weight(w: torch.Tensor, groups: int, grouped: bool) -> Tuple[int, int]:
     """(rows, columns) of one weight."""
-    lead = 1
-    for d in w.shape[:-2]:
-        lead *= d
-    if w.dim() < 2 or (not grouped and w.dim() != 2) or lead != groups:
-        raise ValueError(f"w: want {groups} weight(s) [rows, columns], got {tuple(w.shape)}")
-    return w.shape[-2], w.shape[-1]
+    shape = w.shape
+    if len(shape) < 2 or (not grouped and len(shape) != 2) or prod(shape[:-2]) != groups:
+        raise ValueError(f"w: want {groups} weight(s) [rows, columns], got {tuple(shape)}")
+    return shape[-2], shape[-1]
 
 
 def _forward(x, w, counts, grouped, bias, act, residual, out, out_dtype, preact, status, stream):
@@ -102,17 +114,17 @@ def _forward(x, w, counts, grouped, bias, act, residual, out, out_dtype, preact,
     if wk != k or (code == L.EP_ACT_SWIGLU and wn % 2):
         raise ValueError(f"w: {tuple(w.shape)} does not fit x {tuple(x.shape)} with act {act!r}")
     n = wn // 2 if code == L.EP_ACT_SWIGLU else wn
-    lead = tuple(x.shape[:-1])
+    lead = x.shape[:-1]
     out = _out(out, lead + (n,), out_dtype, dev)
     if bias is not None:
-        _want(bias, "bias", tuple(w.shape[:-1]), dev)
+        _want(bias, "bias", w.shape[:-1], dev)
     if residual is not None:
         _want(residual, "residual", lead + (n,), dev)
     if preact is not None:
         _want(preact, "preact", lead + (wn,), dev)
     a = _args(groups, rows, k, n, code, out, counts, status, dev)
     L.check(L.lib().ep_product(C.byref(a), x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual),
-                               out.data_ptr(), _ptr(preact), _stream_ptr(stream, dev)), "ep_product")
+                               out.data_ptr(), _ptr(preact), stream_of(stream, dev)), "ep_product")
     return out
 
 
@@ -123,7 +135,7 @@ def _dgrad(dy, w, counts, grouped, act, preact, out, out_dtype, status, stream):
     wn, k = _weight(w, groups, grouped)
     if wn != n:
         raise ValueError(f"w: {tuple(w.shape)} does not fit dy {tuple(dy.shape)}")
-    shape = tuple(dy.shape[:-1]) + (2 * k if code == L.EP_ACT_SWIGLU else k,)
+    shape = dy.shape[:-1] + (2 * k if code == L.EP_ACT_SWIGLU else k,)
     if (preact is None) != (code == L.EP_ACT_NONE):
         raise ValueError("preact: wanted with an activation, and only then")
     if preact is not None:
@@ -131,7 +143,7 @@ def _dgrad(dy, w, counts, grouped, act, preact, out, out_dtype, status, stream):
     out = _out(out, shape, out_dtype, dev)
     a = _args(groups, rows, k, n, code, out, counts, status, dev)
     L.check(L.lib().ep_product_dgrad(C.byref(a), dy.data_ptr(), w.data_ptr(), _ptr(preact), out.data_ptr(),
-                                     _stream_ptr(stream, dev)), "ep_product_dgrad")
+                                     stream_of(stream, dev)), "ep_product_dgrad")
     return out
 
 
@@ -142,7 +154,7 @@ def _wgrad(dy, x, counts, grouped, out, out_dtype, accumulate, bias_grad, status
     gx, rx, k = _split(x, "x", grouped)
     if (gx, rx) != (groups, rows):
         raise ValueError(f"x: {tuple(x.shape)} does not fit dy {tuple(dy.shape)}")
-    lead = tuple(dy.shape[:-2]) if grouped else ()
+    lead = dy.shape[:-2] if grouped else ()
     if accumulate and out is None:
         raise ValueError("out: wanted with accumulate")
     out = _out(out, lead + (n, k), out_dtype, dev)
@@ -155,7 +167,7 @@ def _wgrad(dy, x, counts, grouped, out, out_dtype, accumulate, bias_grad, status
         db = torch.empty(lead + (n,), dtype=out.dtype, device=dev)
     a = _args(groups, rows, k, n, L.EP_ACT_NONE, out, counts, status, dev)
     L.check(L.lib().ep_product_wgrad(C.byref(a), dy.data_ptr(), x.data_ptr(), 1 if accumulate else 0,
-                                     out.data_ptr(), _ptr(db), _stream_ptr(stream, dev)), "ep_product_wgrad")
+                                     out.data_ptr(), _ptr(db), stream_of(stream, dev)), "ep_product_wgrad")
     return out if db is None else (out, db)
 
 
@@ -231,10 +243,10 @@ def act_grad(dy: torch.Tensor, preact: torch.Tensor, act: str, *, counts: Option
     if code == L.EP_ACT_NONE:
         raise ValueError("act: want an activation")
     groups, rows, n = _split(dy, "dy", counts is not None)
-    shape = tuple(dy.shape[:-1]) + (2 * n if code == L.EP_ACT_SWIGLU else n,)
+    shape = dy.shape[:-1] + (2 * n if code == L.EP_ACT_SWIGLU else n,)
     _want(preact, "preact", shape, dev)
     out = _out(out, shape, BF16, dev)
     a = _args(groups, rows, n, n, code, out, counts, None, dev)
     L.check(L.lib().ep_act_grad(C.byref(a), dy.data_ptr(), preact.data_ptr(), out.data_ptr(),
-                                _stream_ptr(stream, dev)), "ep_act_grad")
+                                stream_of(stream, dev)), "ep_act_grad")
     return out

@@ -8,7 +8,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib as L
-from .ep import _need, _stream_ptr
+from .product import _want, stream_of
 
 _SCORES = {"softmax": L.EP_SCORE_SOFTMAX, "sigmoid": L.EP_SCORE_SIGMOID}
 _TYPES = {torch.bfloat16: L.EP_BF16, torch.float32: L.EP_F32}
@@ -17,7 +17,7 @@ _TYPES = {torch.bfloat16: L.EP_BF16, torch.float32: L.EP_F32}
 def _args(logits: torch.Tensor, top_k: int, score: str, renormalize: bool, scale: float) -> L.EpTopkC:
     if score not in _SCORES:
         raise ValueError(f"score: want one of {sorted(_SCORES)}, got {score!r}")
-    if logits.dtype not in _TYPES or logits.dim() < 1 or not logits.is_contiguous() or logits.device.type != "cuda":
+    if logits.dtype not in _TYPES or logits.dim() < 1 or not logits.is_contiguous() or not logits.is_cuda:
         raise ValueError(f"logits: want contiguous bfloat16 or float32 [..., E] on a CUDA device, got {logits.dtype} "
                          f"{tuple(logits.shape)} on {logits.device} (contiguous={logits.is_contiguous()})")
     E = logits.shape[-1]
@@ -39,16 +39,18 @@ def route_topk(logits: torch.Tensor, top_k: int, *, score: str = "softmax", reno
     ``top_k`` experts left ends in ids of -1, which dispatch drops.
     """
     a = _args(logits, top_k, score, renormalize, scale)
-    dev, shape = logits.device, tuple(logits.shape[:-1]) + (top_k,)
+    dev, shape = logits.device, logits.shape[:-1] + (top_k,)
     if bias is not None:
-        _need(bias, "bias", torch.float32, (a.E,), dev)
+        _want(bias, "bias", (a.E,), dev, torch.float32)
     if out is None:
-        out = (torch.empty(shape, dtype=torch.int32, device=dev), torch.empty(shape, dtype=torch.float32, device=dev))
-    ids, weights = out
-    _need(ids, "topk_ids", torch.int32, shape, dev)
-    _need(weights, "topk_weights", torch.float32, shape, dev)
+        ids = torch.empty(shape, dtype=torch.int32, device=dev)
+        weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        ids, weights = out
+        _want(ids, "topk_ids", shape, dev, torch.int32)
+        _want(weights, "topk_weights", shape, dev, torch.float32)
     L.check(L.lib().ep_topk_route(C.byref(a), logits.data_ptr(), None if bias is None else bias.data_ptr(),
-                                  ids.data_ptr(), weights.data_ptr(), _stream_ptr(stream, dev)), "ep_topk_route")
+                                  ids.data_ptr(), weights.data_ptr(), stream_of(stream, dev)), "ep_topk_route")
     return ids, weights
 
 
@@ -60,12 +62,13 @@ def route_topk_backward(dweights: torch.Tensor, logits: torch.Tensor, topk_ids: 
     if topk_ids.dim() < 1:
         raise ValueError("topk_ids: want [..., top_k]")
     a = _args(logits, topk_ids.shape[-1], score, renormalize, scale)
-    dev, shape = logits.device, tuple(logits.shape[:-1]) + (a.top_k,)
-    _need(topk_ids, "topk_ids", torch.int32, shape, dev)
-    _need(dweights, "dweights", torch.float32, shape, dev)
+    dev, shape = logits.device, logits.shape[:-1] + (a.top_k,)
+    _want(topk_ids, "topk_ids", shape, dev, torch.int32)
+    _want(dweights, "dweights", shape, dev, torch.float32)
     if out is None:
         out = torch.empty_like(logits)
-    _need(out, "out", logits.dtype, tuple(logits.shape), dev)
+    else:
+        _want(out, "out", logits.shape, dev, logits.dtype)
     L.check(L.lib().ep_topk_route_backward(C.byref(a), dweights.data_ptr(), logits.data_ptr(), topk_ids.data_ptr(),
-                                           out.data_ptr(), _stream_ptr(stream, dev)), "ep_topk_route_backward")
+                                           out.data_ptr(), stream_of(stream, dev)), "ep_topk_route_backward")
     return out
