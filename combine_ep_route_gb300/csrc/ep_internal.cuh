@@ -342,6 +342,22 @@ inline cudaError_t ensure_dyn_smem(const void *fn, size_t bytes) {
     }));
 }
 
+// A launch whose set-up may overlap the end of the kernel before it on the stream; the
+// kernel itself calls pdl_wait() before its first access to global memory.
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int block, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // Each returns the cudaError_t of the launch.
 cudaError_t launch_route(const RouteParams &p, cudaStream_t st);
 size_t route_smem_bytes(int n_ctr, int top_k);

@@ -38,7 +38,7 @@ constexpr int kMaxStages = 12;
 constexpr int kABytes = kLanes * kSubRed * 2;
 constexpr int kChunkBytes = kSubRed * 128;   // MN-major: 64 reduction lines of 64 elements
 constexpr int kTmemCols = 512;       // two accumulators of 256 columns
-constexpr int kMaxSplit = 8;
+constexpr int kMaxSplit = 4;            // clusters of four fill 144 of 152 SMs, of eight 120
 constexpr int kBand = 8;              // lane tiles of a band (see find_tile)
 constexpr uint32_t kSleepNs = 1000000;       // of one attempt at a wait
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -408,8 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int per_cluster = CG == 2 ? 2 : p.split;
     const int t0 = blockIdx.x / per_cluster, t_step = gridDim.x / per_cluster;
 
-    for (int g = threadIdx.x; g < p.groups; g += kThreads)
-        sh->count[g] = p.counts ? max(0, min(p.counts[g], p.rows)) : p.rows;
+    pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(&sh->full[s], 2 * CG);   // an arrival per operand and CTA
@@ -427,6 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         tma_prefetch_map(&p.b[0]);
     }
     if (warp == 3) tmem_alloc<CG>(&sh->tmem, kTmemCols);
+    pdl_wait();   // nothing above reads or writes global memory
+    for (int g = threadIdx.x; g < p.groups; g += kThreads)
+        sh->count[g] = p.counts ? max(0, min(p.counts[g], p.rows)) : p.rows;
     __syncthreads();
     if (warp == 0) {   // exclusive prefix of the groups' column tiles
         int base = 0;
@@ -729,10 +731,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
                 for (int j = 0; j < 32; ++j) acc[j] = 0.f;
                 for (int i = 0; i < p.split; ++i) {
-                    const uint32_t part = map_rank(reinterpret_cast<float *>(stages) + quad * 32 + lane, i);
+                    const uint32_t part =
+                        map_rank(reinterpret_cast<float *>(stages) + c * kLanes + quad * 32 + lane, i);
+                    float got[32];   // all loads on their way before the first is used
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < n) acc[j] += ld_cluster_f32(part + (uint32_t)(c + j) * kLanes * 4);
+                    for (int j = 0; j < 32; ++j) got[j] = j < n ? ld_cluster_f32(part + j * kLanes * 4) : 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[j] += got[j];
                 }
                 tile.row = x.col0 + c;
                 epilogue_chunk(p, acc, row0 + c, n, at, bias, side, tile);
@@ -833,12 +838,15 @@ int launch(const ProductParams &p, int clusters, cudaStream_t st) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemMax;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)size;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    // the set-up (barriers, tensor memory) overlaps the end of the kernel before
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, product_kernel<MODE, GATED, CG>, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 
@@ -860,22 +868,25 @@ int launch(ProductParams &p, cudaStream_t st) {
     if (cg == 1 && !p.counts) {
         // few tiles: narrower ones, then CTAs that share a tile's reduction
         const long long blocks = ceil_div(MODE == PRODUCT_WGRAD ? p.rows : p.red, kSubRed);
-        while (p.col_max > 64 && 16 * (long long)lane_tiles * p.groups * ceil_div(cols, p.col_max) <= sms)
+        while (p.col_max > 64 && 2 * kMaxSplit * (long long)lane_tiles * p.groups * ceil_div(cols, p.col_max) <= sms)
             p.col_max /= 2;
         const long long tiles = (long long)lane_tiles * p.groups * ceil_div(cols, p.col_max);
         while (p.split < kMaxSplit && 2 * p.split * tiles <= sms && blocks >= 8 * p.split) p.split *= 2;
     }
-    p.subs = cg == 2 && !p.out_f32 ? 2 : 1;
-    p.block_red = p.subs * kSubRed;
-    p.block_shift = p.subs == 2 ? 7 : 6;
     p.lane_tiles = (int)ceil_div(lane_tiles, cg);
     const int unit = 16 * cg;
     const int widest = (int)(cols < p.col_max ? ceil_div(cols, unit) * unit : p.col_max);
     p.sub_bytes = kABytes + (MODE == PRODUCT_WGRAD ? (widest / cg + 63) / 64 * kChunkBytes
                                                    : (widest / cg * 128 + 1023) / 1024 * 1024);
-    p.stage_bytes = p.subs * p.sub_bytes;
     const int out_bytes = kEpilogueWarps * (p.out_f32 ? 4096 : 2048);
-    p.stages = (int)((kStageSpace / 1024 * 1024 - out_bytes) / p.stage_bytes);
+    const int space = (int)(kStageSpace / 1024 * 1024) - out_bytes;
+    // two sub-blocks per stage halve the barrier traffic; one where that leaves fewer than
+    // three stages (8192 x 7168 x 4096: 288 against 305 us; 7 rows: 26.7 against 28.7)
+    p.subs = space / (2 * p.sub_bytes) >= 3 ? 2 : 1;
+    p.block_red = p.subs * kSubRed;
+    p.block_shift = p.subs == 2 ? 7 : 6;
+    p.stage_bytes = p.subs * p.sub_bytes;
+    p.stages = space / p.stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     p.out_at = (int)(kStageSpace / 1024 * 1024) - out_bytes;
     if (!make_out_map(&p.o, p.out, p.out_f32, MODE == PRODUCT_DGRAD && gated ? 2 : 1, p.lanes, cols, p.groups))

@@ -89,6 +89,8 @@ __device__ __forceinline__ float usable(float z) { return z >= -FLT_MAX ? fminf(
 
 template <int N, bool BF16>
 __global__ void __launch_bounds__(kThreads) topk_kernel(const TopkParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
     const int lane = threadIdx.x % 32;
     const int t = blockIdx.x * kWarps + threadIdx.x / 32;
     if (t >= p.tokens) return;
@@ -143,6 +145,8 @@ __global__ void __launch_bounds__(kThreads) topk_kernel(const TopkParams p) {
 template <int N, bool BF16>
 __global__ void __launch_bounds__(kThreads) topk_backward_kernel(const TopkParams p) {
     __shared__ float rows[kWarps][N * 32];
+    pdl_launch_dependents();
+    pdl_wait();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int t = blockIdx.x * kWarps + warp;
     if (t >= p.tokens) return;
@@ -199,18 +203,9 @@ __global__ void __launch_bounds__(kThreads) topk_backward_kernel(const TopkParam
 template <bool BACKWARD, int N>
 int launch_n(const TopkParams &p, bool bf16, cudaStream_t st) {
     const int grid = (p.tokens + kWarps - 1) / kWarps;
-    if (BACKWARD) {
-        if (bf16)
-            topk_backward_kernel<N, true><<<grid, kThreads, 0, st>>>(p);
-        else
-            topk_backward_kernel<N, false><<<grid, kThreads, 0, st>>>(p);
-    } else {
-        if (bf16)
-            topk_kernel<N, true><<<grid, kThreads, 0, st>>>(p);
-        else
-            topk_kernel<N, false><<<grid, kThreads, 0, st>>>(p);
-    }
-    return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+    const auto kernel = BACKWARD ? (bf16 ? topk_backward_kernel<N, true> : topk_backward_kernel<N, false>)
+                                 : (bf16 ? topk_kernel<N, true> : topk_kernel<N, false>);
+    return launch_after(kernel, dim3((unsigned)grid), kThreads, st, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 
 template <bool BACKWARD>

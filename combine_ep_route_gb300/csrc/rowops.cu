@@ -24,6 +24,8 @@ __global__ void __launch_bounds__(kThreads) row_sums_kernel(const uint4 *src, co
                                                             int n, int split, int accumulate, void *out) {
     __shared__ float part[kRowLanes][kVecs * 8 + 1];
     __shared__ float sums[kVecs * 8];
+    pdl_launch_dependents();
+    pdl_wait();
     const int g = blockIdx.z, v = blockIdx.y * kVecs + threadIdx.x % kVecs, r0 = threadIdx.x / kVecs;
     const int nvec = n / 8;
     const int count = counts ? max(0, min(counts[g], rows)) : rows;
@@ -94,6 +96,8 @@ __global__ void __launch_bounds__(kThreads) row_sums_kernel(const uint4 *src, co
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const uint4 *dy, const uint4 *z, uint4 *dz,
                                                             const int32_t *counts, int groups, int rows,
                                                             int nvec, int act) {
+    pdl_launch_dependents();
+    pdl_wait();
     const bool gated = act == EP_ACT_SWIGLU;
     for (int g = blockIdx.y; g < groups; g += gridDim.y) {
         const int count = counts ? max(0, min(counts[g], rows)) : rows;
@@ -139,13 +143,15 @@ cudaError_t launch_row_sums(const void *src, const int32_t *counts, int groups, 
     cfg.gridDim = dim3(split, tiles, groups);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     const uint4 *s = static_cast<const uint4 *>(src);
     return out_f32 ? cudaLaunchKernelEx(&cfg, row_sums_kernel<true>, s, counts, rows, n, split, (int)accumulate, out)
                    : cudaLaunchKernelEx(&cfg, row_sums_kernel<false>, s, counts, rows, n, split, (int)accumulate, out);
@@ -170,9 +176,9 @@ extern "C" int ep_act_grad(const ep_product_t *a, const void *dy, const void *pr
     const long long want = a->groups >= 2048 ? 1 : 2432 / a->groups + 1;
     const dim3 grid((unsigned)(per_group < want ? per_group : want), (unsigned)a->groups);
     nvtxRangePushA("ep:act_grad");
-    act_grad_kernel<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint4 *>(dy), static_cast<const uint4 *>(preact), static_cast<uint4 *>(dz), a->counts,
-        a->groups, a->rows, a->n / 8, a->act);
+    const cudaError_t e = launch_after(act_grad_kernel, grid, kThreads, static_cast<cudaStream_t>(stream),
+                                       static_cast<const uint4 *>(dy), static_cast<const uint4 *>(preact),
+                                       static_cast<uint4 *>(dz), a->counts, a->groups, a->rows, a->n / 8, a->act);
     nvtxRangePop();
-    return cudaGetLastError() == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+    return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }

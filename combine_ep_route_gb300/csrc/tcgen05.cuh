@@ -139,7 +139,7 @@ __device__ __forceinline__ uint32_t map_rank(const void *p, uint32_t rank) {
 }
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
