@@ -1,6 +1,8 @@
 // act.cuh -- the activations of the products' epilogues and their derivatives,
-// in fp32. The exponential and division are CUDA's fast forms (a few units in
-// the last place of fp32), far below the rounding of the bf16 they end in.
+// in fp32. Exponentials and reciprocals are the hardware's approximations (PTX
+// ex2.approx and rcp.approx, a unit or two in the last place of fp32), far below the
+// rounding of the bf16 they end in: an epilogue has about as many cycles as its
+// instructions need.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -9,23 +11,57 @@
 
 namespace ep {
 
-__device__ __forceinline__ float sigmoid_f(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+__device__ __forceinline__ float exp2_f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_f(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2E = 1.4426950408889634f;
+
+__device__ __forceinline__ float sigmoid_f(float z) { return rcp_f(1.f + exp2_f(-kLog2E * z)); }
 
 // tanh through one exponential: 1 - 2 / (1 + e^(2u)); the absolute error of a
 // few 2^-24 is what counts, as it is used as 1 + t.
-__device__ __forceinline__ float tanh_f(float u) { return 1.f - __fdividef(2.f, 1.f + __expf(2.f * u)); }
+__device__ __forceinline__ float tanh_f(float u) { return fmaf(-2.f, rcp_f(1.f + exp2_f(2.f * kLog2E * u)), 1.f); }
 
 constexpr float kSqrtHalf = 0.70710678118654752f;     // sqrt(1/2)
 constexpr float kSqrt2OverPi = 0.79788456080286536f;  // sqrt(2/pi)
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;   // 1/sqrt(2 pi)
 constexpr float kGeluCubic = 0.044715f;
 
+// Phi(z), the normal distribution's, and its density's exponential e^(-z^2 / 2): erfc by
+// formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions (absolute
+// error of erf up to 1.5e-7), which shares that exponential with the density. erff and a
+// separate exponential made the epilogue of a gradient through gelu take longer than
+// the product (18 against 16 thousand cycles for a tile of 2048 terms; this: 9).
+__device__ __forceinline__ float normal_cdf(float z, float &density_exp) {
+    const float t = rcp_f(fmaf(0.3275911f * kSqrtHalf, fabsf(z), 1.f));
+    const float e = exp2_f(-0.5f * kLog2E * z * z);
+    float q = 1.061405429f;
+    q = fmaf(q, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    const float tail = 0.5f * q * t * e;
+    density_exp = e;
+    return z < 0.f ? tail : 1.f - tail;
+}
+
 // act(z) of the elementwise activations.
 __device__ __forceinline__ float act_value(float z, int act) {
     switch (act) {
         case EP_ACT_RELU: return z < 0.f ? 0.f : z;   // NaN stays NaN
-        case EP_ACT_SILU: return __fdividef(z, 1.f + __expf(-z));
-        case EP_ACT_GELU: return 0.5f * z * (1.f + erff(z * kSqrtHalf));
+        case EP_ACT_SILU: return z * sigmoid_f(z);
+        case EP_ACT_GELU: {
+            float e;
+            return z * normal_cdf(z, e);
+        }
         case EP_ACT_GELU_TANH:
             return 0.5f * z * (1.f + tanh_f(kSqrt2OverPi * (z + kGeluCubic * z * z * z)));
         default: return z;
@@ -40,8 +76,11 @@ __device__ __forceinline__ float act_slope(float z, int act) {
             const float s = sigmoid_f(z);
             return s * (1.f + z * (1.f - s));
         }
-        case EP_ACT_GELU:
-            return 0.5f * (1.f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * __expf(-0.5f * z * z);
+        case EP_ACT_GELU: {
+            float e;
+            const float cdf = normal_cdf(z, e);
+            return cdf + z * kInvSqrt2Pi * e;
+        }
         case EP_ACT_GELU_TANH: {
             const float t = tanh_f(kSqrt2OverPi * (z + kGeluCubic * z * z * z));
             return 0.5f * (1.f + t) +
@@ -49,6 +88,13 @@ __device__ __forceinline__ float act_slope(float z, int act) {
         }
         default: return 1.f;
     }
+}
+
+// Of y = silu(gate) * up, given dy: the gradients of gate and up.
+__device__ __forceinline__ void swiglu_grad(float dy, float gate, float up, float &dgate, float &dup) {
+    const float s = sigmoid_f(gate), v = gate * s;
+    dup = dy * v;
+    dgate = dy * up * (s + v * (1.f - s));
 }
 
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {

@@ -191,14 +191,33 @@ struct Place {
     }
 };
 
+template <int MODE>
+__device__ __forceinline__ bool wants_side(const ProductParams &p) {
+    return MODE == PRODUCT_FORWARD ? p.residual != nullptr : MODE == PRODUCT_DGRAD ? p.z != nullptr : p.accumulate;
+}
+
+// Has the L2 fetch what the epilogue of a chunk will read, while the product is still
+// being summed: a row per lane.
+template <int MODE, bool GATED>
+__device__ __forceinline__ void prefetch_side(const ProductParams &p, size_t row0, int n, int f, int lane) {
+    if (!wants_side<MODE>(p) || lane >= n || f >= p.lanes) return;
+    const size_t row = row0 + lane;
+    const uint8_t *at;
+    if (MODE == PRODUCT_FORWARD)
+        at = reinterpret_cast<const uint8_t *>(p.residual + row * p.lanes + f);
+    else if (MODE == PRODUCT_DGRAD)
+        at = reinterpret_cast<const uint8_t *>(p.z + row * (GATED ? 2 : 1) * p.lanes + f);
+    else
+        at = static_cast<const uint8_t *>(p.out) + (row * p.lanes + f) * (p.out_f32 ? 4 : 2);
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    if (MODE == PRODUCT_DGRAD && GATED) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 2 * (size_t)p.lanes));
+}
+
 template <int MODE, bool GATED>
 __device__ __forceinline__ void load_side(const ProductParams &p, size_t row0, int n, const Place<MODE, GATED> &at,
                                           Side &side) {
     constexpr int kPairs = MODE == PRODUCT_FORWARD && GATED ? 8 : 16;
-    const bool want = MODE == PRODUCT_FORWARD ? p.residual != nullptr
-                      : MODE == PRODUCT_DGRAD ? GATED || p.act != EP_ACT_NONE
-                                              : p.accumulate;
-    if (!want || !at.ok) return;
+    if (!wants_side<MODE>(p) || !at.ok) return;
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
         const int j = at.column(i);
@@ -352,8 +371,8 @@ __device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const flo
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float2 g = unpack_bf16x2(side.a[i]), u = unpack_bf16x2(side.b[i]);
-            d[i] = make_float2(v[i].x * u.x * act_slope(g.x, EP_ACT_SILU), v[i].y * u.y * act_slope(g.y, EP_ACT_SILU));
-            v[i].x *= act_value(g.x, EP_ACT_SILU), v[i].y *= act_value(g.y, EP_ACT_SILU);
+            swiglu_grad(v[i].x, g.x, u.x, d[i].x, v[i].x);
+            swiglu_grad(v[i].y, g.y, u.y, d[i].y, v[i].y);
         }
         if (n == 32) {
             tile_pairs(p, d, at, tile, 0);
@@ -641,6 +660,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             tile.lane = x.lane0 + quad * 32, tile.group = x.g;
             const int a = n_acc & 1;
             Side side;
+            if (p.split == 1)
+                for (int c = half * 32; c < x.cols; c += 64)
+                    prefetch_side<MODE, GATED>(p, row0 + c, x.cols - c,
+                                               x.lane0 + quad * (MODE == PRODUCT_FORWARD && GATED ? 16 : 32), lane);
             if (p.split == 1 && half * 32 < x.cols)
                 load_side(p, row0 + half * 32, min(32, x.cols - half * 32), at, side);
             if (lo < hi) {
@@ -669,8 +692,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                         if (c + j < x.cols) part[(c + j) * kLanes] = acc[j];
                 } else {
                     tile.row = x.col0 + c;
-                    epilogue_chunk(p, acc, row0 + c, min(32, x.cols - c), at, bias, side, tile);
+                    const Side now = side;
                     if (c + 64 < x.cols) load_side(p, row0 + c + 64, min(32, x.cols - c - 64), at, side);
+                    epilogue_chunk(p, acc, row0 + c, min(32, x.cols - c), at, bias, now, tile);
                 }
             }
             if (lo < hi) {

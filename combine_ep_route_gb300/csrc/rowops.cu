@@ -116,10 +116,11 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const uint4 *dy, con
             for (int q = 0; q < 4; ++q) {
                 const float2 dv = unpack_bf16x2(d[q]), zv = unpack_bf16x2(a[q]), uv = unpack_bf16x2(b[q]);
                 if (gated) {
-                    oa[q] = pack_bf16x2_rn(dv.x * uv.x * act_slope(zv.x, EP_ACT_SILU),
-                                           dv.y * uv.y * act_slope(zv.y, EP_ACT_SILU));
-                    ob[q] = pack_bf16x2_rn(dv.x * act_value(zv.x, EP_ACT_SILU),
-                                           dv.y * act_value(zv.y, EP_ACT_SILU));
+                    float2 dg, du;
+                    swiglu_grad(dv.x, zv.x, uv.x, dg.x, du.x);
+                    swiglu_grad(dv.y, zv.y, uv.y, dg.y, du.y);
+                    oa[q] = pack_bf16x2_rn(dg.x, dg.y);
+                    ob[q] = pack_bf16x2_rn(du.x, du.y);
                 } else {
                     oa[q] = pack_bf16x2_rn(dv.x * act_slope(zv.x, act), dv.y * act_slope(zv.y, act));
                     ob[q] = 0;
