@@ -9,7 +9,7 @@ namespace ep {
 
 enum ProductMode { PRODUCT_FORWARD = 0, PRODUCT_DGRAD = 1, PRODUCT_WGRAD = 2 };
 
-constexpr int kBoxes = 4;   // token-row boxes of the column operand: 128, 64, 32, 16 rows
+constexpr int kBoxes = 8;   // token-row boxes of the column operand: 16, 32, ..., 128 rows
 
 // One product, seen by the kernel as D[col][lane] = sum_r A[lane][r] B[col][r]:
 //   forward  lanes = output features n, columns = tokens, r = k

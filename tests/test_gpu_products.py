@@ -82,6 +82,23 @@ def test_experts_forward_paired(act, k, n):
     check_forward(len(PAIRED), 300, k, n, act, PAIRED, bias=True, residual=True, keep=True)
 
 
+@pytest.mark.parametrize("act", ("none", "swiglu"))
+def test_experts_wide_tiles_long_reduction(act):
+    """257..512 rows of a group as one tile over both accumulators, among narrow ones."""
+    counts = [512, 257, 256, 300, 513, 0, 400, 511, 1, 600, 320, 288] * 4
+    check_forward(len(counts), 600, 2120, 264, act, counts, bias=True, residual=True, keep=True)
+    g = gen(31)
+    E, rows, n, k, two = len(counts), 600, 2120, 136, 2 if act == "swiglu" else 1
+    dy, w, z = normal(g, E, rows, n), normal(g, E, n, k, std=n ** -0.5), normal(g, E, rows, two * k)
+    out = torch.full((E, rows, two * k), 7.0, dtype=BF16, device="cuda")
+    ep.experts_product_dgrad(dy, w, torch.tensor(counts, dtype=torch.int32, device="cuda"), act=act,
+                             preact=None if act == "none" else z, out=out)
+    for e, c in enumerate(counts):
+        d, ed = R.dgrad(dy[e, :c], w[e], act, z[e, :c], BF16)
+        close(out[e, :c], d, ed, f"expert {e}")
+        assert (out[e, c:] == 7.0).all()
+
+
 @pytest.mark.parametrize("rows", [1, 7, 64, 130, 300])
 @pytest.mark.parametrize("k,n", [(4104, 136), (7168, 16), (1000, 3080)])
 def test_linear_long_reduction_few_tiles(rows, k, n):
