@@ -1,10 +1,10 @@
 // router.cu -- top-k routing of tokens from router logits, and its gradient.
 //
 // One warp per token, the token's logits in registers (expert i * 32 + lane in
-// slot i). Each of the top_k rounds is two warp reductions: the largest key (the
-// logit plus bias as an order-preserving integer), then the lowest expert among
-// those that hold it. The weights need the chosen logits only, except for the
-// softmax over all experts, which adds one sum.
+// slot i) as order-preserving integers of logit plus bias. Ties go to the lowest
+// expert. The weights need the chosen logits only, except for the softmax over all
+// experts, which adds one sum. Instructions bound it, not memory: a token's 256 bf16
+// logits are 512 bytes.
 #include "ep_internal.cuh"
 
 #include <cfloat>
@@ -111,29 +111,81 @@ __global__ void __launch_bounds__(kThreads) topk_kernel(const TopkParams p) {
     float2 all = make_float2(0.f, 1.f);
     if (p.score == EP_SCORE_SOFTMAX && !p.renormalize) all = softmax_stats(z);
 
-    int id = -1;        // lane k: the k-th choice
-    for (int k = 0; k < p.K; ++k) {
-        uint32_t best = 0;
-        int slot = 0;
+    int rank = p.K, id = -1;   // this lane's choice, if it has one: place and expert
+    int n = 0;                 // choices of the row
+    bool done = false;
+    if constexpr (N >= 4) {
+        // The top_k-th largest of the lanes' maxima bounds the top_k-th largest logit from
+        // below. What is not smaller is usually little more than top_k: those go to a lane
+        // each, in expert order, and count who is ahead of them. (8192 tokens, 256 experts,
+        // top 8: 11.0 -> 7.9 us against a round per choice.)
+        __shared__ uint2 kept[kWarps][32];
+        uint32_t most = key[0];
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (key[i] > best) best = key[i], slot = i;
-        const uint32_t top = __reduce_max_sync(kAll, best);
-        if (top == 0) break;
-        const int mine = slot * 32 + lane;
-        const int e = (int)__reduce_min_sync(kAll, best == top ? (uint32_t)mine : 0xFFFFFFFFu);
+        for (int i = 1; i < N; ++i) most = max(most, key[i]);
+        uint32_t bound = 0;
+        for (int k = 0; k < p.K; ++k) {
+            bound = __reduce_max_sync(kAll, most);
+            if (most == bound) most = 0;
+        }
+        bound = max(bound, 1u);
+        uint32_t held[N];
+        int total = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (e == i * 32 + lane) key[i] = 0;
-        if (lane == k) id = e;
+        for (int i = 0; i < N; ++i) {
+            held[i] = __ballot_sync(kAll, key[i] >= bound);
+            total += __popc(held[i]);
+        }
+        if (total <= 32) {
+            uint2 *slot = kept[threadIdx.x / 32];
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (key[i] >= bound) slot[at + __popc(held[i] & lanemask_lt())] = make_uint2(key[i], i * 32 + lane);
+                at += __popc(held[i]);
+            }
+            __syncwarp();
+            const uint2 own = lane < total ? slot[lane] : make_uint2(0u, 0u);
+            int ahead = 0;
+            for (int j = 0; j < total; ++j) {
+                const uint32_t other = __shfl_sync(kAll, own.x, j);
+                ahead += other > own.x || (other == own.x && j < lane);
+            }
+            if (lane < total && ahead < p.K) rank = ahead, id = (int)own.y;
+            n = min(total, p.K);
+            done = true;
+        }
+    }
+    if (!done) {   // few experts, or many ties: a round per choice, kept by lane k
+        for (int k = 0; k < p.K; ++k) {
+            uint32_t best = 0;
+            int slot = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (key[i] > best) best = key[i], slot = i;
+            const uint32_t top = __reduce_max_sync(kAll, best);
+            if (top == 0) break;
+            const int mine = slot * 32 + lane;
+            const int e = (int)__reduce_min_sync(kAll, best == top ? (uint32_t)mine : 0xFFFFFFFFu);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (e == i * 32 + lane) key[i] = 0;
+            if (lane == k) rank = k, id = e;
+            ++n;
+        }
     }
     // the chosen logits again, from cache: picking them out of the registers would
     // need a run-time index
     const float chosen = id >= 0 ? usable(load_logit<BF16>(p.logits, (size_t)t * p.E + id)) : 0.f;
     const float w = p.scale * weight_of(p, chosen, id >= 0, all);
-    if (lane < p.K) {
-        p.ids[(size_t)t * p.K + lane] = id;
-        p.weights[(size_t)t * p.K + lane] = id >= 0 ? w : 0.f;
+    const size_t out = (size_t)t * p.K;
+    if (id >= 0) {
+        p.ids[out + rank] = id;
+        p.weights[out + rank] = w;
+    }
+    if (lane >= n && lane < p.K) {
+        p.ids[out + lane] = -1;
+        p.weights[out + lane] = 0.f;
     }
 }
 
