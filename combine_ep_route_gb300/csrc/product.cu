@@ -847,6 +847,54 @@ cudaError_t sm_count(int *out) {
     return e;
 }
 
+constexpr long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// How a product is cut: CTAs per MMA, widest column tile, CTAs that share a tile's reduction.
+struct Plan {
+    int cg, col_max, split;
+};
+
+// Ragged groups, whose row counts the host does not know: pairs of CTAs where one tile
+// per group and lane tile, or full groups, fill the GPU; single CTAs otherwise.
+Plan plan_ragged(long long lane_tiles, long long groups, long long cols, int sms) {
+    const long long pairs = ceil_div(lane_tiles, 2) * groups * ceil_div(cols, kColMax);
+    return {lane_tiles > 1 && 2 * pairs >= sms ? 2 : 1, kColMax, 1};
+}
+
+// Dense products: the cut with the least estimated time. A round (one tile on every SM)
+// costs, per 64 reduction elements, the share kCost of what a pair's tile of 256 lanes x
+// 256 columns takes (0.363 us), measured by column width on 8192 x 7168 x 4096, a tile
+// of 128 lanes on a single CTA included. Narrow tiles are dear (both operands pass through
+// shared memory for fewer MMAs), so they pay only where wide ones leave SMs idle; sharing
+// a reduction adds a join of about 2 us, and the last epilogue shows, 2.3 us for 256 columns.
+// Measured against pairs of full tiles where those fill the GPU and single CTAs otherwise:
+// 512 x 7168 x 4096 33.8 -> 28.5 us, 1024 x 4096 x 4096 29.7 -> 27.2, 3000 x 4096 x 1024
+// 27.6 -> 22.6, 1024 x 7168 x 7168 78 -> 79.
+Plan plan_dense(long long lane_tiles, long long groups, long long cols, long long red, int sms) {
+    static const float kCost[2][8] = {{.51f, .54f, .65f, .73f, .88f, .91f, 1.05f, 1.19f},
+                                      {.46f, .47f, .51f, .58f, .75f, .78f, .91f, 1.f}};
+    const float blocks = (float)ceil_div(red, kSubRed);
+    Plan best = {1, kColMax, 1};
+    float best_us = 0.f;
+    for (int cg = 1; cg <= 2; ++cg) {
+        if (cg == 2 && lane_tiles < 2) break;
+        const int slots = sms / cg;
+        for (int w = 1; w <= kColMax / 32; ++w) {
+            const long long tiles = ceil_div(lane_tiles, cg) * groups * ceil_div(cols, 32 * w);
+            for (int split = 1; split <= (cg == 1 ? kMaxSplit : 1); split *= 2) {
+                // (clusters of four fit on all but a few SMs: 144 of 152)
+                if (split > 1 && (split * tiles > (split == 4 ? sms - sms / 16 : sms) || blocks < 8 * split)) break;
+                const float rounds = split > 1 ? 1.f : (float)ceil_div(tiles, slots);
+                const float us = rounds * kCost[cg - 1][w - 1] * .363f * blocks / split + (split > 1 ? 2.f : 0.f) +
+                                 2.3f / 8 * w / split;
+                if (best_us == 0.f || us < best_us) best_us = us, best = {cg, 32 * w, split};
+            }
+            if (32 * w >= cols) break;
+        }
+    }
+    return best;
+}
+
 template <int MODE, bool GATED, int CG>
 int launch(const ProductParams &p, int clusters, cudaStream_t st) {
     const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, GATED, CG>);
@@ -878,20 +926,11 @@ int launch(ProductParams &p, cudaStream_t st) {
     if (sm_count(&sms) != cudaSuccess) return EP_ERR_CUDA;
     p.wait_limit_ns = kWaitLimitNs;
     const int lane_tiles = (p.lanes + per_tile - 1) / per_tile;
-    auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };
-    // pairs of CTAs where they fill the GPU; otherwise single CTAs, which cut the work finer
-    p.col_max = kColMax;
-    const long long pairs = ceil_div(lane_tiles, 2) * p.groups * ceil_div(cols, kColMax);
-    const int cg = lane_tiles > 1 && 2 * pairs >= sms ? 2 : 1;
-    p.split = 1;
-    if (cg == 1 && !p.counts) {
-        // few tiles: narrower ones, then CTAs that share a tile's reduction
-        const long long blocks = ceil_div(MODE == PRODUCT_WGRAD ? p.rows : p.red, kSubRed);
-        while (p.col_max > 64 && 2 * kMaxSplit * (long long)lane_tiles * p.groups * ceil_div(cols, p.col_max) <= sms)
-            p.col_max /= 2;
-        const long long tiles = (long long)lane_tiles * p.groups * ceil_div(cols, p.col_max);
-        while (p.split < kMaxSplit && 2 * p.split * tiles <= sms && blocks >= 8 * p.split) p.split *= 2;
-    }
+    const Plan plan = p.counts ? plan_ragged(lane_tiles, p.groups, cols, sms)
+                               : plan_dense(lane_tiles, p.groups, cols, MODE == PRODUCT_WGRAD ? p.rows : p.red, sms);
+    const int cg = plan.cg;
+    p.col_max = plan.col_max;
+    p.split = plan.split;
     p.lane_tiles = (int)ceil_div(lane_tiles, cg);
     const int unit = 16 * cg;
     const int widest = (int)(cols < p.col_max ? ceil_div(cols, unit) * unit : p.col_max);
