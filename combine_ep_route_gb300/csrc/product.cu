@@ -13,10 +13,20 @@
 // one lane tile, interleaved in blocks of 8 or 16 by the tensor map alone, so
 // that both halves of an output element are in the same warp.
 //
-// One persistent CTA per SM: a TMA warp, an MMA warp, a warp that zeroes the
-// rows past a group's count in the weight gradient's last block (a count can
-// end inside it, and whatever lies there may be NaN), and four epilogue warps
-// that drain one accumulator while the next fills.
+// One persistent CTA per SM: a TMA warp per operand, an MMA warp, a warp that
+// zeroes the rows past a group's count in the weight gradient's last block (a
+// count can end inside it, and whatever lies there may be NaN), and eight epilogue
+// warps that drain one accumulator while the next fills. Large products run on
+// pairs of CTAs (cta_group::2, 256 lanes x 256 columns): each holds half of either
+// operand, which halves what a tile reads through shared memory, the limit of a
+// single CTA (8192 x 7168 x 4096: 287 against 346 us; a cuBLAS product 279). Products
+// with few tiles run on single CTAs, up to four of them sharing a tile's reduction
+// and joining their sums through distributed shared memory, in order.
+//
+// What bounds it: the tensor cores under the power limit for long dense products
+// (1680 TFLOP/s of 1729 sustained by cuBLAS), the weights' bytes for few rows per
+// expert (128 experts of 4096 x 7168 with 16 rows each: 1.135 ms, 6.62 TB/s of the
+// copy's 6.67), and the depth of the ring of stages, three of 64 KB, in between.
 #include "product.cuh"
 
 #include <atomic>
@@ -278,7 +288,7 @@ struct OutTile {
 
 // Full tiles leave through shared memory and a TMA store: as stores of each lane they
 // kept the epilogue warps waiting on the memory pipe, and with the short reductions of
-// a weight gradient the epilogue sets the pace (0.88 -> 0.68 ms on 32 experts of 4096 x
+// a weight gradient the epilogue sets the pace (885 -> 725 us on 32 experts of 4096 x
 // 7168 with 256 rows each, in fp32). Lanes past the last feature are cut by the map.
 template <int MODE, bool GATED>
 __device__ __forceinline__ void tile_pairs(const ProductParams &p, const float2 (&v)[16], const Place<MODE, GATED> &at,
@@ -297,7 +307,7 @@ __device__ __forceinline__ void tile_pairs(const ProductParams &p, const float2 
     }
     fence_async();
     __syncwarp();
-    if (elect_one()) {
+    if (elect_one() && tile.lane < p.lanes) {
         tma_store_4d(&p.o, tile.smem, tile.lane, half, tile.row, tile.group);
         bulk_commit();
     }
@@ -312,7 +322,7 @@ __device__ __forceinline__ void tile_lanes(const ProductParams &p, const float (
     for (int j = 0; j < 32; ++j) o[j * 32] = acc[j];
     fence_async();
     __syncwarp();
-    if (elect_one()) {
+    if (elect_one() && tile.lane < p.lanes) {
         tma_store_4d(&p.o, tile.smem, tile.lane, 0, tile.row, tile.group);
         bulk_commit();
     }
@@ -966,6 +976,9 @@ bool product_ok(const ep_product_t *a, bool wgrad) {
     if (!a || a->groups < 1 || a->groups > EP_MAX_E || a->rows < 0) return false;
     if (a->k < 8 || a->n < 8 || a->k % 8 || a->n % 8 || a->k > (1 << 24) || a->n > (1 << 24)) return false;
     if ((long long)a->groups * a->rows >= (1LL << 31)) return false;
+    // a tensor map's strides stay below 2^40 bytes
+    const long long wide = 4LL * (a->k > a->n ? a->k : a->n);   // elements of the widest row, and both its halves
+    if (wide * a->rows >= (1LL << 38) || 4LL * a->n * a->k >= (1LL << 38)) return false;
     if (a->act < EP_ACT_NONE || a->act > EP_ACT_SWIGLU || (wgrad && a->act != EP_ACT_NONE)) return false;
     if (a->out_dtype != EP_BF16 && a->out_dtype != EP_F32) return false;
     return reinterpret_cast<uintptr_t>(a->counts) % 4 == 0 && reinterpret_cast<uintptr_t>(a->status) % 4 == 0;

@@ -26,14 +26,15 @@ __global__ void __launch_bounds__(kThreads) row_sums_kernel(const uint4 *src, co
     __shared__ float sums[kVecs * 8];
     pdl_launch_dependents();
     pdl_wait();
-    const int g = blockIdx.z, v = blockIdx.y * kVecs + threadIdx.x % kVecs, r0 = threadIdx.x / kVecs;
+    const int g = blockIdx.y, part_id = blockIdx.x % split, tile = blockIdx.x / split;
+    const int v = tile * kVecs + threadIdx.x % kVecs, r0 = threadIdx.x / kVecs;
     const int nvec = n / 8;
     const int count = counts ? max(0, min(counts[g], rows)) : rows;
     float a[8] = {};
     if (v < nvec) {
         const uint4 *p = src + (size_t)g * rows * nvec + v;
         const int step = kRowLanes * split;
-        int r = blockIdx.x * kRowLanes + r0;
+        int r = part_id * kRowLanes + r0;
         for (; r + 3 * step < count; r += 4 * step) {
             uint4 x[4];
 #pragma unroll
@@ -71,15 +72,15 @@ __global__ void __launch_bounds__(kThreads) row_sums_kernel(const uint4 *src, co
         namespace cg = cooperative_groups;
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
-        if (blockIdx.x == 0 && c < kVecs * 8) {
+        if (part_id == 0 && c < kVecs * 8) {
             float s = 0.f;
             for (int i = 0; i < split; ++i) s += *cluster.map_shared_rank(&sums[c], i);
             sums[c] = s;
         }
         cluster.sync();
-        if (blockIdx.x != 0) return;
+        if (part_id != 0) return;
     }
-    const int col = blockIdx.y * kVecs * 8 + c;
+    const int col = tile * kVecs * 8 + c;
     if (c < kVecs * 8 && col < n) {
         const size_t at = (size_t)g * n + col;
         if (OUT_F32) {
@@ -137,11 +138,10 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const uint4 *dy, con
 cudaError_t launch_row_sums(const void *src, const int32_t *counts, int groups, int rows, int n, bool out_f32,
                             bool accumulate, void *out, cudaStream_t st) {
     const int tiles = (n + kVecs * 8 - 1) / (kVecs * 8);
-    if (tiles > 65535) return cudaErrorInvalidValue;
     // few column tiles with many rows: a cluster's CTAs share the rows
     const int split = (long long)tiles * groups < 512 && rows > 4 * kRowLanes ? kSplit : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(split, tiles, groups);
+    cfg.gridDim = dim3((unsigned)split * tiles, groups);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];

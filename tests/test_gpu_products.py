@@ -404,3 +404,15 @@ def test_refusals():
         ep.experts_product(x[None], w[None], torch.zeros(2, dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         ep.experts_product(x[None], w[None], torch.zeros(1, dtype=torch.int64, device="cuda"))
+
+
+def test_offsets_past_32_bits():
+    """An output of over 2^32 elements, its first and last rows."""
+    g = gen(40)
+    rows, k, n = 140001, 64, 32768
+    x, w = normal(g, rows, k), normal(g, n, k, std=0.125)
+    y = ep.linear(x, w, act="relu")
+    assert y.numel() > 1 << 32
+    for at in (slice(0, 40), slice(rows - 40, rows)):
+        want, e, _, _ = R.forward(x[at], w, None, "relu", None, BF16)
+        close(y[at], want, e)
