@@ -118,33 +118,46 @@ __device__ __forceinline__ int quotient(int a, int b) {
     return q;
 }
 
-// Tile t of the launch. Tiles are visited in rising order, so the group is found by
-// walking on from the last one's (g).
+// A role's place in the launch's tiles, which it visits in rising order: the current
+// group, the first tile after it, and what its tiles have in common.
+struct Walk {
+    int g = -1, begin = 0, end = 0;   // the group's tiles [begin, end)
+    int ct = 0, all = 0, width = 0;   // column tiles, columns, columns of a tile
+    int red = 0, blocks = 0;
+};
+
 template <int MODE, bool GATED, int CG>
-__device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *sh, int t, uint32_t rank, int &g) {
-    while (t >= sh->first[g + 1] * p.lane_tiles) ++g;
-    Tile x;
-    x.g = g;
-    const int first = sh->first[g];
-    const int r = t - first * p.lane_tiles;
-    const int ct = sh->first[g + 1] - first;
-    const int count = sh->count[g];
-    const int all = MODE == PRODUCT_WGRAD ? p.cols : count;
-    // bands of kBand lane tiles, lane tiles innermost: the tiles in flight at a time form
-    // a square rather than a strip, so each operand block is fetched by several of them
-    const int band = ct == 1 ? r / kBand : quotient(r, kBand * ct), in_band = r - band * kBand * ct;
-    const int high = min(kBand, p.lane_tiles - band * kBand);
-    const int c = ct == 1 ? 0 : high == kBand ? in_band / kBand : quotient(in_band, high);
-    const int lt = band * kBand + in_band - c * high;
+__device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *sh, int t, uint32_t rank, Walk &w) {
     constexpr int kUnit = 16 * CG;
     constexpr int kPer = GATED && MODE == PRODUCT_FORWARD ? kLanes / 2 : kLanes;
-    const int width = ((ct == 1 ? all : quotient(all + ct - 1, ct)) + kUnit - 1) / kUnit * kUnit;
+    if (t >= w.end) {
+        do {
+            ++w.g;
+            w.begin = w.end;
+            w.end = sh->first[w.g + 1] * p.lane_tiles;
+        } while (t >= w.end);
+        w.ct = sh->first[w.g + 1] - sh->first[w.g];
+        const int count = sh->count[w.g];
+        w.all = MODE == PRODUCT_WGRAD ? p.cols : count;
+        w.width = ((w.ct == 1 ? w.all : quotient(w.all + w.ct - 1, w.ct)) + kUnit - 1) / kUnit * kUnit;
+        w.red = MODE == PRODUCT_WGRAD ? count : p.red;
+        w.blocks = (w.red + p.block_red - 1) >> p.block_shift;
+    }
+    // bands of kBand lane tiles, lane tiles innermost: the tiles in flight at a time form
+    // a square rather than a strip, so each operand block is fetched by several of them
+    const int r = t - w.begin;
+    const int band = w.ct == 1 ? r / kBand : quotient(r, kBand * w.ct), in_band = r - band * kBand * w.ct;
+    const int high = min(kBand, p.lane_tiles - band * kBand);
+    const int c = w.ct == 1 ? 0 : high == kBand ? in_band / kBand : quotient(in_band, high);
+    const int lt = band * kBand + in_band - c * high;
+    Tile x;
+    x.g = w.g;
     x.lane0 = (CG == 1 ? lt : lt * 2 + (int)rank) * kPer;
-    x.col0 = c * width;
-    x.cols = min(width, all - x.col0);
+    x.col0 = c * w.width;
+    x.cols = min(w.width, w.all - x.col0);
     x.n_mma = (x.cols + kUnit - 1) / kUnit * kUnit;
-    x.red = MODE == PRODUCT_WGRAD ? count : p.red;
-    x.blocks = (x.red + p.block_red - 1) >> p.block_shift;
+    x.red = w.red;
+    x.blocks = w.blocks;
     return x;
 }
 
@@ -160,16 +173,13 @@ __device__ __forceinline__ void my_blocks(const ProductParams &p, const Tile &x,
 // The tensor cores truncate each step's sum to fp32, which a bf16 result hides but an
 // fp32 one shows (relative error 8e-6 after 448 steps, k = 7168). Where a tile's columns
 // leave room, the reduction of an fp32 result goes to several accumulators in turn, added
-// up with rounding in the epilogue: their number, columns apart and blocks each.
+// up with rounding in the epilogue: columns apart, blocks each.
 struct Segments {
-    int most, apart, blocks;
+    int apart, blocks;
 };
 __device__ __forceinline__ Segments segments(const ProductParams &p, const Tile &x, int blocks) {
-    Segments g;
-    g.most = !p.out_f32 ? 1 : x.n_mma <= 64 ? 4 : x.n_mma <= 128 ? 2 : 1;
-    g.apart = kColMax / g.most;
-    g.blocks = g.most == 1 ? blocks : (blocks + g.most - 1) / g.most;
-    return g;
+    const int shift = !p.out_f32 ? 0 : x.n_mma <= 64 ? 2 : x.n_mma <= 128 ? 1 : 0;   // log2 of their number
+    return {kColMax >> shift, (blocks + (1 << shift) - 1) >> shift};
 }
 
 // Two output features (f, f + 1) of token column j or j + 1: lanes trade with
@@ -216,16 +226,11 @@ struct Place {
     }
 };
 
-template <int MODE>
-__device__ __forceinline__ bool wants_side(const ProductParams &p) {
-    return MODE == PRODUCT_FORWARD ? p.residual != nullptr : MODE == PRODUCT_DGRAD ? p.z != nullptr : p.accumulate;
-}
-
 // Has the L2 fetch what the epilogue of a chunk will read, while the product is still
 // being summed: a row per lane.
 template <int MODE, bool GATED>
 __device__ __forceinline__ void prefetch_side(const ProductParams &p, size_t row0, int n, int f, int lane) {
-    if (!wants_side<MODE>(p) || lane >= n || f >= p.lanes) return;
+    if (lane >= n || f >= p.lanes) return;
     const size_t row = row0 + lane;
     const uint8_t *at;
     if (MODE == PRODUCT_FORWARD)
@@ -242,7 +247,7 @@ template <int MODE, bool GATED>
 __device__ __forceinline__ void load_side(const ProductParams &p, size_t row0, int n, const Place<MODE, GATED> &at,
                                           Side &side) {
     constexpr int kPairs = MODE == PRODUCT_FORWARD && GATED ? 8 : 16;
-    if (!wants_side<MODE>(p) || !at.ok) return;
+    if (!at.ok) return;
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
         const int j = at.column(i);
@@ -346,13 +351,13 @@ __device__ __forceinline__ void tile_lanes(const ProductParams &p, const float (
 // The epilogue of 32 accumulator columns of one warp's 32 lanes, of which n are
 // output rows row0 .. row0 + n - 1. Straight-line over the 16 pairs, so that
 // their arithmetic and stores overlap.
-template <int MODE, bool GATED>
+template <int MODE, bool GATED, bool SIDE>
 __device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const float (&acc)[32], size_t row0, int n,
                                                const Place<MODE, GATED> &at, float2 bias, const Side &side,
                                                const OutTile &tile) {
     const size_t L = (size_t)p.lanes;
     if constexpr (MODE == PRODUCT_WGRAD) {
-        if (n == 32 && p.out_f32 && !p.accumulate) {   // nothing to pair up: lanes side by side already
+        if (!SIDE && n == 32 && p.out_f32) {   // nothing to pair up: lanes side by side already
             tile_lanes(p, acc, tile);
             return;
         }
@@ -383,7 +388,7 @@ __device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const flo
             const float2 gate = at.up ? got : a, up = at.up ? b : got;
             y[i] = make_float2(act_value(gate.x, EP_ACT_SILU) * up.x, act_value(gate.y, EP_ACT_SILU) * up.y);
         }
-        if (p.residual) {
+        if (SIDE) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float2 r = unpack_bf16x2(side.a[i]);
@@ -415,7 +420,7 @@ __device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const flo
                 case EP_ACT_GELU_TANH: act_pairs<EP_ACT_GELU_TANH>(v); break;
                 default: break;
             }
-        } else if (MODE == PRODUCT_DGRAD) {
+        } else if (MODE == PRODUCT_DGRAD && SIDE) {
             switch (p.act) {
                 case EP_ACT_RELU: slope_pairs<EP_ACT_RELU>(v, side.a); break;
                 case EP_ACT_SILU: slope_pairs<EP_ACT_SILU>(v, side.a); break;
@@ -424,7 +429,7 @@ __device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const flo
                 default: break;
             }
         }
-        if ((MODE == PRODUCT_FORWARD && p.residual) || (MODE == PRODUCT_WGRAD && p.accumulate)) {
+        if (MODE != PRODUCT_DGRAD && SIDE) {
             const bool wide = MODE == PRODUCT_WGRAD && p.out_f32;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -440,7 +445,7 @@ __device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const flo
     }
 }
 
-template <int MODE, bool GATED, int CG>
+template <int MODE, bool GATED, int CG, bool SIDE>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductParams p) {
     constexpr bool kMnA = MODE != PRODUCT_FORWARD, kMnB = MODE == PRODUCT_WGRAD;
     extern __shared__ uint8_t raw[];
@@ -497,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const uint32_t tmem = sh->tmem;
 
     Ring ring;
-    int group = 0;                          // of the current tile
+    Walk walk;
     uint32_t n_acc = 0;                     // accumulators so far
     int issued = 0;                         // producer: blocks so far
     uint32_t on_tail = 0, tail_phase = 0;   // producer, a bit per stage: last load signals tail[], and its phase
@@ -508,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const bool lanes = warp == 0;
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, group);
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, walk);
             const int own_cols = x.n_mma / CG;
             const int col0 = x.col0 + (CG == 2 ? (int)rank * own_cols : 0);
             const int chunks = (own_cols + 63) / 64;
@@ -573,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         // ---- MMA: one thread issues the steps of 16 of each block
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, group);
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, walk);
             int lo, hi;
             my_blocks(p, x, rank, lo, hi);
             if (lo == hi) continue;
@@ -620,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         uint32_t used = 0;   // a bit per stage: parity of its next use here
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, group);
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, walk);
             int lo, hi;
             my_blocks(p, x, rank, lo, hi);
             const int left = x.red % kSubRed;
@@ -670,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         };
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, group);
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, walk);
             int lo, hi;
             my_blocks(p, x, rank, lo, hi);
             if (p.split == 1 && lo == hi && MODE == PRODUCT_WGRAD && p.accumulate) continue;
@@ -684,11 +689,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int a = n_acc & 1;
             const Segments seg = segments(p, x, hi - lo);
             Side side;
-            if (p.split == 1)
+            if (SIDE && p.split == 1)
                 for (int c = half * 32; c < x.cols; c += 64)
                     prefetch_side<MODE, GATED>(p, row0 + c, x.cols - c,
                                                x.lane0 + quad * (MODE == PRODUCT_FORWARD && GATED ? 16 : 32), lane);
-            if (p.split == 1 && half * 32 < x.cols)
+            if (SIDE && p.split == 1 && half * 32 < x.cols)
                 load_side(p, row0 + half * 32, min(32, x.cols - half * 32), at, side);
             if (lo < hi) {
                 ok = role_wait(&sh->acc_full[a], (n_acc / 2) & 1, sh, p);
@@ -724,8 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 } else {
                     tile.row = x.col0 + c;
                     const Side now = side;
-                    if (c + 64 < x.cols) load_side(p, row0 + c + 64, min(32, x.cols - c - 64), at, side);
-                    epilogue_chunk(p, acc, row0 + c, min(32, x.cols - c), at, bias, now, tile);
+                    if (SIDE && c + 64 < x.cols) load_side(p, row0 + c + 64, min(32, x.cols - c - 64), at, side);
+                    epilogue_chunk<MODE, GATED, SIDE>(p, acc, row0 + c, min(32, x.cols - c), at, bias, now, tile);
                 }
             }
             if (lo < hi) {
@@ -765,8 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         cluster_sync();
         if (t0 < total && warp >= 4) {
             const int quad = warp % 4, half = (warp - 4) / 4;
-            group = 0;
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t0, rank, group);
+            walk = Walk();
+            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t0, rank, walk);
             const Place<MODE, GATED> at(p, x, quad, lane);
             const size_t row0 = (size_t)x.g * (MODE == PRODUCT_WGRAD ? p.cols : p.rows) + x.col0;
             float2 bias = make_float2(0.f, 0.f);
@@ -781,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             for (int c = (int)rank * share + half * 32; c < c1; c += 64) {
                 const int n = min(32, c1 - c);
                 Side side;
-                load_side(p, row0 + c, n, at, side);
+                if (SIDE) load_side(p, row0 + c, n, at, side);
                 float acc[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) acc[j] = 0.f;
@@ -795,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     for (int j = 0; j < 32; ++j) acc[j] += got[j];
                 }
                 tile.row = x.col0 + c;
-                epilogue_chunk(p, acc, row0 + c, n, at, bias, side, tile);
+                epilogue_chunk<MODE, GATED, SIDE>(p, acc, row0 + c, n, at, bias, side, tile);
             }
             if (elect_one()) bulk_wait_all();
         }
@@ -931,9 +936,9 @@ Plan plan_dense(long long lane_tiles, long long groups, long long cols, long lon
     return best;
 }
 
-template <int MODE, bool GATED, int CG>
+template <int MODE, bool GATED, int CG, bool SIDE>
 int launch(const ProductParams &p, int clusters, cudaStream_t st) {
-    const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, GATED, CG>);
+    const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, GATED, CG, SIDE>);
     if (ensure_dyn_smem(fn, kSmemMax) != cudaSuccess) return EP_ERR_CUDA;
     const int size = CG == 2 ? 2 : p.split;
     cudaLaunchConfig_t cfg = {};
@@ -950,7 +955,7 @@ int launch(const ProductParams &p, int clusters, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, product_kernel<MODE, GATED, CG>, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, product_kernel<MODE, GATED, CG, SIDE>, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 
 template <int MODE>
@@ -989,11 +994,18 @@ int launch(ProductParams &p, cudaStream_t st) {
     if (most >= (1LL << 31)) return EP_ERR_INVALID_ARG;
     const long long room = p.split > 1 ? most : sms / cg;
     const int clusters = (int)(most < room ? most : room);
+    // whether the epilogue reads from memory: residual, pre-activations, output added to
+    const bool side = MODE == PRODUCT_FORWARD ? p.residual != nullptr : MODE == PRODUCT_DGRAD ? p.z != nullptr : p.accumulate;
     if constexpr (MODE != PRODUCT_WGRAD) {
-        if (gated)
-            return cg == 2 ? launch<MODE, true, 2>(p, clusters, st) : launch<MODE, true, 1>(p, clusters, st);
+        if (gated) {
+            if (MODE == PRODUCT_DGRAD || side)
+                return cg == 2 ? launch<MODE, true, 2, true>(p, clusters, st) : launch<MODE, true, 1, true>(p, clusters, st);
+            return cg == 2 ? launch<MODE, true, 2, MODE == PRODUCT_DGRAD>(p, clusters, st)
+                           : launch<MODE, true, 1, MODE == PRODUCT_DGRAD>(p, clusters, st);
+        }
     }
-    return cg == 2 ? launch<MODE, false, 2>(p, clusters, st) : launch<MODE, false, 1>(p, clusters, st);
+    if (side) return cg == 2 ? launch<MODE, false, 2, true>(p, clusters, st) : launch<MODE, false, 1, true>(p, clusters, st);
+    return cg == 2 ? launch<MODE, false, 2, false>(p, clusters, st) : launch<MODE, false, 1, false>(p, clusters, st);
 }
 
 bool aligned16(const void *q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
