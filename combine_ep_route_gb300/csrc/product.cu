@@ -958,8 +958,9 @@ int launch(const ProductParams &p, int clusters, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, product_kernel<MODE, GATED, CG, SIDE>, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 
+// Plans and launches; `b` is the column operand, [groups][rows][width].
 template <int MODE>
-int launch(ProductParams &p, cudaStream_t st) {
+int launch(ProductParams &p, const void *b, int width, cudaStream_t st) {
     const bool gated = p.act == EP_ACT_SWIGLU;
     const int per_tile = gated && MODE == PRODUCT_FORWARD ? kLanes / 2 : kLanes;
     const long long cols = MODE == PRODUCT_WGRAD ? p.cols : p.rows;
@@ -988,6 +989,13 @@ int launch(ProductParams &p, cudaStream_t st) {
     p.stages = space / p.stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     p.out_at = (int)(kStageSpace / 1024 * 1024) - out_bytes;
+    if (MODE == PRODUCT_WGRAD) {
+        if (!make_map3(&p.b[0], b, width, p.rows, p.groups, kSubRed)) return EP_ERR_CUDA;
+    } else {
+        const int boxes = widest / cg > 128 ? kBoxes : widest / cg / 16;
+        for (int i = 0; i < boxes; ++i)
+            if (!make_map3(&p.b[i], b, width, p.rows, p.groups, 16u * (i + 1))) return EP_ERR_CUDA;
+    }
     if (!make_out_map(&p.o, p.out, p.out_f32, MODE == PRODUCT_DGRAD && gated ? 2 : 1, p.lanes, cols, p.groups))
         return EP_ERR_CUDA;
     const long long most = (long long)p.lane_tiles * p.groups * ceil_div(cols, p.col_max);
@@ -1071,10 +1079,9 @@ extern "C" int ep_product(const ep_product_t *a, const void *x, const void *w, c
     } else {
         ok = make_map3(&p.a, w, K, N, G, kLanes);
     }
-    for (int b = 0; b < kBoxes && ok; ++b) ok = make_map3(&p.b[b], x, K, a->rows, G, 16u * (b + 1));
     if (!ok) return EP_ERR_CUDA;
     Range range("ep:product");
-    return launch<PRODUCT_FORWARD>(p, static_cast<cudaStream_t>(stream));
+    return launch<PRODUCT_FORWARD>(p, x, a->k, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int ep_product_dgrad(const ep_product_t *a, const void *dy, const void *w, const void *preact,
@@ -1090,11 +1097,9 @@ extern "C" int ep_product_dgrad(const ep_product_t *a, const void *dy, const voi
     p.z = static_cast<const __nv_bfloat16 *>(preact);
     p.out = dx;
     const uint64_t K = a->k, N = a->n, G = a->groups;
-    bool ok = make_map3(&p.a, w, K, N, G, kSubRed);
-    for (int b = 0; b < kBoxes && ok; ++b) ok = make_map3(&p.b[b], dy, N, a->rows, G, 16u * (b + 1));
-    if (!ok) return EP_ERR_CUDA;
+    if (!make_map3(&p.a, w, K, N, G, kSubRed)) return EP_ERR_CUDA;
     Range range("ep:product_dgrad");
-    return launch<PRODUCT_DGRAD>(p, static_cast<cudaStream_t>(stream));
+    return launch<PRODUCT_DGRAD>(p, dy, a->n, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int ep_product_wgrad(const ep_product_t *a, const void *dy, const void *x, int32_t accumulate,
@@ -1117,9 +1122,8 @@ extern "C" int ep_product_wgrad(const ep_product_t *a, const void *dy, const voi
     p.cols = a->n;
     p.accumulate = accumulate;
     p.out = dw;
-    if (!make_map3(&p.a, x, K, a->rows, G, kSubRed) || !make_map3(&p.b[0], dy, N, a->rows, G, kSubRed))
-        return EP_ERR_CUDA;
-    const int rc = launch<PRODUCT_WGRAD>(p, st);
+    if (!make_map3(&p.a, x, K, a->rows, G, kSubRed)) return EP_ERR_CUDA;
+    const int rc = launch<PRODUCT_WGRAD>(p, dy, a->n, st);
     if (rc != EP_OK || !dbias) return rc;
     return launch_row_sums(dy, a->counts, a->groups, a->rows, a->n, p.out_f32, accumulate, dbias, st) ==
                    cudaSuccess

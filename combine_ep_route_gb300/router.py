@@ -15,16 +15,16 @@ _TYPES = {torch.bfloat16: L.EP_BF16, torch.float32: L.EP_F32}
 
 
 def _args(logits: torch.Tensor, top_k: int, score: str, renormalize: bool, scale: float) -> L.EpTopkC:
-    if score not in _SCORES:
+    code, kind, E = _SCORES.get(score), _TYPES.get(logits.dtype), logits.shape[-1] if logits.dim() else 0
+    if (code is not None and kind is not None and logits.is_cuda and logits.is_contiguous()
+            and 1 <= top_k <= E <= L.EP_MAX_E and top_k <= L.EP_MAX_TOPK):
+        return L.EpTopkC(logits.numel() // E, E, top_k, code, 1 if renormalize else 0, kind, scale)
+    if code is None:
         raise ValueError(f"score: want one of {sorted(_SCORES)}, got {score!r}")
-    if logits.dtype not in _TYPES or logits.dim() < 1 or not logits.is_contiguous() or not logits.is_cuda:
+    if kind is None or not logits.dim() or not logits.is_contiguous() or not logits.is_cuda:
         raise ValueError(f"logits: want contiguous bfloat16 or float32 [..., E] on a CUDA device, got {logits.dtype} "
                          f"{tuple(logits.shape)} on {logits.device} (contiguous={logits.is_contiguous()})")
-    E = logits.shape[-1]
-    if not 1 <= E <= L.EP_MAX_E or not 1 <= top_k <= min(E, L.EP_MAX_TOPK):
-        raise ValueError(f"want 1..{L.EP_MAX_E} experts and top_k in 1..min(E, {L.EP_MAX_TOPK}), got E={E}, top_k={top_k}")
-    return L.EpTopkC(logits.numel() // E, E, top_k, _SCORES[score], 1 if renormalize else 0,
-                     _TYPES[logits.dtype], scale)
+    raise ValueError(f"want 1..{L.EP_MAX_E} experts and top_k in 1..min(E, {L.EP_MAX_TOPK}), got E={E}, top_k={top_k}")
 
 
 def route_topk(logits: torch.Tensor, top_k: int, *, score: str = "softmax", renormalize: bool = True,
