@@ -2,7 +2,8 @@
 
 All W expert-parallel ranks live as blocks of one GPU's memory; the kernels
 (sm_103a) sit behind the C-ABI in ``include/ep.h`` and this package binds it
-for PyTorch tensors. See ``ep.EpContext``.
+for PyTorch tensors. See ``ep.EpContext``; ``product`` and ``router`` hold the operators of
+the layer around it (experts' and linear products with their gradients, top-k routing).
 """
 from .ep import (EpConfig, EpContext, DispatchOut, AgrsBuffers, agrs, alloc_agrs_buffers,  # noqa: F401
                  capacities, workspace_bytes)
