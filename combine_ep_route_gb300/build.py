@@ -1,6 +1,6 @@
 """Build the CUDA library ``libep.so`` (sm_103a) in-tree.
 
-Each ``csrc/*.cu`` translation unit is compiled in parallel with nvcc, then
+Each ``csrc/*.cu`` and ``csrc/layers/*.cu`` translation unit is compiled in parallel with nvcc, then
 linked into ``combine_ep_route_gb300/libep.so`` (CUDA runtime linked
 statically, so the library needs only the NVIDIA GPU driver at run time).
 """
@@ -32,7 +32,7 @@ def _nvcc() -> str:
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "layers", "*.cu")))
 
 
 def _stale() -> bool:
@@ -40,7 +40,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + [HEADER])
+            + glob.glob(os.path.join(CSRC, "layers", "*.cuh")) + [HEADER])
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -342,22 +342,6 @@ inline cudaError_t ensure_dyn_smem(const void *fn, size_t bytes) {
     }));
 }
 
-// A launch whose set-up may overlap the end of the kernel before it on the stream; the
-// kernel itself calls pdl_wait() before its first access to global memory.
-template <class... Params, class... Args>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int block, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)block);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
-}
-
 // Each returns the cudaError_t of the launch.
 cudaError_t launch_route(const RouteParams &p, cudaStream_t st);
 size_t route_smem_bytes(int n_ctr, int top_k);
@@ -381,8 +365,5 @@ cudaError_t launch_scale_move(const ScaleMoveParams &p, int grid, cudaStream_t s
 // both stages as one-wave grids over num_sms SMs
 cudaError_t launch_combine_two_stage(const PartialParams &a, const GatherParams &b, bool out_f32,
                                      int num_sms, cudaStream_t st);
-// out[g][c] (+)= the sum over group g's rows in use of src[g][row][c] (bf16), n columns
-cudaError_t launch_row_sums(const void *src, const int32_t *counts, int groups, int rows, int n,
-                            bool out_f32, bool accumulate, void *out, cudaStream_t st);
 
 }  // namespace ep

@@ -7,7 +7,7 @@
 
 #include <cuda_bf16.h>
 
-#include "ep_internal.cuh"
+#include "launch.cuh"
 
 namespace ep {
 

@@ -5,7 +5,7 @@
 // expert. The weights need the chosen logits only, except for the softmax over all
 // experts, which adds one sum. Instructions bound it, not memory: a token's 256 bf16
 // logits are 512 bytes.
-#include "ep_internal.cuh"
+#include "launch.cuh"
 
 #include <cfloat>
 #include <cuda_bf16.h>

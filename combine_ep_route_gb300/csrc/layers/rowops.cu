@@ -1,7 +1,7 @@
 // rowops.cu -- row-wise companions of the products: the bias gradient (a sum of
 // rows per group) and the gradient through an activation that no product follows.
 // Both read each byte once and are bound by HBM.
-#include "ep_internal.cuh"
+#include "launch.cuh"
 
 #include <cooperative_groups.h>
 #include <nvtx3/nvToolsExt.h>

@@ -5,7 +5,7 @@
 
 #include <cuda.h>
 
-#include "ep_internal.cuh"
+#include "launch.cuh"
 
 namespace ep {
 
