@@ -48,9 +48,9 @@ constexpr int kMaxStages = 12;
 constexpr int kABytes = kLanes * kSubRed * 2;
 constexpr int kChunkBytes = kSubRed * 128;   // MN-major: 64 reduction lines of 64 elements
 constexpr int kTmemCols = 512;       // two accumulators of 256 columns
-constexpr int kMaxSplit = 4;            // clusters of four fill 144 of 152 SMs, of eight 120
-constexpr int kBand = 8;              // lane tiles of a band (see find_tile)
-constexpr uint32_t kSleepNs = 1000000;       // of one attempt at a wait
+constexpr int kMaxSplit = 4;         // clusters of four fill 144 of 152 SMs, of eight 120
+constexpr int kBand = 8;             // lane tiles of a band (see find_tile)
+constexpr uint32_t kSleepNs = 1000000;   // of one attempt at a wait
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 struct Shared {
@@ -100,11 +100,11 @@ struct Tile {
 };
 
 // Column tiles of a group are of equal width (a multiple of 16 per CTA), so 260
-// rows make two tiles of 144 and 116 and not of 256 and 4.
+// rows make two tiles of 144 and 116 (of a pair: 160 and 100) and not of 256 and 4.
 template <int MODE>
 __device__ __forceinline__ int col_tiles(const ProductParams &p, int count) {
     const int cols = MODE == PRODUCT_WGRAD ? p.cols : count;
-    return (cols + p.col_max - 1) / p.col_max;
+    return cols > 0 ? (cols - 1) / p.col_max + 1 : 0;
 }
 
 // a / b for 0 <= a, 0 < b: by reciprocal and correction where fp32 holds a exactly (an
@@ -139,7 +139,7 @@ __device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *
         w.ct = sh->first[w.g + 1] - sh->first[w.g];
         const int count = sh->count[w.g];
         w.all = MODE == PRODUCT_WGRAD ? p.cols : count;
-        w.width = ((w.ct == 1 ? w.all : quotient(w.all + w.ct - 1, w.ct)) + kUnit - 1) / kUnit * kUnit;
+        w.width = ((w.ct == 1 ? w.all : quotient(w.all - 1, w.ct) + 1) + kUnit - 1) / kUnit * kUnit;
         w.red = MODE == PRODUCT_WGRAD ? count : p.red;
         w.blocks = (w.red + p.block_red - 1) >> p.block_shift;
     }
@@ -457,7 +457,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int per_cluster = CG == 2 ? 2 : p.split;
     const int t0 = blockIdx.x / per_cluster, t_step = gridDim.x / per_cluster;
 
-    pdl_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(&sh->full[s], 2 * CG);   // an arrival per operand and CTA
@@ -476,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     if (warp == 3) tmem_alloc<CG>(&sh->tmem, kTmemCols);
     pdl_wait();   // nothing above reads or writes global memory
+    pdl_launch_dependents();
     for (int g = threadIdx.x; g < p.groups; g += kThreads)
         sh->count[g] = p.counts ? max(0, min(p.counts[g], p.rows)) : p.rows;
     __syncthreads();
@@ -999,7 +999,7 @@ int launch(ProductParams &p, const void *b, int width, cudaStream_t st) {
     if (!make_out_map(&p.o, p.out, p.out_f32, MODE == PRODUCT_DGRAD && gated ? 2 : 1, p.lanes, cols, p.groups))
         return EP_ERR_CUDA;
     const long long most = (long long)p.lane_tiles * p.groups * ceil_div(cols, p.col_max);
-    if (most >= (1LL << 31)) return EP_ERR_INVALID_ARG;
+    if (most >= (1LL << 30)) return EP_ERR_INVALID_ARG;   // tile numbers stay within int
     const long long room = p.split > 1 ? most : sms / cg;
     const int clusters = (int)(most < room ? most : room);
     // whether the epilogue reads from memory: residual, pre-activations, output added to

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) topk_kernel(const TopkParams p) {
     for (int i = 0; i < N; ++i) {
         const int e = i * 32 + lane;
         key[i] = order_key(z[i]);
-        if (p.bias && e < p.E && key[i]) key[i] = order_key(z[i] + __ldg(p.bias + e));
+        if (p.bias && e < p.E && key[i]) key[i] = order_key(z[i] + p.bias[e]);
         z[i] = usable(z[i]);
     }
     float2 all = make_float2(0.f, 1.f);

@@ -498,7 +498,8 @@ int ep_agrs(const ep_config_t *cfg, const int32_t *num_tokens, const void *a1,
 
 typedef struct ep_product {
     int32_t groups;    /* weights (experts), 1..EP_MAX_E; 1 for a dense product */
-    int32_t rows;      /* row slots per group (expert_cap), >= 0; groups * rows < 2^31 */
+    int32_t rows;      /* row slots per group (expert_cap), >= 0; groups * rows < 2^31, and
+                          rows * k, rows * n, n * k < 2^36 */
     int32_t k, n;      /* columns of x, columns of the product; multiples of 8, <= 2^24 */
     int32_t act;       /* EP_ACT_*; EP_ACT_NONE for ep_product_wgrad */
     int32_t out_dtype; /* EP_BF16 or EP_F32: the type of out / dx / dw and dbias */
