@@ -58,8 +58,10 @@ struct Shared {
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
-    int count[EP_MAX_E];             // rows in use per group
-    int first[EP_MAX_E + 1];         // column tiles before each group
+    // the groups in the order they are worked on
+    int count[EP_MAX_E];             // rows in use
+    int first[EP_MAX_E + 1];         // column tiles before it
+    uint16_t group[EP_MAX_E];        // which it is
 };
 
 constexpr size_t kSmemMax = 227 * 1024;
@@ -118,10 +120,54 @@ __device__ __forceinline__ int quotient(int a, int b) {
     return q;
 }
 
+// Columns of each of ct tiles over `all` > 0.
+template <int CG>
+__device__ __forceinline__ int tile_width(int all, int ct) {
+    constexpr int kUnit = 16 * CG;
+    return ((ct == 1 ? all : quotient(all - 1, ct) + 1) + kUnit - 1) / kUnit * kUnit;
+}
+
+// Reads the groups' counts and puts the groups in order, the dearest tiles first (the
+// widest, or of a weight gradient the longest), so that the last round, which not every
+// SM takes part in, is a cheap one: 64 experts' input gradient 466 -> 452 us, 128 experts'
+// gated product 1669 -> 1615, 64 experts of a decode batch 99.1 -> 99.6. A group's place
+// is the number of groups ahead of it; with more groups than threads the order matters
+// little and stays. Called by every thread, ends in a barrier.
+template <int MODE, int CG>
+__device__ __forceinline__ void order_groups(const ProductParams &p, Shared *sh) {
+    const int own = threadIdx.x;
+    if (p.groups > kThreads || !p.counts) {
+        for (int g = own; g < p.groups; g += kThreads) {
+            sh->count[g] = p.counts ? max(0, min(p.counts[g], p.rows)) : p.rows;
+            sh->group[g] = (uint16_t)g;
+        }
+        __syncthreads();
+        return;
+    }
+    int count = 0, key = 0;
+    if (own < p.groups) {
+        count = max(0, min(p.counts[own], p.rows));
+        key = MODE == PRODUCT_WGRAD || count == 0 ? count : tile_width<CG>(count, col_tiles<MODE>(p, count));
+        sh->first[own] = key;
+    }
+    __syncthreads();
+    if (own < p.groups) {
+        int ahead = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const int other = sh->first[g];
+            ahead += other > key || (other == key && g < own);
+        }
+        sh->count[ahead] = count;
+        sh->group[ahead] = (uint16_t)own;
+    }
+    __syncthreads();
+}
+
 // A role's place in the launch's tiles, which it visits in rising order: the current
 // group, the first tile after it, and what its tiles have in common.
 struct Walk {
-    int g = -1, begin = 0, end = 0;   // the group's tiles [begin, end)
+    int at = -1, begin = 0, end = 0;  // the group's place, its tiles [begin, end)
+    int g = 0;
     int ct = 0, all = 0, width = 0;   // column tiles, columns, columns of a tile
     int red = 0, blocks = 0;
 };
@@ -132,14 +178,15 @@ __device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *
     constexpr int kPer = GATED && MODE == PRODUCT_FORWARD ? kLanes / 2 : kLanes;
     if (t >= w.end) {
         do {
-            ++w.g;
+            ++w.at;
             w.begin = w.end;
-            w.end = sh->first[w.g + 1] * p.lane_tiles;
+            w.end = sh->first[w.at + 1] * p.lane_tiles;
         } while (t >= w.end);
-        w.ct = sh->first[w.g + 1] - sh->first[w.g];
-        const int count = sh->count[w.g];
+        w.g = sh->group[w.at];
+        w.ct = sh->first[w.at + 1] - sh->first[w.at];
+        const int count = sh->count[w.at];
         w.all = MODE == PRODUCT_WGRAD ? p.cols : count;
-        w.width = ((w.ct == 1 ? w.all : quotient(w.all - 1, w.ct) + 1) + kUnit - 1) / kUnit * kUnit;
+        w.width = tile_width<CG>(w.all, w.ct);
         w.red = MODE == PRODUCT_WGRAD ? count : p.red;
         w.blocks = (w.red + p.block_red - 1) >> p.block_shift;
     }
@@ -476,9 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     if (warp == 3) tmem_alloc<CG>(&sh->tmem, kTmemCols);
     pdl_wait();   // nothing above reads or writes global memory
     pdl_launch_dependents();
-    for (int g = threadIdx.x; g < p.groups; g += kThreads)
-        sh->count[g] = p.counts ? max(0, min(p.counts[g], p.rows)) : p.rows;
-    __syncthreads();
+    order_groups<MODE, CG>(p, sh);
     if (warp == 0) {   // exclusive prefix of the groups' column tiles
         int base = 0;
         for (int g0 = 0; g0 < p.groups; g0 += 32) {
