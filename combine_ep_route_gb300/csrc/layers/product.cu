@@ -45,10 +45,11 @@ constexpr int kLanes = 128;          // accumulator lanes of a CTA
 constexpr int kColMax = 256;         // accumulator columns, at most
 constexpr int kSubRed = 64;          // reduction elements of a sub-block: one 128-byte swizzled line
 constexpr int kMaxStages = 12;
-constexpr int kABytes = kLanes * kSubRed * 2;
 constexpr int kChunkBytes = kSubRed * 128;   // MN-major: 64 reduction lines of 64 elements
 constexpr int kTmemCols = 512;       // two accumulators of 256 columns
 constexpr int kMaxSplit = 4;         // clusters of four fill 144 of 152 SMs, of eight 120
+constexpr int kNarrowCols = 32;      // most columns for narrow lane tiles (see plan_dense)
+constexpr float kNarrowSubUs = .08f;  // least time of a sub-block
 constexpr int kBand = 8;             // lane tiles of a band (see find_tile)
 constexpr uint32_t kSleepNs = 1000000;   // of one attempt at a wait
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -172,10 +173,9 @@ struct Walk {
     int red = 0, blocks = 0;
 };
 
-template <int MODE, bool GATED, int CG>
+template <int MODE, int CG>
 __device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *sh, int t, uint32_t rank, Walk &w) {
     constexpr int kUnit = 16 * CG;
-    constexpr int kPer = GATED && MODE == PRODUCT_FORWARD ? kLanes / 2 : kLanes;
     if (t >= w.end) {
         do {
             ++w.at;
@@ -199,7 +199,7 @@ __device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *
     const int lt = band * kBand + in_band - c * high;
     Tile x;
     x.g = w.g;
-    x.lane0 = (CG == 1 ? lt : lt * 2 + (int)rank) * kPer;
+    x.lane0 = (CG == 1 ? lt : lt * 2 + (int)rank) * p.lane_step;
     x.col0 = c * w.width;
     x.cols = min(w.width, w.all - x.col0);
     x.n_mma = (x.cols + kUnit - 1) / kUnit * kUnit;
@@ -261,12 +261,14 @@ struct Place {
         if (MODE == PRODUCT_FORWARD && GATED) {
             const int il = p.interleave;   // 8 or 16
             up = lane & il;
-            f = x.lane0 + quad * 16 + (il == 8 ? (lane >> 4) * 8 : 0) + (lane & (il - 1) & ~1);
+            f = quad * 16 + (il == 8 ? (lane >> 4) * 8 : 0) + (lane & (il - 1) & ~1);
         } else {
             up = false;
-            f = x.lane0 + quad * 32 + (lane & ~1);
+            f = quad * 32 + (lane & ~1);
         }
-        ok = f < p.lanes;
+        ok = f < p.lane_step;   // lanes past a narrow tile hold nothing
+        f += x.lane0;
+        ok = ok && f < p.lanes;
     }
     __device__ __forceinline__ int column(int i) const {
         return MODE == PRODUCT_FORWARD && GATED ? 4 * i + (up ? 2 : 0) + odd : 2 * i + odd;
@@ -485,7 +487,7 @@ __device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const flo
                 v[i].x += r.x, v[i].y += r.y;
             }
         }
-        if (n == 32)
+        if (n == 32 && (MODE != PRODUCT_FORWARD || p.lane_step == kLanes))
             tile_pairs(p, v, at, tile, 0);
         else
             store_pairs(p, v, row0, n, at, L, at.f);
@@ -558,11 +560,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const bool lanes = warp == 0;
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, walk);
+            const Tile x = find_tile<MODE, CG>(p, sh, t, rank, walk);
             const int own_cols = x.n_mma / CG;
             const int col0 = x.col0 + (CG == 2 ? (int)rank * own_cols : 0);
             const int chunks = (own_cols + 63) / 64;
-            const uint32_t sub_bytes = lanes ? kABytes : kMnB ? chunks * kChunkBytes : own_cols * 128;
+            const uint32_t sub_bytes = lanes ? p.a_bytes : kMnB ? chunks * kChunkBytes : own_cols * 128;
             const int lane_block = x.lane0 / (GATED && MODE == PRODUCT_FORWARD ? p.interleave : 1);
             int lo, hi;
             my_blocks(p, x, rank, lo, hi);
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                         bar = smem_u32(local);
                         mbar_arrive_expect_tx(local, sub_bytes * subs);
                     }
-                    uint8_t *dst = stages + (size_t)s * p.stage_bytes + (lanes ? 0 : kABytes);
+                    uint8_t *dst = stages + (size_t)s * p.stage_bytes + (lanes ? 0 : p.a_bytes);
                     for (int sub = 0; sub < subs; ++sub, dst += p.sub_bytes) {
                         const int r = r0 + sub * kSubRed;
                         if (lanes) {
@@ -623,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         // ---- MMA: one thread issues the steps of 16 of each block
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, walk);
+            const Tile x = find_tile<MODE, CG>(p, sh, t, rank, walk);
             int lo, hi;
             my_blocks(p, x, rank, lo, hi);
             if (lo == hi) continue;
@@ -648,8 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     int left = x.red - kb * p.block_red;
                     for (int sub = 0; sub < p.subs && left > 0; ++sub, sa += p.sub_bytes, left -= kSubRed) {
                         const uint64_t da = kMnA ? smem_desc(sa, kChunkBytes, 1024) : smem_desc(sa, 16, 1024);
-                        const uint64_t db = kMnB ? smem_desc(sa + kABytes, kChunkBytes, 1024)
-                                                 : smem_desc(sa + kABytes, 16, 1024);
+                        // (of a narrow tile the MMA reads on past its rows, within shared memory,
+                        // for lanes nobody looks at)
+                        const uint64_t db = kMnB ? smem_desc(sa + p.a_bytes, kChunkBytes, 1024)
+                                                 : smem_desc(sa + p.a_bytes, 16, 1024);
                         constexpr uint32_t kStepA = (kMnA ? 2048 : 32) / 16, kStepB = (kMnB ? 2048 : 32) / 16;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -670,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         uint32_t used = 0;   // a bit per stage: parity of its next use here
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, walk);
+            const Tile x = find_tile<MODE, CG>(p, sh, t, rank, walk);
             int lo, hi;
             my_blocks(p, x, rank, lo, hi);
             const int left = x.red % kSubRed;
@@ -720,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         };
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t, rank, walk);
+            const Tile x = find_tile<MODE, CG>(p, sh, t, rank, walk);
             int lo, hi;
             my_blocks(p, x, rank, lo, hi);
             if (p.split == 1 && lo == hi && MODE == PRODUCT_WGRAD && p.accumulate) continue;
@@ -816,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         if (t0 < total && warp >= 4) {
             const int quad = warp % 4, half = (warp - 4) / 4;
             walk = Walk();
-            const Tile x = find_tile<MODE, GATED, CG>(p, sh, t0, rank, walk);
+            const Tile x = find_tile<MODE, CG>(p, sh, t0, rank, walk);
             const Place<MODE, GATED> at(p, x, quad, lane);
             const size_t row0 = (size_t)x.g * (MODE == PRODUCT_WGRAD ? p.cols : p.rows) + x.col0;
             float2 bias = make_float2(0.f, 0.f);
@@ -938,13 +942,14 @@ constexpr long long ceil_div(long long a, long long b) { return (a + b - 1) / b;
 // How a product is cut: CTAs per MMA, widest column tile, CTAs that share a tile's reduction.
 struct Plan {
     int cg, col_max, split;
+    int lane_step;   // 0 = full lane tiles
 };
 
 // Ragged groups, whose row counts the host does not know: pairs of CTAs where one tile
 // per group and lane tile, or full groups, fill the GPU; single CTAs otherwise.
 Plan plan_ragged(long long lane_tiles, long long groups, long long cols, int sms) {
     const long long pairs = ceil_div(lane_tiles, 2) * groups * ceil_div(cols, kColMax);
-    return {lane_tiles > 1 && 2 * pairs >= sms ? 2 : 1, kColMax, 1};
+    return {lane_tiles > 1 && 2 * pairs >= sms ? 2 : 1, kColMax, 1, 0};
 }
 
 // Dense products: the cut with the least estimated time. A round (one tile on every SM)
@@ -956,11 +961,19 @@ Plan plan_ragged(long long lane_tiles, long long groups, long long cols, int sms
 // Measured against pairs of full tiles where those fill the GPU and single CTAs otherwise:
 // 512 x 7168 x 4096 33.8 -> 28.5 us, 1024 x 4096 x 4096 29.7 -> 27.2, 3000 x 4096 x 1024
 // 27.6 -> 22.6, 1024 x 7168 x 7168 78 -> 79.
-Plan plan_dense(long long lane_tiles, long long groups, long long cols, long long red, int sms) {
+//
+// Few columns on many features (a decoding step's forward product) leave the weight's bytes
+// as the floor. There lane tiles may be narrower than the accumulator, so that one round
+// covers the SMs evenly without a join: `narrow` is 1, or 2 for a gated product's two rows
+// per feature, or 0. 7 x 7168 x 7168: 24.8 -> 22.5 us, 16 x 2048 x 7168 10.7 -> 10.5,
+// 16 x 4096 x 4096 13.3 -> 13.7; at 64 rows it no longer pays (23.5 -> 23.9).
+Plan plan_dense(long long lane_tiles, long long groups, long long cols, long long red, long long lanes, int narrow,
+                int sms) {
     static const float kCost[2][8] = {{.51f, .54f, .65f, .73f, .88f, .91f, 1.05f, 1.19f},
                                       {.46f, .47f, .51f, .58f, .75f, .78f, .91f, 1.f}};
     const float blocks = (float)ceil_div(red, kSubRed);
-    Plan best = {1, kColMax, 1};
+    const float dram_us = (float)(groups * lanes * (narrow > 1 ? 2 : 1) * red) * 2.f / 6.4e6f;
+    Plan best = {1, kColMax, 1, 0};
     float best_us = 0.f;
     for (int cg = 1; cg <= 2; ++cg) {
         if (cg == 2 && lane_tiles < 2) break;
@@ -971,11 +984,22 @@ Plan plan_dense(long long lane_tiles, long long groups, long long cols, long lon
                 // (clusters of four fit on all but a few SMs: 144 of 152)
                 if (split > 1 && (split * tiles > (split == 4 ? sms - sms / 16 : sms) || blocks < 8 * split)) break;
                 const float rounds = split > 1 ? 1.f : (float)ceil_div(tiles, slots);
-                const float us = rounds * kCost[cg - 1][w - 1] * .363f * blocks / split + (split > 1 ? 2.f : 0.f) +
-                                 2.3f / 8 * w / split;
-                if (best_us == 0.f || us < best_us) best_us = us, best = {cg, 32 * w, split};
+                const float sums = rounds * kCost[cg - 1][w - 1] * .363f * blocks / split;
+                const float us = (sums > dram_us ? sums : dram_us) + (split > 1 ? 2.f : 0.f) + 2.3f / 8 * w / split;
+                if (best_us == 0.f || us < best_us) best_us = us, best = {cg, 32 * w, split, 0};
             }
             if (32 * w >= cols) break;
+        }
+    }
+    if (narrow && cols <= kNarrowCols) {
+        const long long step = ceil_div(ceil_div(groups * lanes, sms), 16) * 16;   // one round
+        const long long rows = step * narrow;
+        if (rows < kLanes) {
+            const float sub = (float)(rows + ceil_div(cols, 16) * 16) * 128.f / 95e3f;   // at 95 GB/s a CTA
+            const float rounds = (float)ceil_div(groups * ceil_div(lanes, step), sms);
+            const float sums = (sub > kNarrowSubUs ? sub : kNarrowSubUs) * blocks * rounds;
+            const float us = (sums > dram_us ? sums : dram_us) + 2.3f / 8 * ceil_div(cols, 32);
+            if (us < best_us) best = {1, (int)(ceil_div(cols, 32) * 32), 1, (int)step};
         }
     }
     return best;
@@ -1003,37 +1027,59 @@ int launch(const ProductParams &p, int clusters, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, product_kernel<MODE, GATED, CG, SIDE>, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 
-// Plans and launches; `b` is the column operand, [groups][rows][width].
+// Plans and launches: `a` is the lane operand (a weight, or wgrad's x), `b` the column
+// operand, [groups][rows][width].
 template <int MODE>
-int launch(ProductParams &p, const void *b, int width, cudaStream_t st) {
-    const bool gated = p.act == EP_ACT_SWIGLU;
-    const int per_tile = gated && MODE == PRODUCT_FORWARD ? kLanes / 2 : kLanes;
+int launch(ProductParams &p, const void *a, const void *b, int width, cudaStream_t st) {
+    const bool gated = p.act == EP_ACT_SWIGLU, two = gated && MODE == PRODUCT_FORWARD;
+    const int full_step = two ? kLanes / 2 : kLanes;
     const long long cols = MODE == PRODUCT_WGRAD ? p.cols : p.rows;
     int sms = 0;
     if (sm_count(&sms) != cudaSuccess) return EP_ERR_CUDA;
     p.wait_limit_ns = kWaitLimitNs;
-    const int lane_tiles = (p.lanes + per_tile - 1) / per_tile;
-    const Plan plan = p.counts ? plan_ragged(lane_tiles, p.groups, cols, sms)
-                               : plan_dense(lane_tiles, p.groups, cols, MODE == PRODUCT_WGRAD ? p.rows : p.red, sms);
+    const long long full_tiles = ceil_div(p.lanes, full_step);
+    const Plan plan = p.counts ? plan_ragged(full_tiles, p.groups, cols, sms)
+                               : plan_dense(full_tiles, p.groups, cols, MODE == PRODUCT_WGRAD ? p.rows : p.red, p.lanes,
+                                            MODE != PRODUCT_FORWARD ? 0 : two ? 2 : 1, sms);
     const int cg = plan.cg;
     p.col_max = plan.col_max;
     p.split = plan.split;
-    p.lane_tiles = (int)ceil_div(lane_tiles, cg);
+    p.lane_step = plan.lane_step ? plan.lane_step : full_step;
+    p.lane_tiles = (int)ceil_div(ceil_div(p.lanes, p.lane_step), cg);
+    const int lane_rows = p.lane_step * (two ? 2 : 1);
+    p.a_bytes = lane_rows * kSubRed * 2;
     const int unit = 16 * cg;
     const int widest = (int)(cols < p.col_max ? ceil_div(cols, unit) * unit : p.col_max);
-    p.sub_bytes = kABytes + (MODE == PRODUCT_WGRAD ? (widest / cg + 63) / 64 * kChunkBytes
-                                                   : (widest / cg * 128 + 1023) / 1024 * 1024);
+    p.sub_bytes = p.a_bytes + (MODE == PRODUCT_WGRAD ? (widest / cg + 63) / 64 * kChunkBytes
+                                                     : (widest / cg * 128 + 1023) / 1024 * 1024);
     const int out_bytes = kEpilogueWarps * (p.out_f32 ? 4096 : 2048);
     const int space = (int)(kStageSpace / 1024 * 1024) - out_bytes;
-    // two sub-blocks per stage halve the barrier traffic; one where that leaves fewer than
-    // three stages (8192 x 7168 x 4096: 288 against 305 us; 7 rows: 26.7 against 28.7)
-    p.subs = space / (2 * p.sub_bytes) >= 3 ? 2 : 1;
+    // two sub-blocks per stage (of narrow tiles, four) halve the barrier traffic; one where
+    // that leaves fewer than three stages (8192 x 7168 x 4096: 288 against 305 us; 7 rows:
+    // 26.7 against 28.7)
+    p.subs = plan.lane_step ? 4 : 2;
+    while (p.subs > 1 && space / (p.subs * p.sub_bytes) < 3) p.subs /= 2;
     p.block_red = p.subs * kSubRed;
-    p.block_shift = p.subs == 2 ? 7 : 6;
+    p.block_shift = p.subs == 4 ? 8 : p.subs == 2 ? 7 : 6;
     p.stage_bytes = p.subs * p.sub_bytes;
     p.stages = space / p.stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     p.out_at = (int)(kStageSpace / 1024 * 1024) - out_bytes;
+    const uint64_t L = p.lanes, K = p.red, G = p.groups;
+    bool ok;
+    if (two) {
+        // w [G][gate, up][n][k] read as k x il x (gate, up) x n / il blocks
+        p.interleave = p.lanes % 16 == 0 ? 16 : 8;
+        const uint64_t il = p.interleave;
+        const uint64_t dims[5] = {K, il, 2, L / il, G}, strides[4] = {K, L * K, il * K, 2 * L * K};
+        const uint32_t box[5] = {64, (uint32_t)il, 2, (uint32_t)(p.lane_step / il), 1};
+        ok = make_map(&p.a, a, 5, dims, strides, box);
+    } else if (MODE == PRODUCT_FORWARD) {
+        ok = make_map3(&p.a, a, K, L, G, lane_rows);
+    } else {
+        ok = make_map3(&p.a, a, L, MODE == PRODUCT_DGRAD ? K : p.rows, G, kSubRed);
+    }
+    if (!ok) return EP_ERR_CUDA;
     if (MODE == PRODUCT_WGRAD) {
         if (!make_map3(&p.b[0], b, width, p.rows, p.groups, kSubRed)) return EP_ERR_CUDA;
     } else {
@@ -1104,7 +1150,6 @@ extern "C" int ep_product(const ep_product_t *a, const void *x, const void *w, c
     if (!x || !w || !out || !aligned16(x) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) ||
         !aligned16(out) || !aligned16(preact))
         return EP_ERR_INVALID_ARG;
-    const bool gated = a->act == EP_ACT_SWIGLU;
     ProductParams p = base_params(a);
     p.lanes = a->n;
     p.red = a->k;
@@ -1112,21 +1157,8 @@ extern "C" int ep_product(const ep_product_t *a, const void *x, const void *w, c
     p.residual = static_cast<const __nv_bfloat16 *>(residual);
     p.preact = static_cast<__nv_bfloat16 *>(preact);
     p.out = out;
-    const uint64_t K = a->k, N = a->n, G = a->groups;
-    bool ok;
-    if (gated) {
-        // w [G][gate, up][n][k] read as k x il x (gate, up) x n / il blocks
-        p.interleave = a->n % 16 == 0 ? 16 : 8;
-        const uint64_t il = p.interleave;
-        const uint64_t dims[5] = {K, il, 2, N / il, G}, strides[4] = {K, N * K, il * K, 2 * N * K};
-        const uint32_t box[5] = {64, (uint32_t)il, 2, (uint32_t)(64 / il), 1};
-        ok = make_map(&p.a, w, 5, dims, strides, box);
-    } else {
-        ok = make_map3(&p.a, w, K, N, G, kLanes);
-    }
-    if (!ok) return EP_ERR_CUDA;
     Range range("ep:product");
-    return launch<PRODUCT_FORWARD>(p, x, a->k, static_cast<cudaStream_t>(stream));
+    return launch<PRODUCT_FORWARD>(p, w, x, a->k, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int ep_product_dgrad(const ep_product_t *a, const void *dy, const void *w, const void *preact,
@@ -1141,10 +1173,8 @@ extern "C" int ep_product_dgrad(const ep_product_t *a, const void *dy, const voi
     p.red = a->n;
     p.z = static_cast<const __nv_bfloat16 *>(preact);
     p.out = dx;
-    const uint64_t K = a->k, N = a->n, G = a->groups;
-    if (!make_map3(&p.a, w, K, N, G, kSubRed)) return EP_ERR_CUDA;
     Range range("ep:product_dgrad");
-    return launch<PRODUCT_DGRAD>(p, dy, a->n, static_cast<cudaStream_t>(stream));
+    return launch<PRODUCT_DGRAD>(p, w, dy, a->n, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int ep_product_wgrad(const ep_product_t *a, const void *dy, const void *x, int32_t accumulate,
@@ -1167,8 +1197,7 @@ extern "C" int ep_product_wgrad(const ep_product_t *a, const void *dy, const voi
     p.cols = a->n;
     p.accumulate = accumulate;
     p.out = dw;
-    if (!make_map3(&p.a, x, K, a->rows, G, kSubRed)) return EP_ERR_CUDA;
-    const int rc = launch<PRODUCT_WGRAD>(p, dy, a->n, st);
+    const int rc = launch<PRODUCT_WGRAD>(p, x, dy, a->n, st);
     if (rc != EP_OK || !dbias) return rc;
     return launch_row_sums(dy, a->counts, a->groups, a->rows, a->n, p.out_f32, accumulate, dbias, st) ==
                    cudaSuccess

@@ -25,6 +25,8 @@ struct ProductParams {
     int cols;                 // wgrad: n
     int red;                  // forward: k, dgrad: n (wgrad: the group's rows in use)
     int lane_tiles, col_max;  // lane tiles per group; widest column tile
+    int lane_step;            // output features of a CTA's lane tile
+    int a_bytes;              // a sub-block of its lane operand
     int stages, stage_bytes;  // ring of operand blocks in shared memory,
     int subs, sub_bytes;      // each of this many sub-blocks of 64 reduction elements
     int block_red, block_shift;   // subs * 64, and its logarithm

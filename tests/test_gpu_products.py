@@ -99,6 +99,21 @@ def test_experts_wide_tiles_long_reduction(act):
         assert (out[e, c:] == 7.0).all()
 
 
+@pytest.mark.parametrize("rows", [1, 7, 16, 33, 64])
+@pytest.mark.parametrize("k,n", [(2048, 7168), (712, 4104), (4096, 2056), (7168, 2432)])
+def test_linear_few_rows(rows, k, n):
+    """Few rows on many features: lane tiles narrower than the accumulator."""
+    g = gen(rows + n)
+    for act, dtype in (("none", F32), ("gelu", BF16), ("swiglu", BF16)):
+        wn = 2 * n if act == "swiglu" else n
+        x, w, b, r = normal(g, rows, k), normal(g, wn, k, std=k ** -0.5), normal(g, wn), normal(g, rows, n)
+        z = torch.empty(rows, wn, dtype=BF16, device="cuda")
+        got = ep.linear(x, w, bias=b, act=act, residual=r, out_dtype=dtype, preact=z)
+        y, ey, zz, ez = R.forward(x, w, b, act, r, dtype)
+        close(got, y, ey, act)
+        close(z, zz, ez, act)
+
+
 @pytest.mark.parametrize("rows", [1, 7, 64, 130, 300])
 @pytest.mark.parametrize("k,n", [(4104, 136), (7168, 16), (1000, 3080)])
 def test_linear_long_reduction_few_tiles(rows, k, n):
