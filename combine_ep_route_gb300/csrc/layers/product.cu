@@ -275,21 +275,10 @@ struct Place {
     }
 };
 
-// Has the L2 fetch what the epilogue of a chunk will read, while the product is still
-// being summed: a row per lane.
-template <int MODE, bool GATED>
-__device__ __forceinline__ void prefetch_side(const ProductParams &p, size_t row0, int n, int f, int lane) {
-    if (lane >= n || f >= p.lanes) return;
-    const size_t row = row0 + lane;
-    const uint8_t *at;
-    if (MODE == PRODUCT_FORWARD)
-        at = reinterpret_cast<const uint8_t *>(p.residual + row * p.lanes + f);
-    else if (MODE == PRODUCT_DGRAD)
-        at = reinterpret_cast<const uint8_t *>(p.z + row * (GATED ? 2 : 1) * p.lanes + f);
-    else
-        at = static_cast<const uint8_t *>(p.out) + (row * p.lanes + f) * (p.out_f32 ? 4 : 2);
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
-    if (MODE == PRODUCT_DGRAD && GATED) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 2 * (size_t)p.lanes));
+// Read once: streaming loads, which leave the operands in L2 (gradient through relu,
+// 5001 x 2048 x 4096: 62.1 -> 59.4 us, with no prefetch into L2 beside them).
+__device__ __forceinline__ uint32_t ld_once(const __nv_bfloat16 *ptr) {
+    return __ldcs(reinterpret_cast<const uint32_t *>(ptr));
 }
 
 template <int MODE, bool GATED>
@@ -302,17 +291,17 @@ __device__ __forceinline__ void load_side(const ProductParams &p, size_t row0, i
         const int j = at.column(i);
         if (j >= n) continue;
         if (MODE == PRODUCT_FORWARD) {
-            side.a[i] = ld_pair(p.residual + (row0 + j) * p.lanes + at.f);
+            side.a[i] = ld_once(p.residual + (row0 + j) * p.lanes + at.f);
         } else if (MODE == PRODUCT_DGRAD) {
             const __nv_bfloat16 *z = p.z + (row0 + j) * (GATED ? 2 : 1) * p.lanes + at.f;
-            side.a[i] = ld_pair(z);
-            if (GATED) side.b[i] = ld_pair(z + p.lanes);
+            side.a[i] = ld_once(z);
+            if (GATED) side.b[i] = ld_once(z + p.lanes);
         } else if (p.out_f32) {
-            const float2 v = *reinterpret_cast<const float2 *>(static_cast<const float *>(p.out) +
-                                                               (row0 + j) * p.lanes + at.f);
+            const float2 v = __ldcs(reinterpret_cast<const float2 *>(static_cast<const float *>(p.out) +
+                                                                    (row0 + j) * p.lanes + at.f));
             side.a[i] = __float_as_uint(v.x), side.b[i] = __float_as_uint(v.y);
         } else {
-            side.a[i] = ld_pair(static_cast<const __nv_bfloat16 *>(p.out) + (row0 + j) * p.lanes + at.f);
+            side.a[i] = ld_once(static_cast<const __nv_bfloat16 *>(p.out) + (row0 + j) * p.lanes + at.f);
         }
     }
 }
@@ -738,10 +727,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const int a = n_acc & 1;
             const Segments seg = segments(p, x, hi - lo);
             Side side;
-            if (SIDE && p.split == 1)
-                for (int c = half * 32; c < x.cols; c += 64)
-                    prefetch_side<MODE, GATED>(p, row0 + c, x.cols - c,
-                                               x.lane0 + quad * (MODE == PRODUCT_FORWARD && GATED ? 16 : 32), lane);
             if (SIDE && p.split == 1 && half * 32 < x.cols)
                 load_side(p, row0 + half * 32, min(32, x.cols - half * 32), at, side);
             if (lo < hi) {
