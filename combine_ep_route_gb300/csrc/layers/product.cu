@@ -26,7 +26,8 @@
 // What bounds it: the tensor cores under the power limit for long dense products
 // (1680 TFLOP/s of 1729 sustained by cuBLAS), the weights' bytes for few rows per
 // expert (128 experts of 4096 x 7168 with 16 rows each: 1.135 ms, 6.62 TB/s of the
-// copy's 6.67), and the depth of the ring of stages, three of 64 KB, in between.
+// copy's 6.67). In between, both at once reach the power limit (256 rows each: 1.38 to
+// 1.43 ms at 1.3 GHz), and two stages of 64 KB instead of three cost 15 %.
 #include "product.cuh"
 
 #include <atomic>

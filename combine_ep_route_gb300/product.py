@@ -41,14 +41,14 @@ def _act(act: str) -> int:
 
 
 def _want(t: torch.Tensor, name: str, shape: Tuple[int, ...], dev, dtype=BF16) -> None:
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
         raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
 
 
 def _operands(a: torch.Tensor, b: torch.Tensor, names: Tuple[str, str]) -> None:
     dev = a.device
-    if (a.dtype == BF16 and b.dtype == BF16 and a.is_cuda and b.device == dev and a.is_contiguous()
+    if (a.dtype is BF16 and b.dtype is BF16 and a.is_cuda and b.device == dev and a.is_contiguous()
             and b.is_contiguous()):
         return
     for t, name in ((a, names[0]), (b, names[1])):
@@ -94,14 +94,15 @@ def _split(t: torch.Tensor, name: str, grouped: bool) -> Tuple[int, int, int]:
         raise ValueError(f"{name}: want {'[groups, rows, columns]' if grouped else '[rows, columns]'}, "
                          f"got {tuple(shape)}")
     if grouped:
-        return prod(shape[:-2]), shape[-2], shape[-1]
-    return 1, prod(shape[:-1]), shape[-1]
+        return shape[0] if len(shape) == 3 else prod(shape[:-2]), shape[-2], shape[-1]
+    return 1, shape[0] if len(shape) == 2 else prod(shape[:-1]), shape[-1]
 
 
 def _weight(w: torch.Tensor, groups: int, grouped: bool) -> Tuple[int, int]:
     """(rows, columns) of one weight."""
     shape = w.shape
-    if len(shape) < 2 or (not grouped and len(shape) != 2) or prod(shape[:-2]) != groups:
+    if (len(shape) < 2 or (not grouped and len(shape) != 2)
+            or (shape[0] if len(shape) == 3 else prod(shape[:-2])) != groups):
         raise ValueError(f"w: want {groups} weight(s) [rows, columns], got {tuple(shape)}")
     return shape[-2], shape[-1]
 

@@ -11,6 +11,7 @@ from . import _lib as L
 from .product import _want, stream_of
 
 _SCORES = {"softmax": L.EP_SCORE_SOFTMAX, "sigmoid": L.EP_SCORE_SIGMOID}
+_I32, _F32 = torch.int32, torch.float32
 _TYPES = {torch.bfloat16: L.EP_BF16, torch.float32: L.EP_F32}
 
 
@@ -27,6 +28,11 @@ def _args(logits: torch.Tensor, top_k: int, score: str, renormalize: bool, scale
     raise ValueError(f"want 1..{L.EP_MAX_E} experts and top_k in 1..min(E, {L.EP_MAX_TOPK}), got E={E}, top_k={top_k}")
 
 
+def _chosen(logits: torch.Tensor, a: L.EpTopkC) -> Tuple[int, ...]:
+    """The shape of ids and weights."""
+    return (a.tokens, a.top_k) if logits.dim() == 2 else logits.shape[:-1] + (a.top_k,)
+
+
 def route_topk(logits: torch.Tensor, top_k: int, *, score: str = "softmax", renormalize: bool = True,
                bias: Optional[torch.Tensor] = None, scale: float = 1.0,
                out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
@@ -39,16 +45,15 @@ def route_topk(logits: torch.Tensor, top_k: int, *, score: str = "softmax", reno
     ``top_k`` experts left ends in ids of -1, which dispatch drops.
     """
     a = _args(logits, top_k, score, renormalize, scale)
-    dev, shape = logits.device, logits.shape[:-1] + (top_k,)
+    dev, shape = logits.device, _chosen(logits, a)
     if bias is not None:
-        _want(bias, "bias", (a.E,), dev, torch.float32)
+        _want(bias, "bias", (a.E,), dev, _F32)
     if out is None:
-        ids = torch.empty(shape, dtype=torch.int32, device=dev)
-        weights = torch.empty(shape, dtype=torch.float32, device=dev)
+        ids, weights = torch.empty(shape, dtype=_I32, device=dev), torch.empty(shape, dtype=_F32, device=dev)
     else:
         ids, weights = out
-        _want(ids, "topk_ids", shape, dev, torch.int32)
-        _want(weights, "topk_weights", shape, dev, torch.float32)
+        _want(ids, "topk_ids", shape, dev, _I32)
+        _want(weights, "topk_weights", shape, dev, _F32)
     L.check(L.lib().ep_topk_route(C.byref(a), logits.data_ptr(), None if bias is None else bias.data_ptr(),
                                   ids.data_ptr(), weights.data_ptr(), stream_of(stream, dev)), "ep_topk_route")
     return ids, weights
@@ -62,9 +67,9 @@ def route_topk_backward(dweights: torch.Tensor, logits: torch.Tensor, topk_ids: 
     if topk_ids.dim() < 1:
         raise ValueError("topk_ids: want [..., top_k]")
     a = _args(logits, topk_ids.shape[-1], score, renormalize, scale)
-    dev, shape = logits.device, logits.shape[:-1] + (a.top_k,)
-    _want(topk_ids, "topk_ids", shape, dev, torch.int32)
-    _want(dweights, "dweights", shape, dev, torch.float32)
+    dev, shape = logits.device, _chosen(logits, a)
+    _want(topk_ids, "topk_ids", shape, dev, _I32)
+    _want(dweights, "dweights", shape, dev, _F32)
     if out is None:
         out = torch.empty_like(logits)
     else:
