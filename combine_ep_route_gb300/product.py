@@ -33,6 +33,16 @@ def stream_of(stream: Optional[torch.cuda.Stream], dev: torch.device) -> int:
     return _stream_ptr(stream, dev)
 
 
+def empty(shape: Tuple[int, ...], dtype: torch.dtype, dev: torch.device,
+          stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A new result, of the memory of the stream it is written on: another stream's may still be
+    in use by what that stream has pending."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _act(act: str) -> int:
     code = ACTS.get(act)
     if code is None:
@@ -58,11 +68,11 @@ def _operands(a: torch.Tensor, b: torch.Tensor, names: Tuple[str, str]) -> None:
 
 
 def _out(out: Optional[torch.Tensor], shape: Tuple[int, ...], dtype: Optional[torch.dtype], dev,
-         name: str = "out") -> torch.Tensor:
+         stream: Optional[torch.cuda.Stream], name: str = "out") -> torch.Tensor:
     if out is None:
         if dtype is not None and dtype not in _OUT:
             raise ValueError(f"{name}: want bfloat16 or float32, got {dtype}")
-        return torch.empty(shape, dtype=dtype or BF16, device=dev)
+        return empty(shape, dtype or BF16, dev, stream)
     if dtype is not None and out.dtype != dtype:
         raise ValueError(f"{name}: want {dtype}, got {out.dtype}")
     if out.dtype not in _OUT:
@@ -116,7 +126,7 @@ def _forward(x, w, counts, grouped, bias, act, residual, out, out_dtype, preact,
         raise ValueError(f"w: {tuple(w.shape)} does not fit x {tuple(x.shape)} with act {act!r}")
     n = wn // 2 if code == L.EP_ACT_SWIGLU else wn
     lead = x.shape[:-1]
-    out = _out(out, lead + (n,), out_dtype, dev)
+    out = _out(out, lead + (n,), out_dtype, dev, stream)
     if bias is not None:
         _want(bias, "bias", w.shape[:-1], dev)
     if residual is not None:
@@ -141,7 +151,7 @@ def _dgrad(dy, w, counts, grouped, act, preact, out, out_dtype, status, stream):
         raise ValueError("preact: wanted with an activation, and only then")
     if preact is not None:
         _want(preact, "preact", shape, dev)
-    out = _out(out, shape, out_dtype, dev)
+    out = _out(out, shape, out_dtype, dev, stream)
     a = _args(groups, rows, k, n, code, out, counts, status, dev)
     L.check(L.lib().ep_product_dgrad(C.byref(a), dy.data_ptr(), w.data_ptr(), _ptr(preact), out.data_ptr(),
                                      stream_of(stream, dev)), "ep_product_dgrad")
@@ -158,14 +168,14 @@ def _wgrad(dy, x, counts, grouped, out, out_dtype, accumulate, bias_grad, status
     lead = dy.shape[:-2] if grouped else ()
     if accumulate and out is None:
         raise ValueError("out: wanted with accumulate")
-    out = _out(out, lead + (n, k), out_dtype, dev)
+    out = _out(out, lead + (n, k), out_dtype, dev, stream)
     db = None
     if isinstance(bias_grad, torch.Tensor):
-        db = _out(bias_grad, lead + (n,), out.dtype, dev, "bias_grad")
+        db = _out(bias_grad, lead + (n,), out.dtype, dev, stream, "bias_grad")
     elif bias_grad:
         if accumulate:
             raise ValueError("bias_grad: want a tensor to add to with accumulate")
-        db = torch.empty(lead + (n,), dtype=out.dtype, device=dev)
+        db = empty(lead + (n,), out.dtype, dev, stream)
     a = _args(groups, rows, k, n, L.EP_ACT_NONE, out, counts, status, dev)
     L.check(L.lib().ep_product_wgrad(C.byref(a), dy.data_ptr(), x.data_ptr(), 1 if accumulate else 0,
                                      out.data_ptr(), _ptr(db), stream_of(stream, dev)), "ep_product_wgrad")
@@ -246,7 +256,7 @@ def act_grad(dy: torch.Tensor, preact: torch.Tensor, act: str, *, counts: Option
     groups, rows, n = _split(dy, "dy", counts is not None)
     shape = dy.shape[:-1] + (2 * n if code == L.EP_ACT_SWIGLU else n,)
     _want(preact, "preact", shape, dev)
-    out = _out(out, shape, BF16, dev)
+    out = _out(out, shape, BF16, dev, stream)
     a = _args(groups, rows, n, n, code, out, counts, None, dev)
     L.check(L.lib().ep_act_grad(C.byref(a), dy.data_ptr(), preact.data_ptr(), out.data_ptr(),
                                 stream_of(stream, dev)), "ep_act_grad")

@@ -8,7 +8,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib as L
-from .product import _want, stream_of
+from .product import _want, empty, stream_of
 
 _SCORES = {"softmax": L.EP_SCORE_SOFTMAX, "sigmoid": L.EP_SCORE_SIGMOID}
 _I32, _F32 = torch.int32, torch.float32
@@ -49,7 +49,7 @@ def route_topk(logits: torch.Tensor, top_k: int, *, score: str = "softmax", reno
     if bias is not None:
         _want(bias, "bias", (a.E,), dev, _F32)
     if out is None:
-        ids, weights = torch.empty(shape, dtype=_I32, device=dev), torch.empty(shape, dtype=_F32, device=dev)
+        ids, weights = empty(shape, _I32, dev, stream), empty(shape, _F32, dev, stream)
     else:
         ids, weights = out
         _want(ids, "topk_ids", shape, dev, _I32)
@@ -71,7 +71,7 @@ def route_topk_backward(dweights: torch.Tensor, logits: torch.Tensor, topk_ids: 
     _want(topk_ids, "topk_ids", shape, dev, _I32)
     _want(dweights, "dweights", shape, dev, _F32)
     if out is None:
-        out = torch.empty_like(logits)
+        out = empty(logits.shape, logits.dtype, dev, stream)
     else:
         _want(out, "out", logits.shape, dev, logits.dtype)
     L.check(L.lib().ep_topk_route_backward(C.byref(a), dweights.data_ptr(), logits.data_ptr(), topk_ids.data_ptr(),

@@ -373,8 +373,18 @@ def test_runs_on_a_side_stream_and_in_a_graph():
     out = torch.zeros_like(want)
     side.wait_stream(torch.cuda.current_stream())
     ep.experts_product(x, w, cnt, out=out, stream=side)
+    fresh = [ep.experts_product(x, w, cnt, stream=side), ep.linear(x, w[0], stream=side),
+             *ep.linear_wgrad(x, x, bias_grad=True, stream=side), ep.act_grad(x, x, "relu", stream=side),
+             *ep.route_topk(x[0], 2, stream=side)]
     torch.cuda.current_stream().wait_stream(side)
+    for t in fresh:
+        t.record_stream(torch.cuda.current_stream())
     assert torch.equal(out, want)
+    for e, c in enumerate(cnt.tolist()):
+        assert torch.equal(fresh[0][e, :c], want[e, :c])
+    assert torch.equal(fresh[1], ep.linear(x, w[0]))
+    for a, b in zip(fresh[2:], (*ep.linear_wgrad(x, x, bias_grad=True), ep.act_grad(x, x, "relu"), *ep.route_topk(x[0], 2))):
+        assert torch.equal(a, b)
     graph, out2 = torch.cuda.CUDAGraph(), torch.zeros_like(want)
     with torch.cuda.graph(graph):
         ep.experts_product(x, w, cnt, out=out2)
