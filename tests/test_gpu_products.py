@@ -441,3 +441,45 @@ def test_offsets_past_32_bits():
     for at in (slice(0, 40), slice(rows - 40, rows)):
         want, e, _, _ = R.forward(x[at], w, None, "relu", None, BF16)
         close(y[at], want, e)
+
+
+def test_two_host_threads_on_their_own_streams():
+    """Launches of two threads interleave on the GPU; none disturbs the other's results."""
+    import threading
+    g = gen(41)
+    jobs = []
+    for E, rows, k, n, act in ((24, 200, 264, 520, "swiglu"), (3, 40, 4104, 136, "none")):
+        x, w = normal(g, E, rows, k), normal(g, E, 2 * n if act == "swiglu" else n, k, std=k ** -0.5)
+        cnt = torch.randint(0, rows + 1, (E,), generator=g, device="cuda", dtype=torch.int32)
+        dy = normal(g, E, rows, n)
+        jobs.append((x, w, cnt, dy, act))
+
+    def run(job, stream=None):
+        x, w, cnt, dy, act = job
+        out = torch.zeros(*dy.shape, dtype=BF16, device="cuda")
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        ep.experts_product(x, w, cnt, act=act, out=out, stream=stream)
+        dw = ep.experts_product_wgrad(dy, x, cnt, out_dtype=F32, stream=stream)
+        y = ep.linear(x[0], w[0], act=act, stream=stream)
+        return out, dw, y
+
+    want = [run(j) for j in jobs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def worker(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(25):
+                got = run(jobs[i], s)
+                s.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=60)
+    assert not any(t.is_alive() for t in threads) and not bad
