@@ -26,14 +26,17 @@ constexpr float kLog2E = 1.4426950408889634f;
 
 __device__ __forceinline__ float sigmoid_f(float z) { return rcp_f(1.f + exp2_f(-kLog2E * z)); }
 
-// tanh through one exponential: 1 - 2 / (1 + e^(2u)); the absolute error of a
-// few 2^-24 is what counts, as it is used as 1 + t.
-__device__ __forceinline__ float tanh_f(float u) { return fmaf(-2.f, rcp_f(1.f + exp2_f(2.f * kLog2E * u)), 1.f); }
-
 constexpr float kSqrtHalf = 0.70710678118654752f;     // sqrt(1/2)
 constexpr float kSqrt2OverPi = 0.79788456080286536f;  // sqrt(2/pi)
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;   // 1/sqrt(2 pi)
 constexpr float kGeluCubic = 0.044715f;
+
+// gelu_tanh's factor (1 + tanh u) / 2, u = sqrt(2/pi) (z + c z^3), as the sigmoid of 2u: the
+// same function, but 1 + tanh u cancels below z = -3 (4 % off at -4.5, nothing left at -5),
+// and the sigmoid keeps its relative precision down to the smallest floats. z2 = z * z.
+__device__ __forceinline__ float gelu_tanh_factor(float z, float z2) {
+    return rcp_f(1.f + exp2_f(-2.f * kLog2E * kSqrt2OverPi * z * fmaf(kGeluCubic, z2, 1.f)));
+}
 
 // Phi(z), the normal distribution's, and its density's exponential e^(-z^2 / 2): erfc by
 // formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions (absolute
@@ -62,8 +65,7 @@ __device__ __forceinline__ float act_value(float z, int act) {
             float e;
             return z * normal_cdf(z, e);
         }
-        case EP_ACT_GELU_TANH:
-            return 0.5f * z * (1.f + tanh_f(kSqrt2OverPi * (z + kGeluCubic * z * z * z)));
+        case EP_ACT_GELU_TANH: return z * gelu_tanh_factor(z, z * z);
         default: return z;
     }
 }
@@ -82,9 +84,10 @@ __device__ __forceinline__ float act_slope(float z, int act) {
             return cdf + z * kInvSqrt2Pi * e;
         }
         case EP_ACT_GELU_TANH: {
-            const float t = tanh_f(kSqrt2OverPi * (z + kGeluCubic * z * z * z));
-            return 0.5f * (1.f + t) +
-                   0.5f * z * (1.f - t * t) * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z);
+            // s + z s (1 - s) 2u'. Past |z| = 16 the factor is 0 or 1 to the last digit; z * z
+            // stops there, so that no infinity meets s (1 - s) = 0.
+            const float z2 = fminf(z * z, 256.f), s = gelu_tanh_factor(z, z2);
+            return fmaf(z * (s * (1.f - s)), 2.f * kSqrt2OverPi * fmaf(3.f * kGeluCubic, z2, 1.f), s);
         }
         default: return 1.f;
     }
