@@ -81,3 +81,35 @@ def test_gelu_tanh_of_huge_values():
         assert torch.equal(forward(sign * z, "gelu_tanh", BF16), (sign * z * want).to(BF16))
     nan = torch.tensor([float("nan")], device="cuda", dtype=BF16)
     assert torch.isnan(slope(nan, "gelu_tanh")).all() and torch.isnan(forward(nan, "gelu_tanh", F32)).all()
+
+
+def normal_parts(z):
+    """64-bit (Phi, phi) and the relative error of a tail: fit 3.8e-7, and an exponential whose
+    argument z^2 / 2 is rounded three times."""
+    phi = torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    return 0.5 * torch.erfc(-z * math.sqrt(0.5)), phi, (16 + 3 * z * z) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", (BF16, F32))
+def test_gelu_tail(dtype):
+    z = values(BF16)
+    cdf, _, err = normal_parts(z.to(D))
+    # above zero the tail's error is small beside one
+    err = torch.where(z < 0, err, err * (1 - cdf) + 4 * 2.0 ** -24)
+    fits(forward(z, "gelu", dtype), z.to(D) * cdf, err)
+
+
+def test_gelu_slope_tail():
+    z = values(BF16)
+    z64 = z.to(D)
+    cdf, phi, err = normal_parts(z64)
+    want = cdf + z64 * phi
+    tail = torch.where(z < 0, cdf * err, (1 - cdf) * err + 2 * 2.0 ** -24)
+    fits(slope(z, "gelu"), want, (tail + (z64 * phi).abs() * err + want.abs() * 2.0 ** -23) / want.abs())
+
+
+def test_gelu_of_huge_values():
+    z = torch.tensor([1e3, 3e18, 1e20, 3e38], device="cuda").to(BF16)
+    for sign, want in ((1, 1.0), (-1, 0.0)):
+        assert (slope(sign * z, "gelu") == want).all()
+        assert torch.equal(forward(sign * z, "gelu", BF16), (sign * z * want).to(BF16))
