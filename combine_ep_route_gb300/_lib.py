@@ -36,6 +36,7 @@ EP_FP4X2 = 4
 
 EP_ACT_NONE, EP_ACT_RELU, EP_ACT_SILU, EP_ACT_GELU, EP_ACT_GELU_TANH, EP_ACT_SWIGLU = range(6)
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = range(2)
+EP_BIAS_ON_SCORE = 16
 
 EP_PATH_FUSED = 0
 EP_PATH_SENDBUF = 1

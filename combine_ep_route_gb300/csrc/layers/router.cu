@@ -1,7 +1,7 @@
 // router.cu -- top-k routing of tokens from router logits, and its gradient.
 //
 // One warp per token, the token's logits in registers (expert i * 32 + lane in
-// slot i) as order-preserving integers of logit plus bias. Ties go to the lowest
+// slot i) as order-preserving integers of logit or score plus bias. Ties go to the lowest
 // expert. The weights need the chosen logits only, except for the softmax over all
 // experts, which adds one sum. Instructions and their latency bound it, not memory:
 // 8192 tokens of 256 bf16 logits (4.2 MB) take 7.9 us forward and 4.0 backward, 128
@@ -27,7 +27,7 @@ struct TopkParams {
     const int32_t *ids_in;
     float *weights;
     void *dlogits;
-    int tokens, E, K, score, renormalize;
+    int tokens, E, K, score, renormalize, bias_on_score;
     float scale;
 };
 
@@ -70,10 +70,15 @@ __device__ __forceinline__ float2 softmax_stats(const float (&z)[N]) {
     return make_float2(m, warp_sum(s));
 }
 
+// The score of a logit among all.
+__device__ __forceinline__ float score_of(const TopkParams &p, float z, float2 all) {
+    return p.score == EP_SCORE_SOFTMAX ? expf(z - all.x) / all.y : 1.f / (1.f + expf(-z));
+}
+
 // The unscaled weight of the lane's chosen logit (`on`: the lane holds one).
 __device__ __forceinline__ float weight_of(const TopkParams &p, float z, bool on, float2 all) {
     if (!p.renormalize) {
-        const float w = p.score == EP_SCORE_SOFTMAX ? expf(z - all.x) / all.y : 1.f / (1.f + expf(-z));
+        const float w = score_of(p, z, all);
         return on ? w : 0.f;
     }
     // the chosen scores over their sum, as a softmax of their logarithms: the scores
@@ -106,11 +111,18 @@ __global__ void __launch_bounds__(kThreads) topk_kernel(const TopkParams p) {
     for (int i = 0; i < N; ++i) {
         const int e = i * 32 + lane;
         key[i] = order_key(z[i]);
-        if (p.bias && e < p.E && key[i]) key[i] = order_key(z[i] + p.bias[e]);
+        if (p.bias && !p.bias_on_score && e < p.E && key[i]) key[i] = order_key(z[i] + p.bias[e]);
         z[i] = usable(z[i]);
     }
     float2 all = make_float2(0.f, 1.f);
-    if (p.score == EP_SCORE_SOFTMAX && !p.renormalize) all = softmax_stats(z);
+    if (p.score == EP_SCORE_SOFTMAX && (!p.renormalize || p.bias_on_score)) all = softmax_stats(z);
+    if (p.bias && p.bias_on_score) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = i * 32 + lane;
+            if (e < p.E && key[i]) key[i] = order_key(score_of(p, z[i], all) + p.bias[e]);
+        }
+    }
 
     int rank = p.K, id = -1;   // this lane's choice, if it has one: place and expert
     int n = 0;                 // choices of the row
@@ -274,7 +286,7 @@ int launch_topk(const TopkParams &p, bool bf16, cudaStream_t st) {
 bool topk_params(const ep_topk_t *a, const void *logits, TopkParams &p) {
     if (!a || a->tokens < 0 || a->E < 1 || a->E > EP_MAX_E || a->top_k < 1 || a->top_k > EP_MAX_TOPK ||
         a->top_k > a->E || (a->renormalize != 0 && a->renormalize != 1) ||
-        (a->score != EP_SCORE_SOFTMAX && a->score != EP_SCORE_SIGMOID) ||
+        ((a->score & ~EP_BIAS_ON_SCORE) != EP_SCORE_SOFTMAX && (a->score & ~EP_BIAS_ON_SCORE) != EP_SCORE_SIGMOID) ||
         (a->logits_dtype != EP_BF16 && a->logits_dtype != EP_F32))
         return false;
     p = {};
@@ -282,7 +294,8 @@ bool topk_params(const ep_topk_t *a, const void *logits, TopkParams &p) {
     p.tokens = a->tokens;
     p.E = a->E;
     p.K = a->top_k;
-    p.score = a->score;
+    p.score = a->score & ~EP_BIAS_ON_SCORE;
+    p.bias_on_score = (a->score & EP_BIAS_ON_SCORE) != 0;
     p.renormalize = a->renormalize;
     p.scale = a->scale;
     return true;

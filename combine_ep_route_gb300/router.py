@@ -11,6 +11,7 @@ from . import _lib as L
 from .product import _want, empty, stream_of
 
 _SCORES = {"softmax": L.EP_SCORE_SOFTMAX, "sigmoid": L.EP_SCORE_SIGMOID}
+_BIASED = {"logits": 0, "scores": L.EP_BIAS_ON_SCORE}
 _I32, _F32 = torch.int32, torch.float32
 _TYPES = {torch.bfloat16: L.EP_BF16, torch.float32: L.EP_F32}
 
@@ -34,20 +35,25 @@ def _chosen(logits: torch.Tensor, a: L.EpTopkC) -> Tuple[int, ...]:
 
 
 def route_topk(logits: torch.Tensor, top_k: int, *, score: str = "softmax", renormalize: bool = True,
-               bias: Optional[torch.Tensor] = None, scale: float = 1.0,
+               bias: Optional[torch.Tensor] = None, bias_on: str = "logits", scale: float = 1.0,
                out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
                stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """``(topk_ids int32, topk_weights float32)``, both ``[..., top_k]``, for ``logits`` ``[..., E]``.
 
-    Experts are chosen by ``logits + bias``, largest first, ties to the lowest id; weights are
-    ``scale`` times the score of the unbiased logit, divided by the chosen scores' sum with
-    ``renormalize``. A logit of minus infinity (or NaN) masks its expert; a row with fewer than
-    ``top_k`` experts left ends in ids of -1, which dispatch drops.
+    Experts are chosen by ``logits + bias``, or with ``bias_on="scores"`` by ``score + bias``, largest
+    first, ties to the lowest id; weights are ``scale`` times the score of the unbiased logit, divided by
+    the chosen scores' sum with ``renormalize``. The two choices differ: a correction bias that balances
+    the experts of a sigmoid (or softmax) gate is trained on the scores and needs ``bias_on="scores"``.
+    A logit of minus infinity (or NaN) masks its expert; a row with fewer than ``top_k`` experts left ends
+    in ids of -1, which dispatch drops.
     """
     a = _args(logits, top_k, score, renormalize, scale)
     dev, shape = logits.device, _chosen(logits, a)
+    if bias_on not in _BIASED:
+        raise ValueError(f"bias_on: want one of {sorted(_BIASED)}, got {bias_on!r}")
     if bias is not None:
         _want(bias, "bias", (a.E,), dev, _F32)
+        a.score |= _BIASED[bias_on]
     if out is None:
         ids, weights = empty(shape, _I32, dev, stream), empty(shape, _F32, dev, stream)
     else:

@@ -560,12 +560,13 @@ int ep_act_grad(const ep_product_t *args, const void *dy, const void *preact, vo
 /* ------------------------------------------------------------------ the router */
 #define EP_SCORE_SOFTMAX 0 /* over the E logits of a token */
 #define EP_SCORE_SIGMOID 1 /* of each logit */
+#define EP_BIAS_ON_SCORE 16 /* added to either: the selection bias goes on the score, not on the logit */
 
 typedef struct ep_topk {
     int32_t tokens;       /* rows, >= 0 */
     int32_t E;            /* experts, 1..EP_MAX_E */
     int32_t top_k;        /* 1..min(E, EP_MAX_TOPK) */
-    int32_t score;        /* EP_SCORE_* */
+    int32_t score;        /* EP_SCORE_*, or EP_SCORE_* + EP_BIAS_ON_SCORE */
     int32_t renormalize;  /* 1: the chosen experts' scores are divided by their sum */
     int32_t logits_dtype; /* EP_BF16 or EP_F32 */
     float scale;          /* factor on the weights */
@@ -573,9 +574,11 @@ typedef struct ep_topk {
 
 /*
  * ep_topk_route -- each token's top_k experts and weights, as ep_dispatch takes
- * them. Experts are chosen by logit + bias (rounded to fp32), largest first, ties
- * to the lowest id; weights are scale * score of the unbiased logit. An expert
- * whose logit (or logit + bias) is NaN or minus infinity is never chosen, and a NaN
+ * them. Experts are chosen by logit + bias (with EP_BIAS_ON_SCORE by score + bias, the
+ * scores over all experts; either sum rounded to fp32), largest first, ties to the lowest
+ * id; weights are scale * score of the unbiased logit. The two choices differ: a bias that
+ * was trained to be added to a sigmoid or a probability needs EP_BIAS_ON_SCORE. An expert
+ * whose logit (or biased logit or score) is NaN or minus infinity is never chosen, and a NaN
  * logit takes no part in the softmax; a row with fewer than top_k experts left
  * ends in ids -1 with weight 0.
  *   logits [tokens][E] logits_dtype; bias [E] float or NULL

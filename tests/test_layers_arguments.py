@@ -1,0 +1,22 @@
+"""Arguments of the products and the router on the host: what the entry points take and
+refuse beyond the form of single fields, without a GPU."""
+import ctypes as C
+
+import pytest
+
+from combine_ep_route_gb300 import _lib as L
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from combine_ep_route_gb300 import build
+    build.build()
+    return L.lib()
+
+
+def test_bias_on_score_is_a_flag_of_either_score(lib):
+    for score, want in ((L.EP_SCORE_SOFTMAX, L.EP_OK), (L.EP_SCORE_SIGMOID, L.EP_OK), (2, L.EP_ERR_INVALID_ARG),
+                        (32, L.EP_ERR_INVALID_ARG)):
+        t = C.byref(L.EpTopkC(0, 8, 2, score | L.EP_BIAS_ON_SCORE, 1, L.EP_F32, 1.0))
+        assert lib.ep_topk_route(t, None, None, None, None, None) == want
+        assert lib.ep_topk_route_backward(t, None, None, None, None, None) == want
