@@ -51,9 +51,12 @@ constexpr int kTmemCols = 512;       // two accumulators of 256 columns
 constexpr int kMaxSplit = 4;         // clusters of four fill 144 of 152 SMs, of eight 120
 constexpr int kNarrowCols = 32;      // most columns for narrow lane tiles (see plan_dense)
 constexpr float kNarrowSubUs = .08f;  // least time of a sub-block
+constexpr int kChainF32 = 1024;      // reduction elements summed in one accumulator (see Sums)
+constexpr int kChainBf16 = 16384;
 constexpr int kBand = 8;             // lane tiles of a band (see find_tile)
 constexpr uint32_t kSleepNs = 1000000;   // of one attempt at a wait
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;   // every other wait is for a pass at most
+constexpr uint64_t kBlockNs = 10000;
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages];
@@ -80,15 +83,16 @@ struct Ring {
     }
 };
 
-// A wait of one of the kernel's roles: bounded, and cut short once any role of
-// the CTA has given up.
-__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Shared *sh, const ProductParams &p) {
+// A wait of one of the kernel's roles: bounded (by `more` ns beyond the limit), and cut short
+// once any role of the CTA has given up.
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Shared *sh, const ProductParams &p,
+                                          uint64_t more = 0) {
     if (mbar_try_wait_ns(bar, parity, kSleepNs)) return true;
     const uint64_t t0 = global_ns();
     volatile int *abort = &sh->abort;
     while (!mbar_try_wait_ns(bar, parity, kSleepNs)) {
         if (*abort) return false;
-        if (global_ns() - t0 > p.wait_limit_ns) {
+        if (global_ns() - t0 > p.wait_limit_ns + more) {
             *abort = 1;
             if (p.status) atomicCAS(p.status, 0, EP_ERR_TIMEOUT);
             return false;
@@ -218,16 +222,30 @@ __device__ __forceinline__ void my_blocks(const ProductParams &p, const Tile &x,
     }
 }
 
-// The tensor cores truncate each step's sum to fp32, which a bf16 result hides but an
-// fp32 one shows (relative error 8e-6 after 448 steps, k = 7168). Where a tile's columns
-// leave room, the reduction of an fp32 result goes to several accumulators in turn, added
-// up with rounding in the epilogue: columns apart, blocks each.
-struct Segments {
-    int apart, blocks;
+// The tensor cores truncate each step's sum to fp32, and its terms to the place of the sum's
+// last bits: a chain of steps is off towards zero, and more than in proportion to its length
+// (non-negative terms: 1.7e-6 of the sum after 64 steps, 7.2e-5 after 1024, 3.5e-4 after 4096),
+// where rounded sums err by less than 1e-6 at any length. So a chain ends after p.chain blocks: 64
+// steps for an fp32 result, 1024 for a bf16 one (a twenty-seventh of the least half unit).
+//
+// A pass is what goes to one accumulator before the epilogue takes it. An fp32 result whose
+// columns leave room has several chains side by side in it, added up with rounding by the
+// epilogue. What is longer takes several passes in the same accumulator; the epilogue warps
+// keep the running sums, rounded, in the other, and the MMAs wait meanwhile (fp32 8192 x 7168 x 4096:
+// 271 -> 307 us; a bf16 weight gradient of 65536 rows, 4096 x 2048: 662 -> 664).
+struct Sums {
+    int apart;    // columns between the chains of a pass
+    int chain;    // blocks of a chain
+    int pass;     // blocks of a pass; the tile's, unless it takes several
 };
-__device__ __forceinline__ Segments segments(const ProductParams &p, const Tile &x, int blocks) {
-    const int shift = !p.out_f32 ? 0 : x.n_mma <= 64 ? 2 : x.n_mma <= 128 ? 1 : 0;   // log2 of their number
-    return {kColMax >> shift, (blocks + (1 << shift) - 1) >> shift};
+__device__ __forceinline__ Sums sums_of(const ProductParams &p, const Tile &x, int blocks) {
+    const int shift = !p.out_f32 ? 0 : x.n_mma <= 64 ? 2 : x.n_mma <= 128 ? 1 : 0;   // log2 of the chains
+    int pass = blocks;
+    if (blocks > p.chain << shift) {
+        const int passes = (blocks - 1) / (p.chain << shift) + 1;
+        pass = (blocks - 1) / passes + 1;
+    }
+    return {kColMax >> shift, (pass + (1 << shift) - 1) >> shift, pass};
 }
 
 // Two output features (f, f + 1) of token column j or j + 1: lanes trade with
@@ -540,7 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
     Ring ring;
     Walk walk;
-    uint32_t n_acc = 0;                     // accumulators so far
+    int acc = 0;                            // the accumulator in turn,
+    uint32_t acc_phase = 0;                 // and a bit for each: the phase of its next use
     int issued = 0;                         // producer: blocks so far
     uint32_t on_tail = 0, tail_phase = 0;   // producer, a bit per stage: last load signals tail[], and its phase
     if (warp == 0 || warp == 3) {
@@ -619,45 +638,48 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             int lo, hi;
             my_blocks(p, x, rank, lo, hi);
             if (lo == hi) continue;
-            const int a = n_acc & 1;
-            ok = role_wait(&sh->acc_empty[a], ((n_acc / 2) & 1) ^ 1, sh, p);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            tc_fence_after();
             const uint32_t idesc = mma_idesc(kLanes * CG, x.n_mma, kMnA, kMnB);
-            const Segments seg = segments(p, x, hi - lo);
-            uint32_t d = tmem + a * kColMax;
-            int in_seg = 0;
-            for (int kb = lo; kb < hi; ++kb, ++in_seg, ring.next(p.stages)) {
-                if (in_seg == seg.blocks) in_seg = 0, d += seg.apart;
-                const int s = ring.s;
-                ok = role_wait(&sh->full[s], ring.phase, sh, p);
+            const Sums sums = sums_of(p, x, hi - lo);
+            for (int kb = lo; kb < hi && ok;) {
+                const int end = min(kb + sums.pass, hi);
+                ok = role_wait(&sh->acc_empty[acc], ((acc_phase >> acc) & 1) ^ 1, sh, p);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                if (elect_one()) {
-                    uint32_t sa = smem_u32(stages + (size_t)s * p.stage_bytes);
-                    int left = x.red - kb * p.block_red;
-                    for (int sub = 0; sub < p.subs && left > 0; ++sub, sa += p.sub_bytes, left -= kSubRed) {
-                        const uint64_t da = kMnA ? smem_desc(sa, kChunkBytes, 1024) : smem_desc(sa, 16, 1024);
-                        // (of a narrow tile the MMA reads on past its rows, within shared memory,
-                        // for lanes nobody looks at)
-                        const uint64_t db = kMnB ? smem_desc(sa + p.a_bytes, kChunkBytes, 1024)
-                                                 : smem_desc(sa + p.a_bytes, 16, 1024);
-                        constexpr uint32_t kStepA = (kMnA ? 2048 : 32) / 16, kStepB = (kMnB ? 2048 : 32) / 16;
+                uint32_t d = tmem + acc * kColMax;
+                for (int in_chain = 0; kb < end; ++kb, ++in_chain, ring.next(p.stages)) {
+                    if (in_chain == sums.chain) in_chain = 0, d += sums.apart;
+                    const int s = ring.s;
+                    ok = role_wait(&sh->full[s], ring.phase, sh, p);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        uint32_t sa = smem_u32(stages + (size_t)s * p.stage_bytes);
+                        int left = x.red - kb * p.block_red;
+                        for (int sub = 0; sub < p.subs && left > 0; ++sub, sa += p.sub_bytes, left -= kSubRed) {
+                            const uint64_t da = kMnA ? smem_desc(sa, kChunkBytes, 1024) : smem_desc(sa, 16, 1024);
+                            // (of a narrow tile the MMA reads on past its rows, within shared memory,
+                            // for lanes nobody looks at)
+                            const uint64_t db = kMnB ? smem_desc(sa + p.a_bytes, kChunkBytes, 1024)
+                                                     : smem_desc(sa + p.a_bytes, 16, 1024);
+                            constexpr uint32_t kStepA = (kMnA ? 2048 : 32) / 16, kStepB = (kMnB ? 2048 : 32) / 16;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (left > 16 * i)
-                                mma_bf16<CG>(d, da + kStepA * i, db + kStepB * i, idesc, in_seg > 0 || sub > 0 || i > 0);
+                            for (int i = 0; i < 4; ++i)
+                                if (left > 16 * i)
+                                    mma_bf16<CG>(d, da + kStepA * i, db + kStepB * i, idesc,
+                                                 in_chain > 0 || sub > 0 || i > 0);
+                        }
+                        mma_commit<CG>(&sh->empty[s]);
                     }
-                    mma_commit<CG>(&sh->empty[s]);
+                    __syncwarp();
                 }
+                if (!ok) break;
+                if (elect_one()) mma_commit<CG>(&sh->acc_full[acc]);
                 __syncwarp();
+                acc_phase ^= 1u << acc;
             }
-            if (!ok) break;
-            if (elect_one()) mma_commit<CG>(&sh->acc_full[a]);
-            __syncwarp();
-            ++n_acc;
+            if (sums.pass == hi - lo) acc ^= 1;   // after several passes the next tile goes on in the same
         }
     } else if (warp == 2 && kMnB) {
         // ---- rows at or past the count, in the last block: zero in both operands
@@ -671,7 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             for (int kb = lo; kb < hi; ++kb, ring.next(p.stages)) {
                 if (left == 0 || kb + 1 < x.blocks) continue;
                 const int s = ring.s;
-                ok = role_wait(&sh->tail[s], (used >> s) & 1, sh, p);
+                // (for the whole reduction, so its length counts; a block takes 0.2 to 0.4 us)
+                ok = role_wait(&sh->tail[s], (used >> s) & 1, sh, p, (uint64_t)(hi - lo) * kBlockNs);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 used ^= 1u << s;
                 if (!ok) break;
@@ -712,6 +735,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     mbar_arrive(&sh->acc_empty[a]);
             }
         };
+        auto wait_acc = [&](int a) {
+            const bool full = role_wait(&sh->acc_full[a], (acc_phase >> a) & 1, sh, p);
+            acc_phase ^= 1u << a;
+            const bool all = __all_sync(0xFFFFFFFFu, full);
+            tc_fence_after();
+            return all;
+        };
         bool ok = true;
         for (int t = t0; t < total && ok; t += t_step) {
             const Tile x = find_tile<MODE, CG>(p, sh, t, rank, walk);
@@ -725,52 +755,84 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 bias = unpack_bf16x2(ld_pair(p.bias + (size_t)x.g * (GATED ? 2 : 1) * p.lanes +
                                              (at.up ? p.lanes : 0) + at.f));
             tile.lane = x.lane0 + quad * 32, tile.group = x.g;
-            const int a = n_acc & 1;
-            const Segments seg = segments(p, x, hi - lo);
+            const Sums sums = sums_of(p, x, hi - lo);
+            const uint32_t quad_lanes = (uint32_t)(quad * 32) << 16;
+            uint32_t at_acc = tmem + acc * kColMax + quad_lanes;   // where the sums are read,
+            int chain = sums.chain;                                // and the blocks of each part
+            if (sums.pass < hi - lo) {
+                const uint32_t kept = tmem + (acc ^ 1) * kColMax + quad_lanes;
+                for (int kb = lo; kb < hi; kb += sums.pass) {
+                    ok = wait_acc(acc);
+                    if (!ok) break;
+                    const int n = min(sums.pass, hi - kb);
+                    for (int c = half * 32; c < x.cols; c += 64) {
+                        uint32_t r[32], more[32];
+                        tmem_ld32(at_acc + c, r);
+                        for (int i = 0, done = sums.chain; done < n; done += sums.chain) {
+                            tmem_ld32(at_acc + c + ++i * sums.apart, more);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(more[j]));
+                        }
+                        if (kb > lo) {
+                            tmem_ld32(kept + c, more);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(more[j]));
+                        }
+                        tmem_ld_wait();
+                        tmem_st32(kept + c, r);
+                    }
+                    tmem_st_wait();
+                    if (kb + sums.pass < hi) free_acc(acc);   // the last goes with the sums kept
+                }
+                if (!ok) break;
+                at_acc = kept, chain = hi - lo;
+            }
             Side side;
             if (SIDE && p.split == 1 && half * 32 < x.cols)
                 load_side(p, row0 + half * 32, min(32, x.cols - half * 32), at, side);
-            if (lo < hi) {
-                ok = role_wait(&sh->acc_full[a], (n_acc / 2) & 1, sh, p);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+            if (lo < hi && sums.pass == hi - lo) {
+                ok = wait_acc(acc);
                 if (!ok) break;
-                tc_fence_after();
             }
             for (int c = half * 32; c < x.cols; c += 64) {
-                float acc[32];
+                float v[32];
                 if (lo < hi) {
-                    uint32_t r[32], from = tmem + a * kColMax + c + ((uint32_t)(quad * 32) << 16);
+                    uint32_t r[32], from = at_acc + c;
                     tmem_ld32(from, r);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[j] = __uint_as_float(r[j]);
-                    for (int done = seg.blocks; done < hi - lo; done += seg.blocks) {
-                        from += seg.apart;
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                    for (int done = chain; done < hi - lo; done += chain) {
+                        from += sums.apart;
                         tmem_ld32(from, r);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) acc[j] += __uint_as_float(r[j]);
+                        for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
                     }
-                    if (c + 64 >= x.cols) free_acc(a);
+                    if (c + 64 >= x.cols) free_acc(acc);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
                 }
                 if (p.split > 1) {   // to shared memory, [column][lane]; joined below
                     float *part = reinterpret_cast<float *>(stages) + quad * 32 + lane;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (c + j < x.cols) part[(c + j) * kLanes] = acc[j];
+                        if (c + j < x.cols) part[(c + j) * kLanes] = v[j];
                 } else {
                     tile.row = x.col0 + c;
                     const Side now = side;
                     if (SIDE && c + 64 < x.cols) load_side(p, row0 + c + 64, min(32, x.cols - c - 64), at, side);
-                    epilogue_chunk<MODE, GATED, SIDE>(p, acc, row0 + c, min(32, x.cols - c), at, bias, now, tile);
+                    epilogue_chunk<MODE, GATED, SIDE>(p, v, row0 + c, min(32, x.cols - c), at, bias, now, tile);
                 }
             }
             if (lo < hi) {
-                if (half * 32 >= x.cols) free_acc(a);   // a warp with no columns here
-                ++n_acc;
+                if (half * 32 >= x.cols) free_acc(acc);   // a warp with no columns here
+                if (sums.pass == hi - lo) acc ^= 1;
             }
         }
         if (elect_one()) bulk_wait_all();
@@ -1047,6 +1109,7 @@ int launch(ProductParams &p, const void *a, const void *b, int width, cudaStream
     while (p.subs > 1 && space / (p.subs * p.sub_bytes) < 3) p.subs /= 2;
     p.block_red = p.subs * kSubRed;
     p.block_shift = p.subs == 4 ? 8 : p.subs == 2 ? 7 : 6;
+    p.chain = (p.out_f32 ? kChainF32 : kChainBf16) / p.block_red;
     p.stage_bytes = p.subs * p.sub_bytes;
     p.stages = space / p.stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;

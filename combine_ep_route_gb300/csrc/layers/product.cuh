@@ -30,6 +30,7 @@ struct ProductParams {
     int stages, stage_bytes;  // ring of operand blocks in shared memory,
     int subs, sub_bytes;      // each of this many sub-blocks of 64 reduction elements
     int block_red, block_shift;   // subs * 64, and its logarithm
+    int chain;                // blocks summed in one accumulator, at most (see Sums)
     int out_at;               // offset of the epilogue warps' output tiles, after the stages
     int split;                // CTAs of a cluster that share one tile's reduction (1 = none)
     int act, interleave;      // gated forward: 8 or 16 gate rows, then as many up rows
