@@ -193,7 +193,7 @@ __device__ __forceinline__ Tile find_tile(const ProductParams &p, const Shared *
         w.all = MODE == PRODUCT_WGRAD ? p.cols : count;
         w.width = tile_width<CG>(w.all, w.ct);
         w.red = MODE == PRODUCT_WGRAD ? count : p.red;
-        w.blocks = (w.red + p.block_red - 1) >> p.block_shift;
+        w.blocks = (int)(((uint32_t)w.red + p.block_red - 1) >> p.block_shift);   // red may be 2^31 - 1
     }
     // bands of kBand lane tiles, lane tiles innermost: the tiles in flight at a time form
     // a square rather than a strip, so each operand block is fetched by several of them
@@ -571,7 +571,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         for (int t = t0; t < total && ok; t += t_step) {
             const Tile x = find_tile<MODE, CG>(p, sh, t, rank, walk);
             const int own_cols = x.n_mma / CG;
-            const int col0 = x.col0 + (CG == 2 ? (int)rank * own_cols : 0);
+            // (of the last tile it may lie past the columns, where loads read zeros)
+            const int col0 = (int)((uint32_t)x.col0 + (CG == 2 ? rank * own_cols : 0u));
             const int chunks = (own_cols + 63) / 64;
             const uint32_t sub_bytes = lanes ? p.a_bytes : kMnB ? chunks * kChunkBytes : own_cols * 128;
             const int lane_block = x.lane0 / (GATED && MODE == PRODUCT_FORWARD ? p.interleave : 1);
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 const int r0 = kb * p.block_red, left = x.red - r0;
-                const int subs = min(p.subs, (left + kSubRed - 1) / kSubRed);
+                const int subs = left >= p.block_red ? p.subs : (left + kSubRed - 1) / kSubRed;
                 // a weight gradient's block that ends past the count goes through the
                 // zeroing warp before the MMA warp sees it
                 const bool tail = kMnB && left < p.block_red && left % kSubRed != 0;

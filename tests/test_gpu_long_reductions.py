@@ -129,3 +129,12 @@ def test_a_group_of_800_million_rows():
         dw = ep.experts_product_wgrad(ones, ones, cnt, out_dtype=dtype, status=status)
         assert status.item() == 0
         assert torch.equal(dw, torch.full((1, 8, 8), rows, dtype=D, device="cuda").to(dtype))
+
+
+def test_the_most_rows():
+    """2^31 - 1 rows, the last block of which ends past what 32 bits with a sign hold."""
+    rows = (1 << 31) - 1
+    ones = torch.ones(rows, 8, dtype=BF16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dw = ep.linear_wgrad(ones, ones, out_dtype=F32, status=status)
+    assert status.item() == 0 and (dw == 2.0 ** 31).all()
