@@ -7,7 +7,8 @@ the layer around it (experts' and linear products with their gradients, top-k ro
 """
 from .ep import (EpConfig, EpContext, DispatchOut, AgrsBuffers, agrs, alloc_agrs_buffers,  # noqa: F401
                  capacities, workspace_bytes)
-from .product import (act_grad, experts_product, experts_product_dgrad, experts_product_wgrad,  # noqa: F401
-                      linear, linear_dgrad, linear_wgrad)
+from .product import (act_grad, check_products, experts_product, experts_product_dgrad,  # noqa: F401
+                      experts_product_wgrad, linear, linear_dgrad, linear_wgrad, product_status,
+                      set_product_wait_limit)
 from .router import route_topk, route_topk_backward  # noqa: F401
 from ._lib import EpError  # noqa: F401

@@ -135,6 +135,8 @@ SIGNATURES = {
     "ep_product_wgrad": (C.c_int, [C.POINTER(EpProductC), C.c_void_p, C.c_void_p, C.c_int32,
                                    C.c_void_p, C.c_void_p, C.c_void_p]),
     "ep_act_grad": (C.c_int, [C.POINTER(EpProductC)] + [C.c_void_p] * 4),
+    "ep_product_status": (C.c_int, [C.c_void_p]),
+    "ep_product_wait_limit": (C.c_int, [C.c_int64]),
     "ep_topk_route": (C.c_int, [C.POINTER(EpTopkC)] + [C.c_void_p] * 5),
     "ep_topk_route_backward": (C.c_int, [C.POINTER(EpTopkC)] + [C.c_void_p] * 5),
 }

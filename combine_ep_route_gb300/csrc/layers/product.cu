@@ -31,6 +31,7 @@
 #include "product.cuh"
 
 #include <atomic>
+#include <mutex>
 
 #include <nvtx3/nvToolsExt.h>
 
@@ -54,9 +55,15 @@ constexpr float kNarrowSubUs = .08f;  // least time of a sub-block
 constexpr int kChainF32 = 1024;      // reduction elements summed in one accumulator (see Sums)
 constexpr int kChainBf16 = 16384;
 constexpr int kBand = 8;             // lane tiles of a band (see find_tile)
-constexpr uint32_t kSleepNs = 1000000;   // of one attempt at a wait
+constexpr uint32_t kSleepNs = 1000000;   // of one attempt at a wait, at most
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // every other wait is for a pass at most
 constexpr uint64_t kBlockNs = 10000;
+
+// What calls without a status word have reported, one word per device, and what of it the
+// last ep_product_status took.
+__device__ int32_t device_status, status_taken;
+
+__global__ void take_status() { status_taken = atomicExch(&device_status, 0); }
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], tail[kMaxStages];
@@ -87,14 +94,14 @@ struct Ring {
 // once any role of the CTA has given up.
 __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Shared *sh, const ProductParams &p,
                                           uint64_t more = 0) {
-    if (mbar_try_wait_ns(bar, parity, kSleepNs)) return true;
+    if (mbar_try_wait_ns(bar, parity, p.sleep_ns)) return true;
     const uint64_t t0 = global_ns();
     volatile int *abort = &sh->abort;
-    while (!mbar_try_wait_ns(bar, parity, kSleepNs)) {
+    while (!mbar_try_wait_ns(bar, parity, p.sleep_ns)) {
         if (*abort) return false;
         if (global_ns() - t0 > p.wait_limit_ns + more) {
             *abort = 1;
-            if (p.status) atomicCAS(p.status, 0, EP_ERR_TIMEOUT);
+            atomicCAS(p.status ? p.status : &device_status, 0, EP_ERR_TIMEOUT);
             return false;
         }
     }
@@ -1076,6 +1083,8 @@ int launch(const ProductParams &p, int clusters, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, product_kernel<MODE, GATED, CG, SIDE>, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 
+std::atomic<uint64_t> wait_limit_ns{kWaitLimitNs};
+
 // Plans and launches: `a` is the lane operand (a weight, or wgrad's x), `b` the column
 // operand, [groups][rows][width].
 template <int MODE>
@@ -1085,7 +1094,8 @@ int launch(ProductParams &p, const void *a, const void *b, int width, cudaStream
     const long long cols = MODE == PRODUCT_WGRAD ? p.cols : p.rows;
     int sms = 0;
     if (sm_count(&sms) != cudaSuccess) return EP_ERR_CUDA;
-    p.wait_limit_ns = kWaitLimitNs;
+    p.wait_limit_ns = wait_limit_ns.load(std::memory_order_relaxed);
+    p.sleep_ns = p.wait_limit_ns < kSleepNs ? (uint32_t)p.wait_limit_ns : kSleepNs;
     const long long full_tiles = ceil_div(p.lanes, full_step);
     const Plan plan = p.counts ? plan_ragged(full_tiles, p.groups, cols, sms)
                                : plan_dense(full_tiles, p.groups, cols, MODE == PRODUCT_WGRAD ? p.rows : p.red, p.lanes,
@@ -1253,4 +1263,23 @@ extern "C" int ep_product_wgrad(const ep_product_t *a, const void *dy, const voi
                    cudaSuccess
                ? EP_OK
                : EP_ERR_CUDA;
+}
+
+extern "C" int ep_product_status(void *stream) {
+    static std::mutex one;   // status_taken is shared
+    std::lock_guard<std::mutex> lock(one);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int32_t status = 0;
+    take_status<<<1, 1, 0, st>>>();
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyFromSymbolAsync(&status, status_taken, sizeof(status), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return EP_ERR_CUDA;
+    return status;
+}
+
+extern "C" int ep_product_wait_limit(int64_t ns) {
+    if (ns < 1000 || ns > 60000000000LL) return EP_ERR_INVALID_ARG;
+    wait_limit_ns.store((uint64_t)ns, std::memory_order_relaxed);
+    return EP_OK;
 }

@@ -39,8 +39,9 @@ struct ProductParams {
     const __nv_bfloat16 *z;   // dgrad: pre-activation of the product's input
     __nv_bfloat16 *preact;    // forward: pre-activation kept for the backward pass
     void *out;
-    int32_t *status;
+    int32_t *status;          // or null (= the device's own word)
     uint64_t wait_limit_ns;
+    uint32_t sleep_ns;        // of one attempt at a wait
 };
 
 }  // namespace ep

@@ -4,6 +4,10 @@ batched-experts layout dispatch writes) and dense ones, with their gradients.
 Each call passes tensor pointers and the current stream to ``ep_product``,
 ``ep_product_dgrad``, ``ep_product_wgrad`` or ``ep_act_grad`` (include/ep.h).
 Operands are contiguous bf16; ``k`` and ``n`` are multiples of 8.
+
+The kernels' waits are bounded. One that runs out (the outputs of its call are then invalid) is
+reported in the call's ``status`` tensor, or without one in a word of the device that
+:func:`check_products` reads.
 """
 from __future__ import annotations
 
@@ -14,7 +18,7 @@ from typing import Optional, Tuple, Union
 import torch
 
 from . import _lib as L
-from .ep import _stream_ptr
+from .ep import _cuda_device, _stream_ptr
 
 BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 ACTS = {"none": L.EP_ACT_NONE, "relu": L.EP_ACT_RELU, "silu": L.EP_ACT_SILU, "gelu": L.EP_ACT_GELU,
@@ -261,3 +265,23 @@ def act_grad(dy: torch.Tensor, preact: torch.Tensor, act: str, *, counts: Option
     L.check(L.lib().ep_act_grad(C.byref(a), dy.data_ptr(), preact.data_ptr(), out.data_ptr(),
                                 stream_of(stream, dev)), "ep_act_grad")
     return out
+
+
+# ----------------------------------------------------------------------- status
+
+def product_status(device: Optional[torch.device] = None, stream: Optional[torch.cuda.Stream] = None) -> int:
+    """Wait for ``stream`` (the current one) and return the status code (0 = ok) of the products on
+    ``device`` that were given no ``status`` tensor; clears it."""
+    dev = _cuda_device(device)
+    with torch.cuda.device(dev):
+        return int(L.lib().ep_product_status(_stream_ptr(stream, dev)))
+
+
+def check_products(device: Optional[torch.device] = None, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Raise what :func:`product_status` returns."""
+    L.check(product_status(device, stream), "device status of the products")
+
+
+def set_product_wait_limit(ns: int) -> None:
+    """The bound of every device-side wait of later products, 1000..60e9 ns (default 2e9)."""
+    L.check(L.lib().ep_product_wait_limit(int(ns)), "ep_product_wait_limit")

@@ -505,8 +505,9 @@ typedef struct ep_product {
     int32_t out_dtype; /* EP_BF16 or EP_F32: the type of out / dx / dw and dbias */
     const int32_t *counts; /* device [groups]: rows in use per group (clamped to 0..rows), or
                               NULL: all */
-    int32_t *status;   /* device [1] or NULL: set to EP_ERR_TIMEOUT if a bounded wait of the
-                          kernel ran out (its outputs are then invalid); never cleared here */
+    int32_t *status;   /* device [1]: set to EP_ERR_TIMEOUT if a bounded wait of the kernel ran out
+                          (its outputs are then invalid); never cleared here. NULL: the
+                          device's own word, which ep_product_status reads */
 } ep_product_t;
 
 /*
@@ -556,6 +557,17 @@ int ep_act_grad(const ep_product_t *args, const void *dy, const void *preact, vo
                 void *stream);
 
 /* Host-side errors of the four: EP_ERR_INVALID_ARG, EP_ERR_CUDA. */
+
+/*
+ * ep_product_status -- wait for the work queued on `stream`, then return what the products
+ * without a status word of their own have reported on the current device since the last call
+ * (EP_OK or EP_ERR_TIMEOUT), and clear it. EP_ERR_CUDA if the stream cannot be waited for.
+ */
+int ep_product_status(void *stream);
+
+/* ep_product_wait_limit -- bound of every device-side wait of later products of the process, ns
+ * (1000..6e10, default 2e9; host only). EP_ERR_INVALID_ARG outside. */
+int ep_product_wait_limit(int64_t ns);
 
 /* ------------------------------------------------------------------ the router */
 #define EP_SCORE_SOFTMAX 0 /* over the E logits of a token */

@@ -20,3 +20,9 @@ def test_bias_on_score_is_a_flag_of_either_score(lib):
         t = C.byref(L.EpTopkC(0, 8, 2, score | L.EP_BIAS_ON_SCORE, 1, L.EP_F32, 1.0))
         assert lib.ep_topk_route(t, None, None, None, None, None) == want
         assert lib.ep_topk_route_backward(t, None, None, None, None, None) == want
+
+
+def test_wait_limits_outside_are_refused(lib):
+    for ns in (-1, 0, 999, 60_000_000_001):
+        assert lib.ep_product_wait_limit(ns) == L.EP_ERR_INVALID_ARG
+    assert lib.ep_product_wait_limit(2_000_000_000) == L.EP_OK
