@@ -23,6 +23,7 @@ from .ep import _cuda_device, _stream_ptr
 BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 ACTS = {"none": L.EP_ACT_NONE, "relu": L.EP_ACT_RELU, "silu": L.EP_ACT_SILU, "gelu": L.EP_ACT_GELU,
         "gelu_tanh": L.EP_ACT_GELU_TANH, "swiglu": L.EP_ACT_SWIGLU}
+INT32_MAX = (1 << 31) - 1
 _OUT = {BF16: L.EP_BF16, F32: L.EP_F32}
 
 # The current stream's handle without a Stream object: building one costs as much as
@@ -101,6 +102,11 @@ def _args(groups: int, rows: int, k: int, n: int, act: int, out: torch.Tensor,
     return L.EpProductC(groups, rows, k, n, act, _OUT[out.dtype], _ptr(counts), _ptr(status))
 
 
+def _fits(rows: int, columns: int, name: str) -> None:
+    if rows > INT32_MAX or columns > INT32_MAX:   # ctypes would cut them down to 32 bits
+        raise ValueError(f"{name}: want at most {INT32_MAX} rows and columns, got {rows} x {columns}")
+
+
 def _split(t: torch.Tensor, name: str, grouped: bool) -> Tuple[int, int, int]:
     """(groups, rows, columns) of a row operand; leading dimensions of the experts' form are groups."""
     shape = t.shape
@@ -108,8 +114,11 @@ def _split(t: torch.Tensor, name: str, grouped: bool) -> Tuple[int, int, int]:
         raise ValueError(f"{name}: want {'[groups, rows, columns]' if grouped else '[rows, columns]'}, "
                          f"got {tuple(shape)}")
     if grouped:
-        return shape[0] if len(shape) == 3 else prod(shape[:-2]), shape[-2], shape[-1]
-    return 1, shape[0] if len(shape) == 2 else prod(shape[:-1]), shape[-1]
+        groups, rows = shape[0] if len(shape) == 3 else prod(shape[:-2]), shape[-2]
+    else:
+        groups, rows = 1, shape[0] if len(shape) == 2 else prod(shape[:-1])
+    _fits(rows, shape[-1], name)
+    return groups, rows, shape[-1]
 
 
 def _weight(w: torch.Tensor, groups: int, grouped: bool) -> Tuple[int, int]:
@@ -118,6 +127,7 @@ def _weight(w: torch.Tensor, groups: int, grouped: bool) -> Tuple[int, int]:
     if (len(shape) < 2 or (not grouped and len(shape) != 2)
             or (shape[0] if len(shape) == 3 else prod(shape[:-2])) != groups):
         raise ValueError(f"w: want {groups} weight(s) [rows, columns], got {tuple(shape)}")
+    _fits(shape[-2], shape[-1], "w")
     return shape[-2], shape[-1]
 
 

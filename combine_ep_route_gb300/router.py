@@ -8,7 +8,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib as L
-from .product import _want, empty, stream_of
+from .product import INT32_MAX, _want, empty, stream_of
 
 _SCORES = {"softmax": L.EP_SCORE_SOFTMAX, "sigmoid": L.EP_SCORE_SIGMOID}
 _BIASED = {"logits": 0, "scores": L.EP_BIAS_ON_SCORE}
@@ -19,14 +19,16 @@ _TYPES = {torch.bfloat16: L.EP_BF16, torch.float32: L.EP_F32}
 def _args(logits: torch.Tensor, top_k: int, score: str, renormalize: bool, scale: float) -> L.EpTopkC:
     code, kind, E = _SCORES.get(score), _TYPES.get(logits.dtype), logits.shape[-1] if logits.dim() else 0
     if (code is not None and kind is not None and logits.is_cuda and logits.is_contiguous()
-            and 1 <= top_k <= E <= L.EP_MAX_E and top_k <= L.EP_MAX_TOPK):
-        return L.EpTopkC(logits.numel() // E, E, top_k, code, 1 if renormalize else 0, kind, scale)
+            and 1 <= top_k <= E <= L.EP_MAX_E and top_k <= L.EP_MAX_TOPK
+            and (tokens := logits.numel() // E) <= INT32_MAX):
+        return L.EpTopkC(tokens, E, top_k, code, 1 if renormalize else 0, kind, scale)
     if code is None:
         raise ValueError(f"score: want one of {sorted(_SCORES)}, got {score!r}")
     if kind is None or not logits.dim() or not logits.is_contiguous() or not logits.is_cuda:
         raise ValueError(f"logits: want contiguous bfloat16 or float32 [..., E] on a CUDA device, got {logits.dtype} "
                          f"{tuple(logits.shape)} on {logits.device} (contiguous={logits.is_contiguous()})")
-    raise ValueError(f"want 1..{L.EP_MAX_E} experts and top_k in 1..min(E, {L.EP_MAX_TOPK}), got E={E}, top_k={top_k}")
+    raise ValueError(f"want 1..{L.EP_MAX_E} experts, top_k in 1..min(E, {L.EP_MAX_TOPK}) and at most {INT32_MAX} tokens, "
+                     f"got {tuple(logits.shape)}, top_k={top_k}")
 
 
 def _chosen(logits: torch.Tensor, a: L.EpTopkC) -> Tuple[int, ...]:

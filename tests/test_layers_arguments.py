@@ -3,8 +3,10 @@ refuse beyond the form of single fields, without a GPU."""
 import ctypes as C
 
 import pytest
+import torch
 
 from combine_ep_route_gb300 import _lib as L
+from combine_ep_route_gb300 import product
 
 
 @pytest.fixture(scope="module")
@@ -26,3 +28,14 @@ def test_wait_limits_outside_are_refused(lib):
     for ns in (-1, 0, 999, 60_000_000_001):
         assert lib.ep_product_wait_limit(ns) == L.EP_ERR_INVALID_ARG
     assert lib.ep_product_wait_limit(2_000_000_000) == L.EP_OK
+
+
+@pytest.mark.parametrize("rows,columns", [((1 << 32) + 5, 8), (1 << 31, 8), (5, (1 << 32) + 8)])
+def test_sizes_that_do_not_fit_are_refused(rows, columns):
+    t = torch.empty(rows, columns, device="meta")
+    for refused in (lambda: product._split(t, "x", False), lambda: product._split(t[None], "x", True),
+                    lambda: product._weight(t, 1, False), lambda: product._split(t.view(1, rows, columns), "x", False)):
+        with pytest.raises(ValueError):
+            refused()
+    most = torch.empty((1 << 31) - 1, 8, device="meta")
+    assert product._split(most, "x", False) == (1, (1 << 31) - 1, 8)
