@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) topk_backward_kernel(const TopkParam
 
 template <bool BACKWARD, int N>
 int launch_n(const TopkParams &p, bool bf16, cudaStream_t st) {
-    const int grid = (p.tokens + kWarps - 1) / kWarps;
+    const int grid = (p.tokens - 1) / kWarps + 1;   // tokens may be 2^31 - 1
     const auto kernel = BACKWARD ? (bf16 ? topk_backward_kernel<N, true> : topk_backward_kernel<N, false>)
                                  : (bf16 ? topk_kernel<N, true> : topk_kernel<N, false>);
     return launch_after(kernel, dim3((unsigned)grid), kThreads, st, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;

@@ -31,3 +31,17 @@ def test_more_rows_than_32_bits_hold_are_refused(rows):
         ep.experts_product_wgrad(x[None], x[None], torch.zeros(1, dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         ep.linear(x, torch.zeros(8, 8, dtype=BF16, device="cuda"))
+
+
+def test_the_most_tokens():
+    """2^31 - 1 tokens, one expert: all go there, with weight 1 and no gradient."""
+    tokens = (1 << 31) - 1
+    z = torch.zeros(tokens, 1, dtype=BF16, device="cuda")
+    ids = torch.full((tokens, 1), 7, dtype=torch.int32, device="cuda")
+    w = torch.full((tokens, 1), 7.0, device="cuda")
+    ep.route_topk(z, 1, out=(ids, w))
+    assert not ids.any() and (w == 1).all()
+    z.fill_(3.0)
+    d = torch.full_like(z, 7.0)
+    ep.route_topk_backward(w, z, ids, out=d)
+    assert not d.any()
