@@ -3,7 +3,8 @@ batched-experts layout dispatch writes) and dense ones, with their gradients.
 
 Each call passes tensor pointers and the current stream to ``ep_product``,
 ``ep_product_dgrad``, ``ep_product_wgrad`` or ``ep_act_grad`` (include/ep.h).
-Operands are contiguous bf16; ``k`` and ``n`` are multiples of 8.
+Operands are contiguous bf16; ``k`` and ``n`` are multiples of 8. Nothing is recorded for autograd: an
+operand that requires a gradient is refused unless under ``torch.no_grad()``.
 
 The kernels' waits are bounded. One that runs out (the outputs of its call are then invalid) is
 reported in the call's ``status`` tensor, or without one in a word of the device that
@@ -53,6 +54,16 @@ def _act(act: str) -> int:
     if code is None:
         raise ValueError(f"act: want one of {sorted(ACTS)}, got {act!r}")
     return code
+
+
+def untracked(**tensors: Optional[torch.Tensor]) -> None:
+    """Refuses what autograd would record: the result has no ``grad_fn``, so the gradient would be lost
+    without a word. (The gradient calls look at the incoming gradient only.)"""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name}: requires a gradient, which this call does not record; call it under "
+                                 "torch.no_grad() or on a detached tensor (gradients have calls of their own)")
 
 
 def _want(t: torch.Tensor, name: str, shape: Tuple[int, ...], dev, dtype=BF16) -> None:
@@ -133,6 +144,7 @@ def _weight(w: torch.Tensor, groups: int, grouped: bool) -> Tuple[int, int]:
 
 def _forward(x, w, counts, grouped, bias, act, residual, out, out_dtype, preact, status, stream):
     _operands(x, w, ("x", "w"))
+    untracked(x=x, w=w, bias=bias, residual=residual)
     dev, code = x.device, _act(act)
     groups, rows, k = _split(x, "x", grouped)
     wn, wk = _weight(w, groups, grouped)
@@ -155,6 +167,7 @@ def _forward(x, w, counts, grouped, bias, act, residual, out, out_dtype, preact,
 
 def _dgrad(dy, w, counts, grouped, act, preact, out, out_dtype, status, stream):
     _operands(dy, w, ("dy", "w"))
+    untracked(dy=dy)
     dev, code = dy.device, _act(act)
     groups, rows, n = _split(dy, "dy", grouped)
     wn, k = _weight(w, groups, grouped)
@@ -174,6 +187,7 @@ def _dgrad(dy, w, counts, grouped, act, preact, out, out_dtype, status, stream):
 
 def _wgrad(dy, x, counts, grouped, out, out_dtype, accumulate, bias_grad, status, stream):
     _operands(dy, x, ("dy", "x"))
+    untracked(dy=dy)
     dev = dy.device
     groups, rows, n = _split(dy, "dy", grouped)
     gx, rx, k = _split(x, "x", grouped)
@@ -264,6 +278,7 @@ def act_grad(dy: torch.Tensor, preact: torch.Tensor, act: str, *, counts: Option
     """``dy * act'(preact)``, for an activation that no product follows. With ``counts``, ``dy`` is
     ``[..., E, rows, n]`` and only the rows in use are written."""
     _operands(dy, preact, ("dy", "preact"))
+    untracked(dy=dy)
     dev, code = dy.device, _act(act)
     if code == L.EP_ACT_NONE:
         raise ValueError("act: want an activation")

@@ -8,7 +8,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib as L
-from .product import INT32_MAX, _want, empty, stream_of
+from .product import INT32_MAX, _want, empty, stream_of, untracked
 
 _SCORES = {"softmax": L.EP_SCORE_SOFTMAX, "sigmoid": L.EP_SCORE_SIGMOID}
 _BIASED = {"logits": 0, "scores": L.EP_BIAS_ON_SCORE}
@@ -50,6 +50,7 @@ def route_topk(logits: torch.Tensor, top_k: int, *, score: str = "softmax", reno
     in ids of -1, which dispatch drops.
     """
     a = _args(logits, top_k, score, renormalize, scale)
+    untracked(logits=logits, bias=bias)
     dev, shape = logits.device, _chosen(logits, a)
     if bias_on not in _BIASED:
         raise ValueError(f"bias_on: want one of {sorted(_BIASED)}, got {bias_on!r}")
@@ -75,6 +76,7 @@ def route_topk_backward(dweights: torch.Tensor, logits: torch.Tensor, topk_ids: 
     if topk_ids.dim() < 1:
         raise ValueError("topk_ids: want [..., top_k]")
     a = _args(logits, topk_ids.shape[-1], score, renormalize, scale)
+    untracked(dweights=dweights)
     dev, shape = logits.device, _chosen(logits, a)
     _want(topk_ids, "topk_ids", shape, dev, _I32)
     _want(dweights, "dweights", shape, dev, _F32)
