@@ -101,6 +101,11 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _counted(counts: Optional[torch.Tensor], grouped: bool) -> None:
+    if grouped and counts is None:   # the C entry takes every row then, also what dispatch never wrote
+        raise ValueError("counts: want the rows in use per expert, got None")
+
+
 def _args(groups: int, rows: int, k: int, n: int, act: int, out: torch.Tensor,
           counts: Optional[torch.Tensor], status: Optional[torch.Tensor], dev) -> L.EpProductC:
     if counts is not None:
@@ -143,6 +148,7 @@ def _weight(w: torch.Tensor, groups: int, grouped: bool) -> Tuple[int, int]:
 
 
 def _forward(x, w, counts, grouped, bias, act, residual, out, out_dtype, preact, status, stream):
+    _counted(counts, grouped)
     _operands(x, w, ("x", "w"))
     untracked(x=x, w=w, bias=bias, residual=residual)
     dev, code = x.device, _act(act)
@@ -166,6 +172,7 @@ def _forward(x, w, counts, grouped, bias, act, residual, out, out_dtype, preact,
 
 
 def _dgrad(dy, w, counts, grouped, act, preact, out, out_dtype, status, stream):
+    _counted(counts, grouped)
     _operands(dy, w, ("dy", "w"))
     untracked(dy=dy)
     dev, code = dy.device, _act(act)
@@ -186,6 +193,7 @@ def _dgrad(dy, w, counts, grouped, act, preact, out, out_dtype, status, stream):
 
 
 def _wgrad(dy, x, counts, grouped, out, out_dtype, accumulate, bias_grad, status, stream):
+    _counted(counts, grouped)
     _operands(dy, x, ("dy", "x"))
     untracked(dy=dy)
     dev = dy.device

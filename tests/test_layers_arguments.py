@@ -5,6 +5,7 @@ import ctypes as C
 import pytest
 import torch
 
+import combine_ep_route_gb300 as ep
 from combine_ep_route_gb300 import _lib as L
 from combine_ep_route_gb300 import product
 
@@ -39,3 +40,11 @@ def test_sizes_that_do_not_fit_are_refused(rows, columns):
             refused()
     most = torch.empty((1 << 31) - 1, 8, device="meta")
     assert product._split(most, "x", False) == (1, (1 << 31) - 1, 8)
+
+
+def test_experts_without_counts_are_refused():
+    x, w = torch.zeros(2, 4, 8, dtype=torch.bfloat16), torch.zeros(2, 8, 8, dtype=torch.bfloat16)
+    for call in (lambda: ep.experts_product(x, w, None), lambda: ep.experts_product_dgrad(x, w, None),
+                 lambda: ep.experts_product_wgrad(x, x, None)):
+        with pytest.raises(ValueError, match="counts"):
+            call()
