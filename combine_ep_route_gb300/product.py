@@ -262,7 +262,11 @@ def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = N
            residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
            out_dtype: Optional[torch.dtype] = None, preact: Optional[torch.Tensor] = None,
            status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
-    """``act(x @ w^T + bias) + residual`` for ``x`` ``[..., k]`` and ``w`` ``[n, k]`` (``swiglu``: ``[2n, k]``)."""
+    """``act(x @ w^T + bias) + residual`` for ``x`` ``[..., k]`` and ``w`` ``[n, k]`` (``swiglu``: ``[2n, k]``).
+
+    ``n`` and ``k`` are multiples of 8. A router for another number of experts keeps its weight padded with
+    zero rows and a ``bias`` of minus infinity there: such logits are never chosen and have no gradient.
+    """
     return _forward(x, w, None, False, bias, act, residual, out, out_dtype, preact, status, stream)
 
 
