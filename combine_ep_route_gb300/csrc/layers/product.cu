@@ -1156,12 +1156,12 @@ int launch(ProductParams &p, const void *a, const void *b, int width, cudaStream
     // whether the epilogue reads from memory: residual, pre-activations, output added to
     const bool side = MODE == PRODUCT_FORWARD ? p.residual != nullptr : MODE == PRODUCT_DGRAD ? p.z != nullptr : p.accumulate;
     if constexpr (MODE != PRODUCT_WGRAD) {
-        if (gated) {
-            if (MODE == PRODUCT_DGRAD || side)
-                return cg == 2 ? launch<MODE, true, 2, true>(p, clusters, st) : launch<MODE, true, 1, true>(p, clusters, st);
-            return cg == 2 ? launch<MODE, true, 2, MODE == PRODUCT_DGRAD>(p, clusters, st)
-                           : launch<MODE, true, 1, MODE == PRODUCT_DGRAD>(p, clusters, st);
-        }
+        if (gated && side)
+            return cg == 2 ? launch<MODE, true, 2, true>(p, clusters, st) : launch<MODE, true, 1, true>(p, clusters, st);
+    }
+    if constexpr (MODE == PRODUCT_FORWARD) {   // (a gated gradient always reads its pre-activation)
+        if (gated)
+            return cg == 2 ? launch<MODE, true, 2, false>(p, clusters, st) : launch<MODE, true, 1, false>(p, clusters, st);
     }
     if (side) return cg == 2 ? launch<MODE, false, 2, true>(p, clusters, st) : launch<MODE, false, 1, true>(p, clusters, st);
     return cg == 2 ? launch<MODE, false, 2, false>(p, clusters, st) : launch<MODE, false, 1, false>(p, clusters, st);

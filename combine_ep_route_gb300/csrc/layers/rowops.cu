@@ -1,6 +1,6 @@
 // rowops.cu -- row-wise companions of the products: the bias gradient (a sum of
-// rows per group) and the gradient through an activation that no product follows.
-// Both read each byte once and are bound by HBM.
+// rows per group), which latency bounds, and the gradient through an activation that no
+// product follows, which HBM does. Both read each byte once.
 #include "launch.cuh"
 
 #include <cooperative_groups.h>
@@ -104,41 +104,39 @@ __global__ void __launch_bounds__(kSumThreads) row_sums_kernel(const uint4 *src,
 // One thread per 16-byte vector of dy, rows in use only. 8192 x 7168: gelu 57.7 us (6.1 TB/s),
 // relu 56.1 (6.3); 8192 x 4096 through swiglu 53.0 (6.3).
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const uint4 *dy, const uint4 *z, uint4 *dz,
-                                                            const int32_t *counts, int groups, int rows,
-                                                            int nvec, int act) {
+                                                            const int32_t *counts, int rows, int nvec, int act) {
     pdl_launch_dependents();
     pdl_wait();
     const bool gated = act == EP_ACT_SWIGLU;
-    for (int g = blockIdx.y; g < groups; g += gridDim.y) {
-        const int count = counts ? max(0, min(counts[g], rows)) : rows;
-        const long long items = (long long)count * nvec;
-        for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < items;
-             i += (long long)gridDim.x * kThreads) {
-            const size_t row = (size_t)g * rows + (size_t)(i / nvec);
-            const int v = (int)(i % nvec);
-            const size_t zi = row * nvec * (gated ? 2 : 1) + v;
-            const uint4 d4 = dy[row * nvec + v], a4 = z[zi];
-            const uint4 b4 = gated ? z[zi + nvec] : make_uint4(0, 0, 0, 0);
-            const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w}, a[4] = {a4.x, a4.y, a4.z, a4.w},
-                           b[4] = {b4.x, b4.y, b4.z, b4.w};
-            uint32_t oa[4], ob[4];
+    const int g = blockIdx.y;
+    const int count = counts ? max(0, min(counts[g], rows)) : rows;
+    const long long items = (long long)count * nvec;
+    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < items;
+         i += (long long)gridDim.x * kThreads) {
+        const size_t row = (size_t)g * rows + (size_t)(i / nvec);
+        const int v = (int)(i % nvec);
+        const size_t zi = row * nvec * (gated ? 2 : 1) + v;
+        const uint4 d4 = dy[row * nvec + v], a4 = z[zi];
+        const uint4 b4 = gated ? z[zi + nvec] : make_uint4(0, 0, 0, 0);
+        const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w}, a[4] = {a4.x, a4.y, a4.z, a4.w},
+                       b[4] = {b4.x, b4.y, b4.z, b4.w};
+        uint32_t oa[4], ob[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 dv = unpack_bf16x2(d[q]), zv = unpack_bf16x2(a[q]), uv = unpack_bf16x2(b[q]);
-                if (gated) {
-                    float2 dg, du;
-                    swiglu_grad(dv.x, zv.x, uv.x, dg.x, du.x);
-                    swiglu_grad(dv.y, zv.y, uv.y, dg.y, du.y);
-                    oa[q] = pack_bf16x2_rn(dg.x, dg.y);
-                    ob[q] = pack_bf16x2_rn(du.x, du.y);
-                } else {
-                    oa[q] = pack_bf16x2_rn(dv.x * act_slope(zv.x, act), dv.y * act_slope(zv.y, act));
-                    ob[q] = 0;
-                }
+        for (int q = 0; q < 4; ++q) {
+            const float2 dv = unpack_bf16x2(d[q]), zv = unpack_bf16x2(a[q]), uv = unpack_bf16x2(b[q]);
+            if (gated) {
+                float2 dg, du;
+                swiglu_grad(dv.x, zv.x, uv.x, dg.x, du.x);
+                swiglu_grad(dv.y, zv.y, uv.y, dg.y, du.y);
+                oa[q] = pack_bf16x2_rn(dg.x, dg.y);
+                ob[q] = pack_bf16x2_rn(du.x, du.y);
+            } else {
+                oa[q] = pack_bf16x2_rn(dv.x * act_slope(zv.x, act), dv.y * act_slope(zv.y, act));
+                ob[q] = 0;
             }
-            dz[zi] = make_uint4(oa[0], oa[1], oa[2], oa[3]);
-            if (gated) dz[zi + nvec] = make_uint4(ob[0], ob[1], ob[2], ob[3]);
         }
+        dz[zi] = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+        if (gated) dz[zi + nvec] = make_uint4(ob[0], ob[1], ob[2], ob[3]);
     }
 }
 
@@ -183,12 +181,12 @@ extern "C" int ep_act_grad(const ep_product_t *a, const void *dy, const void *pr
         return EP_ERR_INVALID_ARG;
     const long long per_group = ((long long)a->rows * (a->n / 8) + kThreads - 1) / kThreads;
     // about sixteen CTAs per SM in all, however many groups share them
-    const long long want = a->groups >= 2048 ? 1 : 2432 / a->groups + 1;
+    const long long want = 2432 / a->groups + 1;
     const dim3 grid((unsigned)(per_group < want ? per_group : want), (unsigned)a->groups);
     nvtxRangePushA("ep:act_grad");
     const cudaError_t e = launch_after(act_grad_kernel, grid, kThreads, static_cast<cudaStream_t>(stream),
                                        static_cast<const uint4 *>(dy), static_cast<const uint4 *>(preact),
-                                       static_cast<uint4 *>(dz), a->counts, a->groups, a->rows, a->n / 8, a->act);
+                                       static_cast<uint4 *>(dz), a->counts, a->rows, a->n / 8, a->act);
     nvtxRangePop();
     return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
