@@ -239,16 +239,19 @@ __device__ __forceinline__ void my_blocks(const ProductParams &p, const Tile &x,
 // columns leave room has several chains side by side in it, added up with rounding by the
 // epilogue. What is longer takes several passes in the same accumulator; the epilogue warps
 // keep the running sums, rounded, in the other, and the MMAs wait meanwhile (fp32 8192 x 7168 x 4096:
-// 271 -> 307 us; a bf16 weight gradient of 65536 rows, 4096 x 2048: 662 -> 664).
+// 271 -> 307 us; a bf16 weight gradient of 65536 rows, 4096 x 2048: 662 -> 664). Such products
+// have kernels of their own (LONG): in one kernel for both the others lost 1 to 2 % (7 x 7168 x 7168
+// 22.8 -> 23.0 us, the gradients of 5001 x 4096 x 2048 137.2 -> 139.5).
 struct Sums {
     int apart;    // columns between the chains of a pass
     int chain;    // blocks of a chain
     int pass;     // blocks of a pass; the tile's, unless it takes several
 };
+template <bool LONG>
 __device__ __forceinline__ Sums sums_of(const ProductParams &p, const Tile &x, int blocks) {
     const int shift = !p.out_f32 ? 0 : x.n_mma <= 64 ? 2 : x.n_mma <= 128 ? 1 : 0;   // log2 of the chains
     int pass = blocks;
-    if (blocks > p.chain << shift) {
+    if (LONG && blocks > p.chain << shift) {
         const int passes = (blocks - 1) / (p.chain << shift) + 1;
         pass = (blocks - 1) / passes + 1;
     }
@@ -509,7 +512,7 @@ __device__ __forceinline__ void epilogue_chunk(const ProductParams &p, const flo
     }
 }
 
-template <int MODE, bool GATED, int CG, bool SIDE>
+template <int MODE, bool GATED, int CG, bool SIDE, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductParams p) {
     constexpr bool kMnA = MODE != PRODUCT_FORWARD, kMnB = MODE == PRODUCT_WGRAD;
     extern __shared__ uint8_t raw[];
@@ -647,9 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             my_blocks(p, x, rank, lo, hi);
             if (lo == hi) continue;
             const uint32_t idesc = mma_idesc(kLanes * CG, x.n_mma, kMnA, kMnB);
-            const Sums sums = sums_of(p, x, hi - lo);
+            const Sums sums = sums_of<LONG>(p, x, hi - lo);
             for (int kb = lo; kb < hi && ok;) {
-                const int end = min(kb + sums.pass, hi);
+                const int end = LONG ? min(kb + sums.pass, hi) : hi;
                 ok = role_wait(&sh->acc_empty[acc], ((acc_phase >> acc) & 1) ^ 1, sh, p);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
@@ -687,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 __syncwarp();
                 acc_phase ^= 1u << acc;
             }
-            if (sums.pass == hi - lo) acc ^= 1;   // after several passes the next tile goes on in the same
+            if (!LONG || sums.pass == hi - lo) acc ^= 1;   // after several passes the next tile goes on in the same
         }
     } else if (warp == 2 && kMnB) {
         // ---- rows at or past the count, in the last block: zero in both operands
@@ -763,11 +766,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 bias = unpack_bf16x2(ld_pair(p.bias + (size_t)x.g * (GATED ? 2 : 1) * p.lanes +
                                              (at.up ? p.lanes : 0) + at.f));
             tile.lane = x.lane0 + quad * 32, tile.group = x.g;
-            const Sums sums = sums_of(p, x, hi - lo);
+            const Sums sums = sums_of<LONG>(p, x, hi - lo);
             const uint32_t quad_lanes = (uint32_t)(quad * 32) << 16;
             uint32_t at_acc = tmem + acc * kColMax + quad_lanes;   // where the sums are read,
             int chain = sums.chain;                                // and the blocks of each part
-            if (sums.pass < hi - lo) {
+            if (LONG && sums.pass < hi - lo) {
                 const uint32_t kept = tmem + (acc ^ 1) * kColMax + quad_lanes;
                 for (int kb = lo; kb < hi; kb += sums.pass) {
                     ok = wait_acc(acc);
@@ -802,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             Side side;
             if (SIDE && p.split == 1 && half * 32 < x.cols)
                 load_side(p, row0 + half * 32, min(32, x.cols - half * 32), at, side);
-            if (lo < hi && sums.pass == hi - lo) {
+            if (lo < hi && (!LONG || sums.pass == hi - lo)) {
                 ok = wait_acc(acc);
                 if (!ok) break;
             }
@@ -840,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
             if (lo < hi) {
                 if (half * 32 >= x.cols) free_acc(acc);   // a warp with no columns here
-                if (sums.pass == hi - lo) acc ^= 1;
+                if (!LONG || sums.pass == hi - lo) acc ^= 1;
             }
         }
         if (elect_one()) bulk_wait_all();
@@ -1062,9 +1065,9 @@ Plan plan_dense(long long lane_tiles, long long groups, long long cols, long lon
 }
 
 template <int MODE, bool GATED, int CG, bool SIDE>
-int launch(const ProductParams &p, int clusters, cudaStream_t st) {
-    const void *fn = reinterpret_cast<const void *>(&product_kernel<MODE, GATED, CG, SIDE>);
-    if (ensure_dyn_smem(fn, kSmemMax) != cudaSuccess) return EP_ERR_CUDA;
+int launch(const ProductParams &p, bool is_long, int clusters, cudaStream_t st) {
+    const auto kernel = is_long ? &product_kernel<MODE, GATED, CG, SIDE, true> : &product_kernel<MODE, GATED, CG, SIDE, false>;
+    if (ensure_dyn_smem(reinterpret_cast<const void *>(kernel), kSmemMax) != cudaSuccess) return EP_ERR_CUDA;
     const int size = CG == 2 ? 2 : p.split;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * size));
@@ -1080,7 +1083,7 @@ int launch(const ProductParams &p, int clusters, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, product_kernel<MODE, GATED, CG, SIDE>, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 
 std::atomic<uint64_t> wait_limit_ns{kWaitLimitNs};
@@ -1121,6 +1124,9 @@ int launch(ProductParams &p, const void *a, const void *b, int width, cudaStream
     p.block_red = p.subs * kSubRed;
     p.block_shift = p.subs == 4 ? 8 : p.subs == 2 ? 7 : 6;
     p.chain = (p.out_f32 ? kChainF32 : kChainBf16) / p.block_red;
+    // whether a tile may take several passes (see Sums; the widest has the fewest chains)
+    const long long own_blocks = ceil_div(ceil_div(MODE == PRODUCT_WGRAD ? p.rows : p.red, p.block_red), p.split);
+    const bool is_long = own_blocks > (long long)p.chain << (!p.out_f32 ? 0 : widest <= 64 ? 2 : widest <= 128 ? 1 : 0);
     p.stage_bytes = p.subs * p.sub_bytes;
     p.stages = space / p.stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
@@ -1157,14 +1163,14 @@ int launch(ProductParams &p, const void *a, const void *b, int width, cudaStream
     const bool side = MODE == PRODUCT_FORWARD ? p.residual != nullptr : MODE == PRODUCT_DGRAD ? p.z != nullptr : p.accumulate;
     if constexpr (MODE != PRODUCT_WGRAD) {
         if (gated && side)
-            return cg == 2 ? launch<MODE, true, 2, true>(p, clusters, st) : launch<MODE, true, 1, true>(p, clusters, st);
+            return cg == 2 ? launch<MODE, true, 2, true>(p, is_long, clusters, st) : launch<MODE, true, 1, true>(p, is_long, clusters, st);
     }
     if constexpr (MODE == PRODUCT_FORWARD) {   // (a gated gradient always reads its pre-activation)
         if (gated)
-            return cg == 2 ? launch<MODE, true, 2, false>(p, clusters, st) : launch<MODE, true, 1, false>(p, clusters, st);
+            return cg == 2 ? launch<MODE, true, 2, false>(p, is_long, clusters, st) : launch<MODE, true, 1, false>(p, is_long, clusters, st);
     }
-    if (side) return cg == 2 ? launch<MODE, false, 2, true>(p, clusters, st) : launch<MODE, false, 1, true>(p, clusters, st);
-    return cg == 2 ? launch<MODE, false, 2, false>(p, clusters, st) : launch<MODE, false, 1, false>(p, clusters, st);
+    if (side) return cg == 2 ? launch<MODE, false, 2, true>(p, is_long, clusters, st) : launch<MODE, false, 1, true>(p, is_long, clusters, st);
+    return cg == 2 ? launch<MODE, false, 2, false>(p, is_long, clusters, st) : launch<MODE, false, 1, false>(p, is_long, clusters, st);
 }
 
 bool aligned16(const void *q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
