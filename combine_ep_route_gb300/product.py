@@ -25,6 +25,8 @@ BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 ACTS = {"none": L.EP_ACT_NONE, "relu": L.EP_ACT_RELU, "silu": L.EP_ACT_SILU, "gelu": L.EP_ACT_GELU,
         "gelu_tanh": L.EP_ACT_GELU_TANH, "swiglu": L.EP_ACT_SWIGLU}
 INT32_MAX = (1 << 31) - 1
+# (the C entry takes every row then, also what dispatch never wrote)
+_NO_COUNTS = "counts: want the rows in use per expert, got None"
 _OUT = {BF16: L.EP_BF16, F32: L.EP_F32}
 
 # The current stream's handle without a Stream object: building one costs as much as
@@ -101,11 +103,6 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _counted(counts: Optional[torch.Tensor], grouped: bool) -> None:
-    if grouped and counts is None:   # the C entry takes every row then, also what dispatch never wrote
-        raise ValueError("counts: want the rows in use per expert, got None")
-
-
 def _args(groups: int, rows: int, k: int, n: int, act: int, out: torch.Tensor,
           counts: Optional[torch.Tensor], status: Optional[torch.Tensor], dev) -> L.EpProductC:
     if counts is not None:
@@ -118,11 +115,6 @@ def _args(groups: int, rows: int, k: int, n: int, act: int, out: torch.Tensor,
     return L.EpProductC(groups, rows, k, n, act, _OUT[out.dtype], _ptr(counts), _ptr(status))
 
 
-def _fits(rows: int, columns: int, name: str) -> None:
-    if rows > INT32_MAX or columns > INT32_MAX:   # ctypes would cut them down to 32 bits
-        raise ValueError(f"{name}: want at most {INT32_MAX} rows and columns, got {rows} x {columns}")
-
-
 def _split(t: torch.Tensor, name: str, grouped: bool) -> Tuple[int, int, int]:
     """(groups, rows, columns) of a row operand; leading dimensions of the experts' form are groups."""
     shape = t.shape
@@ -133,8 +125,10 @@ def _split(t: torch.Tensor, name: str, grouped: bool) -> Tuple[int, int, int]:
         groups, rows = shape[0] if len(shape) == 3 else prod(shape[:-2]), shape[-2]
     else:
         groups, rows = 1, shape[0] if len(shape) == 2 else prod(shape[:-1])
-    _fits(rows, shape[-1], name)
-    return groups, rows, shape[-1]
+    columns = shape[-1]
+    if rows > INT32_MAX or columns > INT32_MAX:   # ctypes would cut them down to 32 bits
+        raise ValueError(f"{name}: want at most {INT32_MAX} rows and columns, got {rows} x {columns}")
+    return groups, rows, columns
 
 
 def _weight(w: torch.Tensor, groups: int, grouped: bool) -> Tuple[int, int]:
@@ -143,14 +137,19 @@ def _weight(w: torch.Tensor, groups: int, grouped: bool) -> Tuple[int, int]:
     if (len(shape) < 2 or (not grouped and len(shape) != 2)
             or (shape[0] if len(shape) == 3 else prod(shape[:-2])) != groups):
         raise ValueError(f"w: want {groups} weight(s) [rows, columns], got {tuple(shape)}")
-    _fits(shape[-2], shape[-1], "w")
-    return shape[-2], shape[-1]
+    rows, columns = shape[-2], shape[-1]
+    if rows > INT32_MAX or columns > INT32_MAX:
+        raise ValueError(f"w: want at most {INT32_MAX} rows and columns, got {rows} x {columns}")
+    return rows, columns
 
 
 def _forward(x, w, counts, grouped, bias, act, residual, out, out_dtype, preact, status, stream):
-    _counted(counts, grouped)
+    if grouped and counts is None:
+        raise ValueError(_NO_COUNTS)
     _operands(x, w, ("x", "w"))
-    untracked(x=x, w=w, bias=bias, residual=residual)
+    if (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad)
+            or (residual is not None and residual.requires_grad)):
+        untracked(x=x, w=w, bias=bias, residual=residual)
     dev, code = x.device, _act(act)
     groups, rows, k = _split(x, "x", grouped)
     wn, wk = _weight(w, groups, grouped)
@@ -172,9 +171,11 @@ def _forward(x, w, counts, grouped, bias, act, residual, out, out_dtype, preact,
 
 
 def _dgrad(dy, w, counts, grouped, act, preact, out, out_dtype, status, stream):
-    _counted(counts, grouped)
+    if grouped and counts is None:
+        raise ValueError(_NO_COUNTS)
     _operands(dy, w, ("dy", "w"))
-    untracked(dy=dy)
+    if dy.requires_grad:
+        untracked(dy=dy)
     dev, code = dy.device, _act(act)
     groups, rows, n = _split(dy, "dy", grouped)
     wn, k = _weight(w, groups, grouped)
@@ -193,9 +194,11 @@ def _dgrad(dy, w, counts, grouped, act, preact, out, out_dtype, status, stream):
 
 
 def _wgrad(dy, x, counts, grouped, out, out_dtype, accumulate, bias_grad, status, stream):
-    _counted(counts, grouped)
+    if grouped and counts is None:
+        raise ValueError(_NO_COUNTS)
     _operands(dy, x, ("dy", "x"))
-    untracked(dy=dy)
+    if dy.requires_grad:
+        untracked(dy=dy)
     dev = dy.device
     groups, rows, n = _split(dy, "dy", grouped)
     gx, rx, k = _split(x, "x", grouped)
@@ -290,7 +293,8 @@ def act_grad(dy: torch.Tensor, preact: torch.Tensor, act: str, *, counts: Option
     """``dy * act'(preact)``, for an activation that no product follows. With ``counts``, ``dy`` is
     ``[..., E, rows, n]`` and only the rows in use are written."""
     _operands(dy, preact, ("dy", "preact"))
-    untracked(dy=dy)
+    if dy.requires_grad:
+        untracked(dy=dy)
     dev, code = dy.device, _act(act)
     if code == L.EP_ACT_NONE:
         raise ValueError("act: want an activation")

@@ -50,7 +50,8 @@ def route_topk(logits: torch.Tensor, top_k: int, *, score: str = "softmax", reno
     in ids of -1, which dispatch drops.
     """
     a = _args(logits, top_k, score, renormalize, scale)
-    untracked(logits=logits, bias=bias)
+    if logits.requires_grad or (bias is not None and bias.requires_grad):
+        untracked(logits=logits, bias=bias)
     dev, shape = logits.device, _chosen(logits, a)
     if bias_on not in _BIASED:
         raise ValueError(f"bias_on: want one of {sorted(_BIASED)}, got {bias_on!r}")
@@ -76,7 +77,8 @@ def route_topk_backward(dweights: torch.Tensor, logits: torch.Tensor, topk_ids: 
     if topk_ids.dim() < 1:
         raise ValueError("topk_ids: want [..., top_k]")
     a = _args(logits, topk_ids.shape[-1], score, renormalize, scale)
-    untracked(dweights=dweights)
+    if dweights.requires_grad:
+        untracked(dweights=dweights)
     dev, shape = logits.device, _chosen(logits, a)
     _want(topk_ids, "topk_ids", shape, dev, _I32)
     _want(dweights, "dweights", shape, dev, _F32)
