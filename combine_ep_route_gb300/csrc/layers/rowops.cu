@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(kSumThreads) row_sums_kernel(const uint4 *src,
     }
 }
 
-// One thread per 16-byte vector of dy, rows in use only. 8192 x 7168: gelu 57.7 us (6.1 TB/s),
-// relu 56.1 (6.3); 8192 x 4096 through swiglu 53.0 (6.3).
+// One thread per 16-byte vector of dy, rows in use only. 8192 x 7168: gelu 59.0 us (6.0 TB/s),
+// gelu_tanh 56.5 (6.2), relu 56.0 (6.3); 8192 x 4096 through swiglu 52.5 (6.4).
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const uint4 *dy, const uint4 *z, uint4 *dz,
                                                             const int32_t *counts, int rows, int nvec, int act) {
     pdl_launch_dependents();
