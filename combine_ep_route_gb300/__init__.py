@@ -11,4 +11,6 @@ from .product import (act_grad, check_products, experts_product, experts_product
                       experts_product_wgrad, linear, linear_dgrad, linear_wgrad, product_status,
                       set_product_wait_limit)
 from .router import route_topk, route_topk_backward  # noqa: F401
+from .balance import balance_loss, balance_loss_backward  # noqa: F401
+from .gradnorm import clip_grad_norm  # noqa: F401
 from ._lib import EpError  # noqa: F401

@@ -107,6 +107,17 @@ class EpTopkC(C.Structure):
                 ("renormalize", C.c_int32), ("logits_dtype", C.c_int32), ("scale", C.c_float)]
 
 
+class EpBalanceC(C.Structure):
+    _fields_ = [("seqs", C.c_int32), ("tokens", C.c_int32), ("E", C.c_int32), ("top_k", C.c_int32),
+                ("score", C.c_int32), ("per_sequence", C.c_int32), ("logits_dtype", C.c_int32),
+                ("num_tokens", C.c_void_p)]
+
+
+class EpGradsC(C.Structure):
+    _fields_ = [("n", C.c_int32), ("grads", C.c_void_p), ("out", C.c_void_p), ("numel", C.c_void_p),
+                ("dtypes", C.c_void_p)]
+
+
 # name -> (restype, argtypes); mirrors include/ep.h one to one
 SIGNATURES = {
     "ep_capacities": (C.c_int, [C.POINTER(EpConfigC), C.POINTER(C.c_int32), C.POINTER(C.c_int32),
@@ -139,6 +150,13 @@ SIGNATURES = {
     "ep_product_wait_limit": (C.c_int, [C.c_int64]),
     "ep_topk_route": (C.c_int, [C.POINTER(EpTopkC)] + [C.c_void_p] * 5),
     "ep_topk_route_backward": (C.c_int, [C.POINTER(EpTopkC)] + [C.c_void_p] * 5),
+    "ep_balance_workspace_bytes": (C.c_int, [C.POINTER(EpBalanceC), C.POINTER(C.c_size_t)]),
+    "ep_balance_loss": (C.c_int, [C.POINTER(EpBalanceC)] + [C.c_void_p] * 5 + [C.c_size_t, C.c_void_p]),
+    "ep_balance_loss_backward": (C.c_int, [C.POINTER(EpBalanceC)] + [C.c_void_p] * 3
+                                 + [C.c_int32, C.c_void_p, C.c_void_p]),
+    "ep_clip_workspace_bytes": (C.c_int, [C.POINTER(EpGradsC), C.POINTER(C.c_size_t)]),
+    "ep_clip_grad_norm": (C.c_int, [C.POINTER(EpGradsC), C.c_float, C.c_void_p, C.c_void_p, C.c_size_t,
+                                    C.c_void_p]),
 }
 
 _lib = None

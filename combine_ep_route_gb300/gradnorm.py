@@ -1,0 +1,58 @@
+"""The global norm of many gradients and their clipping by it (``ep_clip_grad_norm`` in include/ep.h)."""
+from __future__ import annotations
+
+import ctypes as C
+from typing import Optional, Sequence
+
+import torch
+
+from . import _lib as L
+from .product import _OUT, INT32_MAX, empty, stream_of, untracked
+
+
+def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[Sequence[torch.Tensor]] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The norm of all ``grads`` together (float32, no dimensions), which are scaled in place by ``max_norm / norm``
+    where it is finite and above ``max_norm``, and otherwise left as they are; a norm that is not finite is the
+    caller's to handle.
+
+    ``grads`` are contiguous bf16 and float32 tensors of any shape on one CUDA device, of which no two overlap;
+    ``max_norm`` of infinity gives the norm alone. With ``out`` (tensors of the same shapes and types) the
+    gradients, scaled or not, are written there and ``grads`` stay as they are. Nothing waits for the GPU.
+    """
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    max_norm = float(max_norm)
+    if not grads:
+        raise ValueError("grads: want one tensor at least")
+    if not max_norm >= 0:
+        raise ValueError(f"max_norm: want a number from 0, got {max_norm}")
+    if len(outs) != len(grads):
+        raise ValueError(f"out: want {len(grads)} tensors, got {len(outs)}")
+    n, dev = len(grads), grads[0].device
+    if n > INT32_MAX:
+        raise ValueError("grads: too many")
+    for t in grads:
+        if t.dtype not in _OUT or not t.is_cuda or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"grads: want contiguous bfloat16 or float32 on one CUDA device, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
+        if t.requires_grad:
+            untracked(grads=t)
+    if out is not None:
+        for o, t in zip(outs, grads):
+            if o.dtype != t.dtype or o.shape != t.shape or o.device != dev or not o.is_contiguous():
+                raise ValueError(f"out: want contiguous {t.dtype} {tuple(t.shape)} on {dev}, got {o.dtype} "
+                                 f"{tuple(o.shape)} on {o.device} (contiguous={o.is_contiguous()})")
+            if o.requires_grad:
+                untracked(out=o)
+    ptrs = (C.c_void_p * n)(*[t.data_ptr() for t in grads])
+    to = None if out is None else (C.c_void_p * n)(*[t.data_ptr() for t in outs])
+    numel = (C.c_int64 * n)(*[t.numel() for t in grads])
+    kinds = (C.c_int32 * n)(*[_OUT[t.dtype] for t in grads])
+    a = L.EpGradsC(n, C.addressof(ptrs), None if to is None else C.addressof(to), C.addressof(numel), C.addressof(kinds))
+    size, lib = C.c_size_t(), L.lib()
+    L.check(lib.ep_clip_workspace_bytes(C.byref(a), C.byref(size)), "ep_clip_workspace_bytes")
+    norm, work = empty((), torch.float32, dev, stream), empty((size.value,), torch.uint8, dev, stream)
+    L.check(lib.ep_clip_grad_norm(C.byref(a), max_norm, norm.data_ptr(), work.data_ptr(), size.value,
+                                  stream_of(stream, dev)), "ep_clip_grad_norm (tensors must not overlap)")
+    return norm

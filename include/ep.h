@@ -610,6 +610,79 @@ int ep_topk_route_backward(const ep_topk_t *args, const float *dweights, const v
 
 /* Both: pointers aligned to their element. Host-side errors: EP_ERR_INVALID_ARG, EP_ERR_CUDA. */
 
+/* -------------------------------------------------------- the router's balance loss
+ *
+ * Of `seqs` sequences (or ranks) of `tokens` token slots each, num_tokens[s] of sequence s
+ * hold tokens (NULL: all; clamped to 0..tokens). Tokens form pools: all together, or with
+ * per_sequence 1 each sequence its own. In a pool of N tokens, c_e counts the tokens' choices
+ * of expert e, p_e is a token's probability of it (EP_SCORE_SOFTMAX: of the logits;
+ * EP_SCORE_SIGMOID: its sigmoid over the sum of all), and
+ *   losses[0] = mean over the pools with tokens of sum_e E c_e / (top_k N) * (sum of p_e) / N,
+ *               1 where choices and probabilities are even
+ *   losses[1] = mean over all tokens of (log of the sum of exp(logit))^2, whatever the score
+ * (0 without tokens). A logit of minus infinity or NaN takes no part in its token's
+ * probabilities, a token without any other adds nothing to either sum; ids outside 0..E-1 are
+ * not counted. Sums do not depend on the order of execution.
+ */
+typedef struct ep_balance {
+    int32_t seqs, tokens;      /* >= 0, seqs * tokens < 2^31 */
+    int32_t E;                 /* experts, 1..EP_MAX_E */
+    int32_t top_k;             /* ids of a token, 1..min(E, EP_MAX_TOPK) */
+    int32_t score;             /* EP_SCORE_* */
+    int32_t per_sequence;      /* 1: a pool per sequence, 0: one pool */
+    int32_t logits_dtype;      /* EP_BF16 or EP_F32 */
+    const int32_t *num_tokens; /* device [seqs] or NULL */
+} ep_balance_t;
+
+/* ep_balance_workspace_bytes -- device workspace of ep_balance_loss (host only). */
+int ep_balance_workspace_bytes(const ep_balance_t *args, size_t *bytes);
+
+/*
+ * ep_balance_loss -- the two losses and each pool's counts c_e.
+ *   logits [seqs][tokens][E] logits_dtype; topk_ids [seqs][tokens][top_k] int32
+ *   losses [2] float; counts [seqs][E] int32 with per_sequence, else [E]
+ *   workspace: 16-byte aligned, of the call alone until its kernels are done
+ */
+int ep_balance_loss(const ep_balance_t *args, const void *logits, const int32_t *topk_ids, float *losses,
+                    int32_t *counts, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ep_balance_loss_backward -- the logits' gradient for dlosses [2] (device), the counts that
+ * ep_balance_loss wrote held fixed; zero past num_tokens. With accumulate 1 it is added to
+ * what dlogits (like logits) holds, and rows past num_tokens are left as they are.
+ */
+int ep_balance_loss_backward(const ep_balance_t *args, const float *dlosses, const void *logits,
+                             const int32_t *counts, int32_t accumulate, void *dlogits, void *stream);
+
+/* All three: pointers aligned to their element. Host-side errors: EP_ERR_INVALID_ARG,
+ * EP_ERR_WORKSPACE, EP_ERR_CUDA. */
+
+/* -------------------------------------------------------- the gradients' norm and clipping */
+typedef struct ep_grads {      /* host arrays of n entries each */
+    int32_t n;                 /* tensors, >= 0 */
+    const void *const *grads;  /* device, aligned to their element */
+    void *const *out;          /* device, or NULL: clipped in place */
+    const int64_t *numel;      /* elements, 0..2^44 - 1 */
+    const int32_t *dtypes;     /* EP_BF16 or EP_F32, of grads[i] and out[i] */
+} ep_grads_t;
+
+/* ep_clip_workspace_bytes -- device workspace of ep_clip_grad_norm (host only). */
+int ep_clip_workspace_bytes(const ep_grads_t *args, size_t *bytes);
+
+/*
+ * ep_clip_grad_norm -- *norm (device) = the square root of the sum of all elements' squares,
+ * and out[i] = grads[i] * max_norm / norm where norm is finite and above max_norm (>= 0; infinity:
+ * the norm alone), else grads[i] unchanged. In place nothing is written then. The sum neither
+ * overflows nor underflows where the elements do not, and does not depend on the order of
+ * execution. out[i] may be grads[i]; no other two tensors may overlap (refused). The arrays are
+ * read before the call returns. The workspace is 16-byte aligned and of the call alone until
+ * its kernels are done. Tensors whose grads[i] and out[i] differ in their address modulo 16
+ * take several times as long.
+ * Host-side errors: EP_ERR_INVALID_ARG, EP_ERR_WORKSPACE, EP_ERR_CUDA.
+ */
+int ep_clip_grad_norm(const ep_grads_t *args, float max_norm, float *norm, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
