@@ -12,5 +12,7 @@ from .product import (act_grad, check_products, experts_product, experts_product
                       set_product_wait_limit)
 from .router import route_topk, route_topk_backward  # noqa: F401
 from .balance import balance_loss, balance_loss_backward  # noqa: F401
+from .product_w4 import (dequantize_weight4, experts_product_w4, linear_w4, pack_weight4,  # noqa: F401
+                         quantize_weight4)
 from .gradnorm import clip_grad_norm  # noqa: F401
 from ._lib import EpError  # noqa: F401

@@ -37,6 +37,8 @@ EP_FP4X2 = 4
 EP_ACT_NONE, EP_ACT_RELU, EP_ACT_SILU, EP_ACT_GELU, EP_ACT_GELU_TANH, EP_ACT_SWIGLU = range(6)
 EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = range(2)
 EP_BIAS_ON_SCORE = 16
+EP_W4_INT4, EP_W4_FP4 = range(2)
+EP_W4_MAX_K = 32768
 
 EP_PATH_FUSED = 0
 EP_PATH_SENDBUF = 1
@@ -107,6 +109,12 @@ class EpTopkC(C.Structure):
                 ("renormalize", C.c_int32), ("logits_dtype", C.c_int32), ("scale", C.c_float)]
 
 
+class EpW4C(C.Structure):
+    _fields_ = [("groups", C.c_int32), ("rows", C.c_int32), ("k", C.c_int32), ("n", C.c_int32),
+                ("act", C.c_int32), ("kind", C.c_int32), ("group", C.c_int32), ("counts", C.c_void_p),
+                ("status", C.c_void_p)]
+
+
 class EpBalanceC(C.Structure):
     _fields_ = [("seqs", C.c_int32), ("tokens", C.c_int32), ("E", C.c_int32), ("top_k", C.c_int32),
                 ("score", C.c_int32), ("per_sequence", C.c_int32), ("logits_dtype", C.c_int32),
@@ -150,6 +158,7 @@ SIGNATURES = {
     "ep_product_wait_limit": (C.c_int, [C.c_int64]),
     "ep_topk_route": (C.c_int, [C.POINTER(EpTopkC)] + [C.c_void_p] * 5),
     "ep_topk_route_backward": (C.c_int, [C.POINTER(EpTopkC)] + [C.c_void_p] * 5),
+    "ep_product_w4": (C.c_int, [C.POINTER(EpW4C)] + [C.c_void_p] * 7),
     "ep_balance_workspace_bytes": (C.c_int, [C.POINTER(EpBalanceC), C.POINTER(C.c_size_t)]),
     "ep_balance_loss": (C.c_int, [C.POINTER(EpBalanceC)] + [C.c_void_p] * 5 + [C.c_size_t, C.c_void_p]),
     "ep_balance_loss_backward": (C.c_int, [C.POINTER(EpBalanceC)] + [C.c_void_p] * 3

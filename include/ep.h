@@ -569,6 +569,47 @@ int ep_product_status(void *stream);
  * (1000..6e10, default 2e9; host only). EP_ERR_INVALID_ARG outside. */
 int ep_product_wait_limit(int64_t ns);
 
+/* -------------------------------------------------- products with 4-bit weights
+ *
+ * ep_product (forward) with weights of 4-bit codes and a bf16 scale for each `group`
+ * consecutive elements of a row: w = bf16(value * scale), rounded once, and then, as there,
+ * out[g][r] = act(x[g][r] . w[g]^T + bias[g]) + residual[g][r], fp32 sums, one rounding. For
+ * serving, where the weights' bytes are what a product with few rows takes.
+ *
+ * Layout of a weight's row of k elements: k / 8 little-endian words of 32 bits; of a word's eight
+ * fields of 4 bits, lowest first, the first four are its elements 0, 2, 4, 6, the others
+ * 1, 3, 5, 7. Scales lie group-major: [k / group][rows of the weight].
+ */
+#define EP_W4_INT4 0 /* a code's value: two's complement, -8..7 */
+#define EP_W4_FP4 1  /* sign, two bits of exponent (bias 1), one of mantissa: 0, .5, 1, 1.5, 2, 3, 4, 6 */
+#define EP_W4_MAX_K 32768
+
+typedef struct ep_w4 {
+    int32_t groups, rows;  /* as in ep_product_t */
+    int32_t k;             /* columns of x: a multiple of group, <= EP_W4_MAX_K (the sum of one output
+                              is a chain of truncated steps, see ep_product's precision) */
+    int32_t n;             /* columns of the product: a multiple of 8, <= 2^24 */
+    int32_t act;           /* EP_ACT_* */
+    int32_t kind;          /* EP_W4_* */
+    int32_t group;         /* elements of k that share a scale: 32, 64 or 128 */
+    const int32_t *counts; /* device [groups] or NULL, as in ep_product_t */
+    int32_t *status;       /* device [1] or NULL, as in ep_product_t */
+} ep_w4_t;
+
+/*
+ * ep_product_w4 -- per group g and row r in use, the product above. Rows not in use are
+ * neither read into a result nor written.
+ *   x        [groups][rows][k] bf16
+ *   codes    [groups][n][k / 2] bytes; EP_ACT_SWIGLU: [groups][2n][k / 2], gate rows first
+ *   scales   [groups][k / group][n] ([2n]) bf16
+ *   bias     [groups][n] ([2n]) bf16, or NULL;  residual [groups][rows][n] bf16, or NULL
+ *   out      [groups][rows][n] bf16
+ * out may be residual itself; no other buffers may overlap. All 16-byte aligned.
+ * Host-side errors: EP_ERR_INVALID_ARG, EP_ERR_CUDA.
+ */
+int ep_product_w4(const ep_w4_t *args, const void *x, const void *codes, const void *scales, const void *bias,
+                  const void *residual, void *out, void *stream);
+
 /* ------------------------------------------------------------------ the router */
 #define EP_SCORE_SOFTMAX 0 /* over the E logits of a token */
 #define EP_SCORE_SIGMOID 1 /* of each logit */
