@@ -25,4 +25,11 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int block, cudaSt
 cudaError_t launch_row_sums(const void *src, const int32_t *counts, int groups, int rows, int n, bool out_f32,
                             bool accumulate, void *out, cudaStream_t st);
 
+// The bound of a product's device-side waits, ns (ep_product_wait_limit).
+uint64_t product_wait_limit();
+
+// What the products with 4-bit weights without a status word have reported on the current
+// device, cleared; waits for the stream.
+int take_w4_status(cudaStream_t st);
+
 }  // namespace ep

@@ -36,6 +36,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "act.cuh"
+#include "tensor_map.cuh"
 
 namespace ep {
 
@@ -921,54 +922,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
 // ------------------------------------------------------------------ host side
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's encoder, looked up once (the library links no driver library).
-EncodeTiled encoder() {
-    static std::atomic<EncodeTiled> found{nullptr};
-    EncodeTiled e = found.load(std::memory_order_acquire);
-    if (e) return e;
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-        return nullptr;
-    e = reinterpret_cast<EncodeTiled>(fn);
-    found.store(e, std::memory_order_release);
-    return e;
-}
-
-// A bf16 tensor of `rank` dimensions (innermost first, strides in elements of
-// dimensions 1..), read in boxes with the 128-byte swizzle and zeros outside.
-bool make_map(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
-              const uint32_t *box) {
-    EncodeTiled enc = encoder();
-    if (!enc) return false;
-    cuuint64_t d[5], s[4];
-    cuuint32_t b[5], one[5];
-    for (int i = 0; i < rank; ++i) {
-        d[i] = dims[i];
-        b[i] = box[i];
-        one[i] = 1;
-        if (i > 0) s[i - 1] = strides[i - 1] * 2;
-    }
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), d, s, b, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// [groups][rows][cols] read in boxes of 64 columns and box_rows rows.
-bool make_map3(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t groups,
-               uint32_t box_rows) {
-    const uint64_t dims[3] = {cols, rows, groups}, strides[2] = {cols, cols * rows};
-    const uint32_t box[3] = {64, box_rows, 1};
-    return make_map(m, base, 3, dims, strides, box);
-}
-
 // The output [groups][rows][halves][lanes], written in boxes of 32 lanes and 32 rows.
 bool make_out_map(CUtensorMap *m, void *out, bool f32, uint64_t halves, uint64_t lanes, uint64_t rows,
                   uint64_t groups) {
@@ -981,19 +934,6 @@ bool make_out_map(CUtensorMap *m, void *out, bool f32, uint64_t halves, uint64_t
     return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, out, dims, strides, box,
                one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The multiprocessor count of the current device.
-cudaError_t sm_count(int *out) {
-    constexpr int kMaxDevices = 64;
-    static std::atomic<int> cached[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < kMaxDevices && (*out = cached[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-    e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess && dev < kMaxDevices) cached[dev].store(*out, std::memory_order_relaxed);
-    return e;
 }
 
 constexpr long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -1205,6 +1145,8 @@ struct Range {
 
 }  // namespace
 
+uint64_t product_wait_limit() { return wait_limit_ns.load(std::memory_order_relaxed); }
+
 }  // namespace ep
 
 using namespace ep;
@@ -1281,7 +1223,8 @@ extern "C" int ep_product_status(void *stream) {
         cudaMemcpyFromSymbolAsync(&status, status_taken, sizeof(status), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)
         return EP_ERR_CUDA;
-    return status;
+    const int of_w4 = take_w4_status(st);
+    return status != EP_OK ? status : of_w4;
 }
 
 extern "C" int ep_product_wait_limit(int64_t ns) {

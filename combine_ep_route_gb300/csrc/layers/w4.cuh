@@ -69,5 +69,6 @@ __device__ __forceinline__ void w4_values(uint32_t word, __nv_bfloat162 scale, u
 }
 
 cudaError_t launch_w4_rows(const W4Params &p, bool fp4, cudaStream_t st);
+int launch_w4_tiles(const W4Params &p, bool fp4, int32_t *status, cudaStream_t st);
 
 }  // namespace ep

@@ -21,6 +21,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 128;     // elements of k that a warp takes at once: 32 per lane of a row's four
+constexpr int kFewRows = 16;   // row slots of a group for which this kernel is the faster one
 constexpr int kFlight = 2;     // steps whose codes are on their way together
 
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -192,5 +193,6 @@ extern "C" int ep_product_w4(const ep_w4_t *a, const void *x, const void *codes,
     p.act = a->act;
     Range range("ep:product_w4");
     const bool fp4 = a->kind == EP_W4_FP4;
+    if (a->rows > kFewRows) return launch_w4_tiles(p, fp4, a->status, static_cast<cudaStream_t>(stream));
     return launch_w4_rows(p, fp4, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }

@@ -1,0 +1,638 @@
+// w4_tiles.cu -- products with 4-bit weights on the 5th-generation tensor cores.
+//
+// D[lane][col] = sum_k w[lane][k] x[col][k]: 128 rows of the weight on the accumulator's lanes,
+// up to 128 rows of x on its columns. The weight is the operand that sits in tensor memory:
+// TMA brings blocks of 128 elements of 4-bit codes and their scales, eight warps make bf16 of
+// them (a lane its own row, 64 bytes of codes at a time) and store them to tensor memory, from
+// where the MMAs read them; x goes by TMA to shared memory with the 128-byte swizzle. So the
+// expanded weight never passes through shared memory, whose bandwidth the MMAs' other operand
+// needs. A gated product's gate and up rows are interleaved by eights by the tensor maps alone.
+//
+// One persistent CTA per SM: a TMA warp for the codes and scales, one for x, an MMA warp, two
+// groups of four warps that expand every other block each, and four epilogue warps that drain
+// one accumulator while the next fills. Dense products with few tiles let up to four CTAs of a
+// cluster share a tile's reduction and join their sums through distributed shared memory.
+#include "w4.cuh"
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "act.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.cuh"
+
+namespace ep {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kLanes = 128;          // weight rows of a tile
+constexpr int kBlock = 128;          // elements of k of a block
+constexpr int kColMax = 128;         // rows of x of a tile, at most
+constexpr int kBoxes = kColMax / 16;
+constexpr int kABuffers = 4;         // blocks of the weight in tensor memory
+constexpr int kACols = kBlock / 2;   // its columns: two elements to one
+constexpr int kTmemCols = 512;       // two accumulators, four blocks of the weight
+constexpr int kABase = 2 * kColMax;
+constexpr int kCodeBytes = kLanes * kBlock / 2;
+constexpr int kCodeSlot = kCodeBytes + 1024;   // with the scales: four times 128 at most
+constexpr int kMaxCodeSlots = 12;
+constexpr int kMaxXSlots = 12;
+constexpr int kMaxSplit = 4;
+constexpr uint32_t kSleepNs = 1000000;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+__device__ int32_t w4_status, w4_status_taken;
+
+__global__ void take_status() { w4_status_taken = atomicExch(&w4_status, 0); }
+
+struct TileParams {
+    CUtensorMap codes, scales;
+    CUtensorMap x[kBoxes];    // boxes of 16, 32, ... 128 rows
+    W4Params w;
+    int lane_step, lane_tiles;       // output features of a tile, tiles per group
+    int col_max;                     // widest column tile
+    int code_slots, x_slots, x_bytes;   // rings; bytes of an x slot
+    int scale_bytes;                 // of a block
+    int blocks, split;
+    int32_t *status;
+    uint64_t wait_limit_ns;
+    uint32_t sleep_ns;
+};
+
+struct Shared {
+    uint64_t code_full[kMaxCodeSlots], code_empty[kMaxCodeSlots];
+    uint64_t x_full[kMaxXSlots], x_empty[kMaxXSlots];
+    uint64_t a_full[kABuffers], a_empty[kABuffers];
+    uint64_t acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort;
+    int count[EP_MAX_E];             // rows in use, of the groups in the order they are worked on
+    int first[EP_MAX_E + 1];         // column tiles before it
+    uint16_t group[EP_MAX_E];
+};
+
+constexpr size_t kSmemMax = 227 * 1024;
+constexpr size_t kRingSpace = (kSmemMax - 1024 - sizeof(Shared)) / 1024 * 1024;
+
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int slots) {
+        if (++s == slots) s = 0, phase ^= 1;
+    }
+};
+
+// D (+)= A * B over 16 elements, A from tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// A bounded wait, cut short once any role of the CTA has given up.
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Shared *sh, const TileParams &p) {
+    if (mbar_try_wait_ns(bar, parity, p.sleep_ns)) return true;
+    const uint64_t t0 = global_ns();
+    volatile int *abort = &sh->abort;
+    while (!mbar_try_wait_ns(bar, parity, p.sleep_ns)) {
+        if (*abort) return false;
+        if (global_ns() - t0 > p.wait_limit_ns) {
+            *abort = 1;
+            atomicCAS(p.status ? p.status : &w4_status, 0, EP_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+// The same by a whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Shared *sh, const TileParams &p) {
+    return __all_sync(kAll, role_wait(bar, parity, sh, p));
+}
+
+// Columns of each of ct tiles over `all` > 0 columns: 130 rows make 80 and 50, not 128 and 2.
+__device__ __forceinline__ int tile_width(int all, int ct) { return ((all - 1) / ct + 16) / 16 * 16; }
+
+// The groups' row counts, dearest tiles first, so that the last round is a cheap one. Ends in a barrier.
+__device__ __forceinline__ void order_groups(const TileParams &p, Shared *sh) {
+    const int own = threadIdx.x, groups = p.w.groups;
+    const int32_t *counts = p.w.counts;
+    if (groups > kThreads || !counts) {
+        for (int g = own; g < groups; g += kThreads) {
+            sh->count[g] = counts ? max(0, min(counts[g], p.w.rows)) : p.w.rows;
+            sh->group[g] = (uint16_t)g;
+        }
+        __syncthreads();
+        return;
+    }
+    int count = 0;
+    if (own < groups) {
+        count = max(0, min(counts[own], p.w.rows));
+        sh->first[own] = min(count, kColMax);
+    }
+    __syncthreads();
+    if (own < groups) {
+        const int key = min(count, kColMax);
+        int ahead = 0;
+        for (int g = 0; g < groups; ++g) {
+            const int other = sh->first[g];
+            ahead += other > key || (other == key && g < own);
+        }
+        sh->count[ahead] = count;
+        sh->group[ahead] = (uint16_t)own;
+    }
+    __syncthreads();
+}
+
+struct Tile {
+    int g, lane0;            // group, first output feature
+    int col0, cols, n_mma;   // first row of x, rows in use, columns of the MMA
+};
+struct Walk {
+    int at = -1, begin = 0, end = 0;   // the current group's place, its tiles [begin, end)
+    int ct = 0, width = 0;
+};
+
+// Column tiles innermost: the CTAs that share a lane tile's weight work at the same time, so
+// all but one find it in L2.
+__device__ __forceinline__ Tile find_tile(const TileParams &p, const Shared *sh, int t, Walk &w) {
+    if (t >= w.end) {
+        do {
+            ++w.at;
+            w.begin = w.end;
+            w.end = sh->first[w.at + 1] * p.lane_tiles;
+        } while (t >= w.end);
+        w.ct = sh->first[w.at + 1] - sh->first[w.at];
+        w.width = tile_width(sh->count[w.at], w.ct);
+    }
+    const int r = t - w.begin, lt = w.ct == 1 ? r : r / w.ct, c = r - lt * w.ct;
+    Tile x;
+    x.g = sh->group[w.at];
+    x.lane0 = lt * p.lane_step;
+    x.col0 = c * w.width;
+    x.cols = min(w.width, sh->count[w.at] - x.col0);
+    x.n_mma = (x.cols + 15) / 16 * 16;
+    return x;
+}
+
+// 32 columns of one warp's 32 lanes: bias, activation, residual, out. n of them are rows in use.
+template <bool GATED>
+__device__ __forceinline__ void epilogue_chunk(const TileParams &p, float (&v)[32], size_t row0, int n, int quad, int lane,
+                                               int lane0, float bias) {
+    const W4Params &w = p.w;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += bias;
+    if (GATED) {
+        // lanes 0-7 and 16-23 hold gates, eight lanes on their ups: gate lanes end with the even
+        // columns, up lanes with the odd ones
+        const bool up = lane & 8;
+        const int f = lane0 + quad * 16 + (lane >> 4) * 8 + (lane & 7);
+        if (w.residual == nullptr) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float got = __shfl_xor_sync(kAll, up ? v[2 * i] : v[2 * i + 1], 8);
+                const float y = act_value(up ? got : v[2 * i], EP_ACT_SILU) * (up ? v[2 * i + 1] : got);
+                if (f < w.n && 2 * i + up < n) w.out[(row0 + 2 * i + up) * w.n + f] = __float2bfloat16_rn(y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float got = __shfl_xor_sync(kAll, up ? v[2 * i] : v[2 * i + 1], 8);
+                const float y = act_value(up ? got : v[2 * i], EP_ACT_SILU) * (up ? v[2 * i + 1] : got);
+                const size_t at = (row0 + 2 * i + up) * w.n + f;
+                if (f < w.n && 2 * i + up < n) w.out[at] = __float2bfloat16_rn(y + __bfloat162float(w.residual[at]));
+            }
+        }
+        return;
+    }
+    switch (w.act) {
+        case EP_ACT_RELU:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], EP_ACT_RELU);
+            break;
+        case EP_ACT_SILU:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], EP_ACT_SILU);
+            break;
+        case EP_ACT_GELU:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], EP_ACT_GELU);
+            break;
+        case EP_ACT_GELU_TANH:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], EP_ACT_GELU_TANH);
+            break;
+        default: break;
+    }
+    // neighbours trade, so that even lanes hold a pair of features of the even columns, odd
+    // lanes of the odd ones
+    const bool odd = lane & 1;
+    const int f = lane0 + quad * 32 + (lane & ~1);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float got = __shfl_xor_sync(kAll, odd ? v[2 * i] : v[2 * i + 1], 1);
+        float lo = odd ? got : v[2 * i], hi = odd ? v[2 * i + 1] : got;
+        if (f >= w.n || 2 * i + odd >= n) continue;
+        const size_t at = (row0 + 2 * i + odd) * w.n + f;
+        if (w.residual) {
+            const float2 r = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(w.residual + at));
+            lo += r.x, hi += r.y;
+        }
+        *reinterpret_cast<uint32_t *>(w.out + at) = pack_bf16x2_rn(lo, hi);
+    }
+}
+
+template <bool GATED>
+__device__ __forceinline__ float bias_of(const TileParams &p, const Tile &x, int quad, int lane) {
+    if (!p.w.bias) return 0.f;
+    const int f = GATED ? x.lane0 + quad * 16 + (lane >> 4) * 8 + (lane & 7) : x.lane0 + quad * 32 + lane;
+    if (f >= p.w.n) return 0.f;
+    return __bfloat162float(p.w.bias[(size_t)x.g * p.w.wide + (GATED && (lane & 8) ? p.w.n : 0) + f]);
+}
+
+template <bool FP4, bool GATED>
+__global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_constant__ TileParams p) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *rings = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *xs = rings, *cs = rings + (size_t)p.x_slots * p.x_bytes;
+    Shared *sh = reinterpret_cast<Shared *>(rings + kRingSpace);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = p.split > 1 ? cluster_rank() : 0;
+    const int t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.code_slots; ++s) {
+            mbar_init(&sh->code_full[s], 1);
+            mbar_init(&sh->code_empty[s], 4);   // the four warps that expand it
+        }
+        for (int s = 0; s < p.x_slots; ++s) {
+            mbar_init(&sh->x_full[s], 1);
+            mbar_init(&sh->x_empty[s], 1);
+        }
+        for (int a = 0; a < kABuffers; ++a) {
+            mbar_init(&sh->a_full[a], 4);
+            mbar_init(&sh->a_empty[a], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&sh->acc_full[a], 1);
+            mbar_init(&sh->acc_empty[a], 4);
+        }
+        mbar_init(&sh->drain, 1);
+        sh->abort = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&p.codes);
+        tma_prefetch_map(&p.scales);
+    }
+    if (warp == 2) tmem_alloc<1>(&sh->tmem, kTmemCols);
+    pdl_wait();   // nothing above reads or writes global memory
+    pdl_launch_dependents();
+    order_groups(p, sh);
+    if (warp == 0) {   // exclusive prefix of the groups' column tiles
+        int base = 0;
+        for (int g0 = 0; g0 < p.w.groups; g0 += 32) {
+            const int g = g0 + lane;
+            const int own = g < p.w.groups ? (sh->count[g] + p.col_max - 1) / p.col_max : 0;
+            int sum = own;
+            for (int d = 1; d < 32; d *= 2) {
+                const int v = __shfl_up_sync(kAll, sum, d);
+                if (lane >= d) sum += v;
+            }
+            if (g < p.w.groups) sh->first[g] = base + sum - own;
+            base += __shfl_sync(kAll, sum, 31);
+        }
+        if (lane == 0) sh->first[p.w.groups] = base;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const int total = sh->first[p.w.groups] * p.lane_tiles;
+    const uint32_t tmem = sh->tmem;
+    const int lo = p.blocks * (int)rank / p.split, hi = p.blocks * ((int)rank + 1) / p.split;
+
+    Walk walk;
+    Ring ring;
+    int issued = 0;   // producers: blocks so far
+    bool ok = true;
+    if (warp == 0) {
+        // ---- TMA: codes and scales
+        for (int t = t0; t < total && ok; t += t_step) {
+            const Tile x = find_tile(p, sh, t, walk);
+            for (int kb = lo; kb < hi; ++kb, ++issued, ring.next(p.code_slots)) {
+                ok = warp_wait(&sh->code_empty[ring.s], ring.phase ^ 1, sh, p);
+                if (!ok) break;
+                if (elect_one()) {
+                    uint64_t *full = &sh->code_full[ring.s];
+                    mbar_arrive_expect_tx(full, kCodeBytes + p.scale_bytes);
+                    const uint32_t bar = smem_u32(full);
+                    uint8_t *dst = cs + ring.s * kCodeSlot;
+                    const int group0 = (kb * kBlock) >> p.w.group_shift;
+                    if (GATED) {
+                        tma_load_5d<1>(dst, &p.codes, kb * (kBlock / 2), 0, 0, x.lane0 / 8, x.g, bar);
+                        tma_load_5d<1>(dst + kCodeBytes, &p.scales, 0, 0, x.lane0 / 8, group0, x.g, bar);
+                    } else {
+                        tma_load_3d<1>(dst, &p.codes, kb * (kBlock / 2), x.lane0, x.g, bar);
+                        tma_load_3d<1>(dst + kCodeBytes, &p.scales, x.lane0, group0, x.g, bar);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp == 3) {
+        // ---- TMA: rows of x
+        for (int t = t0; t < total && ok; t += t_step) {
+            const Tile x = find_tile(p, sh, t, walk);
+            for (int kb = lo; kb < hi; ++kb, ++issued, ring.next(p.x_slots)) {
+                ok = warp_wait(&sh->x_empty[ring.s], ring.phase ^ 1, sh, p);
+                if (!ok) break;
+                if (elect_one()) {
+                    uint64_t *full = &sh->x_full[ring.s];
+                    const int subs = p.w.k - kb * kBlock > 64 ? 2 : 1;
+                    mbar_arrive_expect_tx(full, subs * x.n_mma * 128);
+                    const CUtensorMap *map = &p.x[x.n_mma / 16 - 1];
+                    for (int i = 0; i < subs; ++i)
+                        tma_load_3d<1>(xs + (size_t)ring.s * p.x_bytes + i * x.n_mma * 128, map, kb * kBlock + i * 64, x.col0,
+                                       x.g, smem_u32(full));
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp == 1) {
+        // ---- MMA: one thread issues a block's steps of 16
+        int acc = 0, a = 0;
+        uint32_t acc_phase = 0, a_phase = 0;
+        for (int t = t0; t < total && ok; t += t_step) {
+            const Tile x = find_tile(p, sh, t, walk);
+            if (lo == hi) continue;
+            const uint32_t idesc = mma_idesc(kLanes, x.n_mma, false, false), d = tmem + acc * kColMax;
+            ok = warp_wait(&sh->acc_empty[acc], ((acc_phase >> acc) & 1) ^ 1, sh, p);
+            if (!ok) break;
+            acc_phase ^= 1u << acc;
+            for (int kb = lo; kb < hi; ++kb, ring.next(p.x_slots)) {
+                ok = warp_wait(&sh->x_full[ring.s], ring.phase, sh, p) && warp_wait(&sh->a_full[a], a_phase, sh, p);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t sx = smem_u32(xs + (size_t)ring.s * p.x_bytes);
+                    const uint32_t from = tmem + kABase + a * kACols;
+                    const int steps = min(kBlock, p.w.k - kb * kBlock) / 16;
+                    const uint64_t b0 = smem_desc(sx, 16, 1024), b1 = smem_desc(sx + x.n_mma * 128, 16, 1024);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < steps) mma_ts(d, from + i * 8, (i < 4 ? b0 : b1) + 2 * (i % 4), idesc, kb > lo || i > 0);
+                    mma_commit<1>(&sh->x_empty[ring.s]);
+                    mma_commit<1>(&sh->a_empty[a]);
+                }
+                __syncwarp();
+                if (++a == kABuffers) a = 0, a_phase ^= 1;
+            }
+            if (!ok) break;
+            if (elect_one()) mma_commit<1>(&sh->acc_full[acc]);
+            __syncwarp();
+            acc ^= 1;
+        }
+    } else if (warp >= 4 && warp < 12) {
+        // ---- codes to bf16, from shared to tensor memory; the two groups take turns
+        const int turn = (warp - 4) / 4, quad = warp % 4, row = quad * 32 + lane;
+        int a = 0, b = 0;   // b: blocks so far, whose lowest bits say whose turn it is
+        uint32_t a_phase = 0;
+        for (int t = t0; t < total && ok; t += t_step) {
+            for (int kb = lo; kb < hi; ++kb, ++b) {
+                if ((b & 1) == turn) {
+                    ok = warp_wait(&sh->code_full[ring.s], ring.phase, sh, p);
+                    if (!ok) break;
+                    const uint8_t *slot = cs + ring.s * kCodeSlot;
+                    uint4 c[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)   // (the 64-byte swizzle)
+                        c[i] = *reinterpret_cast<const uint4 *>(slot + row * 64 + ((i ^ ((row >> 1) & 3)) << 4));
+                    __nv_bfloat162 scale[4];
+                    const __nv_bfloat16 *sc = reinterpret_cast<const __nv_bfloat16 *>(slot + kCodeBytes) + row;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        scale[i] = __bfloat162bfloat162(sc[((i * 32) >> p.w.group_shift) * kLanes]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->code_empty[ring.s]);
+                    ok = warp_wait(&sh->a_empty[a], a_phase ^ 1, sh, p);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t to = tmem + kABase + a * kACols + ((uint32_t)(quad * 32) << 16);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[32];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 v = c[2 * h + i];
+                            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                uint32_t pair[4];
+                                w4_values<FP4>(words[q], scale[2 * h + i], pair);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) r[i * 16 + q * 4 + j] = pair[j];
+                            }
+                        }
+                        tmem_st32(to + h * 32, r);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->a_full[a]);
+                }
+                ring.next(p.code_slots);
+                if (++a == kABuffers) a = 0, a_phase ^= 1;
+            }
+        }
+    } else if (warp >= 12) {
+        // ---- epilogue
+        const int quad = warp % 4;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int t = t0; t < total && ok; t += t_step) {
+            const Tile x = find_tile(p, sh, t, walk);
+            const float bias = bias_of<GATED>(p, x, quad, lane);
+            const size_t row0 = (size_t)x.g * p.w.rows + x.col0;
+            if (lo < hi) {
+                ok = warp_wait(&sh->acc_full[acc], (acc_phase >> acc) & 1, sh, p);
+                if (!ok) break;
+                acc_phase ^= 1u << acc;
+                tc_fence_after();
+            }
+            const uint32_t from = tmem + acc * kColMax + ((uint32_t)(quad * 32) << 16);
+            for (int c = 0; c < x.cols; c += 32) {
+                float v[32];
+                if (lo < hi) {
+                    uint32_t r[32];
+                    tmem_ld32(from + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                }
+                if (p.split > 1) {   // to shared memory, [column][lane]; joined below
+                    float *part = reinterpret_cast<float *>(rings) + quad * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j < x.cols) part[(c + j) * kLanes] = v[j];
+                } else {
+                    if (c + 32 >= x.cols) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
+                    }
+                    epilogue_chunk<GATED>(p, v, row0 + c, min(32, x.cols - c), quad, lane, x.lane0, bias);
+                }
+            }
+            acc ^= 1;
+        }
+    }
+    __syncthreads();
+    if (sh->abort && threadIdx.x < 128) {
+        // a wait ran out: let the copies and MMAs in flight finish (bounded) before shared and
+        // tensor memory are given up
+        const uint64_t since = global_ns();
+        if (threadIdx.x == 0 || threadIdx.x == 96) {
+            const int slots = threadIdx.x == 0 ? p.code_slots : p.x_slots;
+            uint64_t *full = threadIdx.x == 0 ? sh->code_full : sh->x_full;
+            for (int i = max(0, issued - slots); i < issued; ++i)
+                while (!mbar_try_wait(&full[i % slots], (uint32_t)(i / slots) & 1) && global_ns() - since < 100000000ull)
+                    ;
+        } else if (threadIdx.x == 32) {
+            mma_commit<1>(&sh->drain);
+            while (!mbar_try_wait(&sh->drain, 0) && global_ns() - since < 100000000ull)
+                ;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (p.split > 1) {
+        // ---- a shared tile: every CTA has its sums in shared memory; each adds up its share of
+        // the columns, in rank order, and finishes them
+        cluster_sync();
+        if (t0 < total && warp >= 12) {
+            const int quad = warp % 4;
+            walk = Walk();
+            const Tile x = find_tile(p, sh, t0, walk);
+            const float bias = bias_of<GATED>(p, x, quad, lane);
+            const size_t row0 = (size_t)x.g * p.w.rows + x.col0;
+            const int share = (x.cols + p.split - 1) / p.split, c1 = min(x.cols, ((int)rank + 1) * share);
+            for (int c = (int)rank * share; c < c1; c += 32) {
+                const int n = min(32, c1 - c);
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                for (int i = 0; i < p.split; ++i) {
+                    const uint32_t part = map_rank(reinterpret_cast<float *>(rings) + c * kLanes + quad * 32 + lane, i);
+                    float got[32];   // all loads on their way before the first is used
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) got[j] = j < n ? ld_cluster_f32(part + j * kLanes * 4) : 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] += got[j];
+                }
+                epilogue_chunk<GATED>(p, v, row0 + c, n, quad, lane, x.lane0, bias);
+            }
+        }
+        cluster_sync();   // no CTA leaves while another reads its shared memory
+    }
+    tc_fence_after();
+    if (warp == 2) tmem_free<1>(tmem, kTmemCols);
+}
+
+constexpr long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+template <bool FP4, bool GATED>
+cudaError_t launch(const TileParams &p, long long clusters, cudaStream_t st) {
+    const auto kernel = &w4_tiles_kernel<FP4, GATED>;
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kernel), kSmemMax);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * p.split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemMax;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+int launch_w4_tiles(const W4Params &w, bool fp4, int32_t *status, cudaStream_t st) {
+    const bool gated = w.act == EP_ACT_SWIGLU;
+    TileParams p = {};
+    p.w = w;
+    p.status = status;
+    int sms = 0;
+    if (sm_count(&sms) != cudaSuccess) return EP_ERR_CUDA;
+    p.wait_limit_ns = product_wait_limit();
+    p.sleep_ns = p.wait_limit_ns < kSleepNs ? (uint32_t)p.wait_limit_ns : kSleepNs;
+    p.lane_step = gated ? kLanes / 2 : kLanes;
+    p.lane_tiles = (int)ceil_div(w.n, p.lane_step);
+    p.col_max = w.rows < kColMax ? (int)ceil_div(w.rows, 16) * 16 : kColMax;
+    p.blocks = (int)ceil_div(w.k, kBlock);
+    const long long most = (long long)p.lane_tiles * w.groups * ceil_div(w.rows, p.col_max);
+    if (most >= (1LL << 30)) return EP_ERR_INVALID_ARG;   // tile numbers stay within int
+    // dense products with few tiles share each one's reduction (clusters of four fill 144 SMs)
+    p.split = 1;
+    if (!w.counts)
+        while (p.split < kMaxSplit && most * p.split * 2 <= sms - sms / 16 && p.blocks >= 4 * p.split) p.split *= 2;
+    p.x_bytes = p.col_max * kBlock * 2;
+    p.scale_bytes = kLanes * 2 * (kBlock >> w.group_shift);
+    // the rings: half of the codes' slots first, then x, then what is left
+    p.code_slots = 8;
+    p.x_slots = (int)(kRingSpace - p.code_slots * kCodeSlot) / p.x_bytes;
+    if (p.x_slots > kMaxXSlots) p.x_slots = kMaxXSlots;
+    p.code_slots = (int)(kRingSpace - (size_t)p.x_slots * p.x_bytes) / kCodeSlot;
+    if (p.code_slots > kMaxCodeSlots) p.code_slots = kMaxCodeSlots;
+    const uint64_t K = w.k, N = w.n, W = w.wide, G = w.groups, parts = K >> w.group_shift;
+    const uint32_t per_block = kBlock >> w.group_shift;
+    bool good;
+    if (gated) {
+        // gate and up rows by turns of eight: 8 rows x (gate, up) x n / 8
+        const uint64_t dims[5] = {K / 2, 8, 2, N / 8, G}, strides[4] = {K / 2, N * K / 2, 8 * K / 2, 2 * N * K / 2};
+        const uint32_t box[5] = {kBlock / 2, 8, 2, 8, 1};
+        const uint64_t sdims[5] = {8, 2, N / 8, parts, G}, sstrides[4] = {N, 8, W, W * parts};
+        const uint32_t sbox[5] = {8, 2, 8, per_block, 1};
+        good = make_map(&p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.codes, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B) &&
+               make_map(&p.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w.scales, 5, sdims, sstrides, sbox,
+                        CU_TENSOR_MAP_SWIZZLE_NONE);
+    } else {
+        const uint64_t dims[3] = {K / 2, N, G}, strides[2] = {K / 2, N * K / 2};
+        const uint32_t box[3] = {kBlock / 2, kLanes, 1};
+        const uint64_t sdims[3] = {N, parts, G}, sstrides[2] = {N, N * parts};
+        const uint32_t sbox[3] = {kLanes, per_block, 1};
+        good = make_map(&p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.codes, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B) &&
+               make_map(&p.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w.scales, 3, sdims, sstrides, sbox,
+                        CU_TENSOR_MAP_SWIZZLE_NONE);
+    }
+    for (int i = 0; good && i < p.col_max / 16; ++i)
+        good = make_map3(&p.x[i], w.x, K, w.rows, G, 16u * (i + 1));
+    if (!good) return EP_ERR_CUDA;
+    const long long clusters = p.split > 1 || most < sms ? most : sms;
+    cudaError_t e;
+    if (gated)
+        e = fp4 ? launch<true, true>(p, clusters, st) : launch<false, true>(p, clusters, st);
+    else
+        e = fp4 ? launch<true, false>(p, clusters, st) : launch<false, false>(p, clusters, st);
+    return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+}
+
+int take_w4_status(cudaStream_t st) {
+    int32_t status = 0;
+    take_status<<<1, 1, 0, st>>>();
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyFromSymbolAsync(&status, w4_status_taken, sizeof(status), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return EP_ERR_CUDA;
+    return status;
+}
+
+}  // namespace ep
