@@ -24,19 +24,20 @@ namespace ep {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kTurns = 4;            // groups of four warps that expand blocks by turns
+constexpr int kThreads = 128 + kTurns * 128 + 128;
+constexpr int kFirstEpilogue = 4 + kTurns * 4;
 constexpr int kLanes = 128;          // weight rows of a tile
-constexpr int kBlock = 128;          // elements of k of a block
+constexpr int kBlock = 128;          // elements of k of a block of codes
+constexpr int kStep = 2 * kBlock;    // and of what the MMA thread waits for and issues at once
 constexpr int kColMax = 128;         // rows of x of a tile, at most
 constexpr int kBoxes = kColMax / 16;
-constexpr int kABuffers = 4;         // blocks of the weight in tensor memory
-constexpr int kACols = kBlock / 2;   // its columns: two elements to one
-constexpr int kTmemCols = 512;       // two accumulators, four blocks of the weight
-constexpr int kABase = 2 * kColMax;
+constexpr int kACols = kStep / 2;    // tensor-memory columns of a step: two elements to one
+constexpr int kTmemCols = 512;       // two accumulators, then steps of the weight
+constexpr int kMaxSlots = (kTmemCols - 2 * 32) / kACols;
 constexpr int kCodeBytes = kLanes * kBlock / 2;
 constexpr int kCodeSlot = kCodeBytes + 1024;   // with the scales: four times 128 at most
 constexpr int kMaxCodeSlots = 12;
-constexpr int kMaxXSlots = 12;
 constexpr int kMaxSplit = 4;
 constexpr uint32_t kSleepNs = 1000000;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -51,9 +52,11 @@ struct TileParams {
     W4Params w;
     int lane_step, lane_tiles;       // output features of a tile, tiles per group
     int col_max;                     // widest column tile
-    int code_slots, x_slots, x_bytes;   // rings; bytes of an x slot
+    int code_slots;                  // ring of codes and scales
+    int slots, x_bytes;              // ring of steps, expanded weight and x; bytes of an x slot
+    int acc_stride;                  // columns of an accumulator
     int scale_bytes;                 // of a block
-    int blocks, split;
+    int steps, split;                // steps of k; CTAs of a cluster that share them
     int32_t *status;
     uint64_t wait_limit_ns;
     uint32_t sleep_ns;
@@ -61,8 +64,7 @@ struct TileParams {
 
 struct Shared {
     uint64_t code_full[kMaxCodeSlots], code_empty[kMaxCodeSlots];
-    uint64_t x_full[kMaxXSlots], x_empty[kMaxXSlots];
-    uint64_t a_full[kABuffers], a_empty[kABuffers];
+    uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
@@ -80,7 +82,24 @@ struct Ring {
     __device__ __forceinline__ void next(int slots) {
         if (++s == slots) s = 0, phase ^= 1;
     }
+    __device__ __forceinline__ void skip(int n, int slots) {   // n <= slots
+        s += n;
+        if (s >= slots) s -= slots, phase ^= 1;
+    }
 };
+
+// 32 weights from 16 bytes of codes.
+template <bool FP4, bool LARGE>
+__device__ __forceinline__ void expand(uint4 c, const W4Scale<FP4> &scale, uint32_t *r) {
+    const uint32_t words[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t pair[4];
+        w4_values<FP4, LARGE>(words[q], scale, pair);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[q * 4 + j] = pair[j];
+    }
+}
 
 // D (+)= A * B over 16 elements, A from tensor memory.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
@@ -109,6 +128,14 @@ __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Shared
 // The same by a whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Shared *sh, const TileParams &p) {
     return __all_sync(kAll, role_wait(bar, parity, sh, p));
+}
+
+// Waits (bounded) for the MMAs that this thread has issued.
+__device__ __forceinline__ void drain_mma(Shared *sh) {
+    const uint64_t since = global_ns();
+    mma_commit<1>(&sh->drain);
+    while (!mbar_try_wait(&sh->drain, 0) && global_ns() - since < 100000000ull)
+        ;
 }
 
 // Columns of each of ct tiles over `all` > 0 columns: 130 rows make 80 and 50, not 128 and 2.
@@ -176,70 +203,52 @@ __device__ __forceinline__ Tile find_tile(const TileParams &p, const Shared *sh,
     return x;
 }
 
+template <int ACT>
+__device__ __forceinline__ void act_all(float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], ACT);
+}
+
 // 32 columns of one warp's 32 lanes: bias, activation, residual, out. n of them are rows in use.
+// Lanes first trade columns with a partner, so that each ends with 16 columns: of a gated product
+// gate lanes (0-7, 16-23) take the even ones' ups from the lanes eight further and give the odd
+// ones' gates; otherwise neighbours end with two features of the even or the odd columns.
 template <bool GATED>
 __device__ __forceinline__ void epilogue_chunk(const TileParams &p, float (&v)[32], size_t row0, int n, int quad, int lane,
                                                int lane0, float bias) {
     const W4Params &w = p.w;
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] += bias;
-    if (GATED) {
-        // lanes 0-7 and 16-23 hold gates, eight lanes on their ups: gate lanes end with the even
-        // columns, up lanes with the odd ones
-        const bool up = lane & 8;
-        const int f = lane0 + quad * 16 + (lane >> 4) * 8 + (lane & 7);
-        if (w.residual == nullptr) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float got = __shfl_xor_sync(kAll, up ? v[2 * i] : v[2 * i + 1], 8);
-                const float y = act_value(up ? got : v[2 * i], EP_ACT_SILU) * (up ? v[2 * i + 1] : got);
-                if (f < w.n && 2 * i + up < n) w.out[(row0 + 2 * i + up) * w.n + f] = __float2bfloat16_rn(y);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float got = __shfl_xor_sync(kAll, up ? v[2 * i] : v[2 * i + 1], 8);
-                const float y = act_value(up ? got : v[2 * i], EP_ACT_SILU) * (up ? v[2 * i + 1] : got);
-                const size_t at = (row0 + 2 * i + up) * w.n + f;
-                if (f < w.n && 2 * i + up < n) w.out[at] = __float2bfloat16_rn(y + __bfloat162float(w.residual[at]));
-            }
+    if (!GATED) {
+        switch (w.act) {
+            case EP_ACT_RELU: act_all<EP_ACT_RELU>(v); break;
+            case EP_ACT_SILU: act_all<EP_ACT_SILU>(v); break;
+            case EP_ACT_GELU: act_all<EP_ACT_GELU>(v); break;
+            case EP_ACT_GELU_TANH: act_all<EP_ACT_GELU_TANH>(v); break;
+            default: break;
         }
-        return;
     }
-    switch (w.act) {
-        case EP_ACT_RELU:
+    const bool odd = GATED ? lane & 8 : lane & 1;
+    const int f = GATED ? lane0 + quad * 16 + (lane >> 4) * 8 + (lane & 7) : lane0 + quad * 32 + (lane & ~1);
+    const int last = f < w.n ? n - odd : 0;   // this lane's columns are those of 0, 2, .. below it
+    const size_t step = 2 * (size_t)w.n, at = (row0 + odd) * w.n + f;
+    __nv_bfloat16 *out = w.out + at;
+    const __nv_bfloat16 *residual = w.residual ? w.residual + at : nullptr;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], EP_ACT_RELU);
-            break;
-        case EP_ACT_SILU:
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], EP_ACT_SILU);
-            break;
-        case EP_ACT_GELU:
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], EP_ACT_GELU);
-            break;
-        case EP_ACT_GELU_TANH:
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], EP_ACT_GELU_TANH);
-            break;
-        default: break;
-    }
-    // neighbours trade, so that even lanes hold a pair of features of the even columns, odd
-    // lanes of the odd ones
-    const bool odd = lane & 1;
-    const int f = lane0 + quad * 32 + (lane & ~1);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float got = __shfl_xor_sync(kAll, odd ? v[2 * i] : v[2 * i + 1], 1);
+    for (int i = 0; i < 16; ++i, out += step) {
+        const float got = __shfl_xor_sync(kAll, odd ? v[2 * i] : v[2 * i + 1], GATED ? 8 : 1);
         float lo = odd ? got : v[2 * i], hi = odd ? v[2 * i + 1] : got;
-        if (f >= w.n || 2 * i + odd >= n) continue;
-        const size_t at = (row0 + 2 * i + odd) * w.n + f;
-        if (w.residual) {
-            const float2 r = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(w.residual + at));
-            lo += r.x, hi += r.y;
+        if (GATED) {
+            lo = act_value(lo, EP_ACT_SILU) * hi;
+            if (residual && 2 * i < last) lo += __bfloat162float(residual[i * step]);
+            if (2 * i < last) *out = __float2bfloat16_rn(lo);
+        } else {
+            if (residual && 2 * i < last) {
+                const float2 r = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(residual + i * step));
+                lo += r.x, hi += r.y;
+            }
+            if (2 * i < last) *reinterpret_cast<uint32_t *>(out) = pack_bf16x2_rn(lo, hi);
         }
-        *reinterpret_cast<uint32_t *>(w.out + at) = pack_bf16x2_rn(lo, hi);
     }
 }
 
@@ -255,7 +264,7 @@ template <bool FP4, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_constant__ TileParams p) {
     extern __shared__ uint8_t raw[];
     uint8_t *rings = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *xs = rings, *cs = rings + (size_t)p.x_slots * p.x_bytes;
+    uint8_t *xs = rings, *cs = rings + (size_t)p.slots * p.x_bytes;
     Shared *sh = reinterpret_cast<Shared *>(rings + kRingSpace);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = p.split > 1 ? cluster_rank() : 0;
@@ -266,13 +275,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
             mbar_init(&sh->code_full[s], 1);
             mbar_init(&sh->code_empty[s], 4);   // the four warps that expand it
         }
-        for (int s = 0; s < p.x_slots; ++s) {
-            mbar_init(&sh->x_full[s], 1);
-            mbar_init(&sh->x_empty[s], 1);
-        }
-        for (int a = 0; a < kABuffers; ++a) {
-            mbar_init(&sh->a_full[a], 4);
-            mbar_init(&sh->a_empty[a], 1);
+        for (int s = 0; s < p.slots; ++s) {
+            mbar_init(&sh->full[s], 9);   // the eight warps that expand it, and x's copies
+            mbar_init(&sh->empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh->acc_full[a], 1);
@@ -308,17 +313,17 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
     tc_fence_after();
     const int total = sh->first[p.w.groups] * p.lane_tiles;
     const uint32_t tmem = sh->tmem;
-    const int lo = p.blocks * (int)rank / p.split, hi = p.blocks * ((int)rank + 1) / p.split;
+    const int lo = p.steps * (int)rank / p.split, hi = p.steps * ((int)rank + 1) / p.split;
 
     Walk walk;
     Ring ring;
-    int issued = 0;   // producers: blocks so far
+    int issued = 0;   // codes' blocks so far
     bool ok = true;
     if (warp == 0) {
         // ---- TMA: codes and scales
         for (int t = t0; t < total && ok; t += t_step) {
             const Tile x = find_tile(p, sh, t, walk);
-            for (int kb = lo; kb < hi; ++kb, ++issued, ring.next(p.code_slots)) {
+            for (int kb = 2 * lo; kb < 2 * hi; ++kb, ++issued, ring.next(p.code_slots)) {
                 ok = warp_wait(&sh->code_empty[ring.s], ring.phase ^ 1, sh, p);
                 if (!ok) break;
                 if (elect_one()) {
@@ -342,108 +347,111 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
         // ---- TMA: rows of x
         for (int t = t0; t < total && ok; t += t_step) {
             const Tile x = find_tile(p, sh, t, walk);
-            for (int kb = lo; kb < hi; ++kb, ++issued, ring.next(p.x_slots)) {
-                ok = warp_wait(&sh->x_empty[ring.s], ring.phase ^ 1, sh, p);
+            for (int ks = lo; ks < hi; ++ks, ring.next(p.slots)) {
+                ok = warp_wait(&sh->empty[ring.s], ring.phase ^ 1, sh, p);
                 if (!ok) break;
                 if (elect_one()) {
-                    uint64_t *full = &sh->x_full[ring.s];
-                    const int subs = p.w.k - kb * kBlock > 64 ? 2 : 1;
+                    uint64_t *full = &sh->full[ring.s];
+                    const int subs = min(kStep / 64, (p.w.k - ks * kStep + 63) / 64);
                     mbar_arrive_expect_tx(full, subs * x.n_mma * 128);
                     const CUtensorMap *map = &p.x[x.n_mma / 16 - 1];
                     for (int i = 0; i < subs; ++i)
-                        tma_load_3d<1>(xs + (size_t)ring.s * p.x_bytes + i * x.n_mma * 128, map, kb * kBlock + i * 64, x.col0,
+                        tma_load_3d<1>(xs + (size_t)ring.s * p.x_bytes + i * x.n_mma * 128, map, ks * kStep + i * 64, x.col0,
                                        x.g, smem_u32(full));
                 }
                 __syncwarp();
             }
         }
     } else if (warp == 1) {
-        // ---- MMA: one thread issues a block's steps of 16
-        int acc = 0, a = 0;
-        uint32_t acc_phase = 0, a_phase = 0;
-        for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile(p, sh, t, walk);
-            if (lo == hi) continue;
-            const uint32_t idesc = mma_idesc(kLanes, x.n_mma, false, false), d = tmem + acc * kColMax;
-            ok = warp_wait(&sh->acc_empty[acc], ((acc_phase >> acc) & 1) ^ 1, sh, p);
-            if (!ok) break;
-            acc_phase ^= 1u << acc;
-            for (int kb = lo; kb < hi; ++kb, ring.next(p.x_slots)) {
-                ok = warp_wait(&sh->x_full[ring.s], ring.phase, sh, p) && warp_wait(&sh->a_full[a], a_phase, sh, p);
+        // ---- MMA: one thread waits and issues. (By the whole warp, with a vote after each wait, a
+        // block took over 1100 cycles, whatever its columns: 64 experts with four rows 228 -> 181 us.)
+        if (elect_one()) {
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            const uint64_t base = smem_desc(smem_u32(xs), 16, 1024);
+            for (int t = t0; t < total && ok; t += t_step) {
+                const Tile x = find_tile(p, sh, t, walk);
+                const uint32_t idesc = mma_idesc(kLanes, x.n_mma, false, false), d = tmem + acc * p.acc_stride;
+                ok = role_wait(&sh->acc_empty[acc], ((acc_phase >> acc) & 1) ^ 1, sh, p);
                 if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t sx = smem_u32(xs + (size_t)ring.s * p.x_bytes);
-                    const uint32_t from = tmem + kABase + a * kACols;
-                    const int steps = min(kBlock, p.w.k - kb * kBlock) / 16;
-                    const uint64_t b0 = smem_desc(sx, 16, 1024), b1 = smem_desc(sx + x.n_mma * 128, 16, 1024);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < steps) mma_ts(d, from + i * 8, (i < 4 ? b0 : b1) + 2 * (i % 4), idesc, kb > lo || i > 0);
-                    mma_commit<1>(&sh->x_empty[ring.s]);
-                    mma_commit<1>(&sh->a_empty[a]);
-                }
-                __syncwarp();
-                if (++a == kABuffers) a = 0, a_phase ^= 1;
-            }
-            if (!ok) break;
-            if (elect_one()) mma_commit<1>(&sh->acc_full[acc]);
-            __syncwarp();
-            acc ^= 1;
-        }
-    } else if (warp >= 4 && warp < 12) {
-        // ---- codes to bf16, from shared to tensor memory; the two groups take turns
-        const int turn = (warp - 4) / 4, quad = warp % 4, row = quad * 32 + lane;
-        int a = 0, b = 0;   // b: blocks so far, whose lowest bits say whose turn it is
-        uint32_t a_phase = 0;
-        for (int t = t0; t < total && ok; t += t_step) {
-            for (int kb = lo; kb < hi; ++kb, ++b) {
-                if ((b & 1) == turn) {
-                    ok = warp_wait(&sh->code_full[ring.s], ring.phase, sh, p);
-                    if (!ok) break;
-                    const uint8_t *slot = cs + ring.s * kCodeSlot;
-                    uint4 c[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)   // (the 64-byte swizzle)
-                        c[i] = *reinterpret_cast<const uint4 *>(slot + row * 64 + ((i ^ ((row >> 1) & 3)) << 4));
-                    __nv_bfloat162 scale[4];
-                    const __nv_bfloat16 *sc = reinterpret_cast<const __nv_bfloat16 *>(slot + kCodeBytes) + row;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        scale[i] = __bfloat162bfloat162(sc[((i * 32) >> p.w.group_shift) * kLanes]);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh->code_empty[ring.s]);
-                    ok = warp_wait(&sh->a_empty[a], a_phase ^ 1, sh, p);
+                acc_phase ^= 1u << acc;
+                bool more = false;
+                for (int ks = lo; ks < hi; ++ks, ring.next(p.slots)) {
+                    ok = role_wait(&sh->full[ring.s], ring.phase, sh, p);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t to = tmem + kABase + a * kACols + ((uint32_t)(quad * 32) << 16);
+                    const uint32_t from = tmem + 2 * p.acc_stride + ring.s * kACols;
+                    uint64_t b = base + (uint32_t)(ring.s * p.x_bytes) / 16;
+                    const int left = p.w.k - ks * kStep;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[32];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 v = c[2 * h + i];
-                            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                uint32_t pair[4];
-                                w4_values<FP4>(words[q], scale[2 * h + i], pair);
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) r[i * 16 + q * 4 + j] = pair[j];
-                            }
-                        }
-                        tmem_st32(to + h * 32, r);
+                    for (int sub = 0; sub < kStep / 64; ++sub, b += x.n_mma * 8) {
+                        if (left <= sub * 64) break;
+                        mma_ts(d, from + sub * 32, b, idesc, more);
+                        more = true;
+                        mma_ts(d, from + sub * 32 + 8, b + 2, idesc, true);
+                        if (left <= sub * 64 + 32) break;
+                        mma_ts(d, from + sub * 32 + 16, b + 4, idesc, true);
+                        mma_ts(d, from + sub * 32 + 24, b + 6, idesc, true);
                     }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh->a_full[a]);
+                    mma_commit<1>(&sh->empty[ring.s]);
                 }
-                ring.next(p.code_slots);
-                if (++a == kABuffers) a = 0, a_phase ^= 1;
+                if (!ok) break;
+                mma_commit<1>(&sh->acc_full[acc]);
+                acc ^= 1;
             }
         }
-    } else if (warp >= 12) {
+        __syncwarp();
+    } else if (warp >= 4 && warp < kFirstEpilogue) {
+        // ---- codes to bf16, from shared to tensor memory; the groups take turns. What tile a block
+        // belongs to does not matter here, so a group goes from one of its blocks straight to the next.
+        const int turn = (warp - 4) / 4, quad = warp % 4, row = quad * 32 + lane;
+        const int tiles = t0 < total ? (total - t0 - 1) / t_step + 1 : 0;
+        const long long blocks = (long long)tiles * 2 * (hi - lo);
+        ring.s = turn;
+        Ring to_ring;
+        to_ring.s = turn / 2;
+        for (long long b = turn; b < blocks; b += kTurns, ring.skip(kTurns, p.code_slots), to_ring.skip(kTurns / 2, p.slots)) {
+            ok = warp_wait(&sh->code_full[ring.s], ring.phase, sh, p);
+            if (!ok) break;
+            const uint8_t *slot = cs + ring.s * kCodeSlot;
+            uint4 c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)   // (the 64-byte swizzle)
+                c[i] = *reinterpret_cast<const uint4 *>(slot + row * 64 + ((i ^ ((row >> 1) & 3)) << 4));
+            W4Scale<FP4> scale[4];
+            const __nv_bfloat16 *sc = reinterpret_cast<const __nv_bfloat16 *>(slot + kCodeBytes) + row;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) scale[i] = W4Scale<FP4>(sc[((i * 32) >> p.w.group_shift) * kLanes]);
+            const uint32_t to = tmem + 2 * p.acc_stride + to_ring.s * kACols + (turn & 1) * (kBlock / 2) +
+                                ((uint32_t)(quad * 32) << 16);
+            bool large = false;
+            if (FP4) large = __any_sync(kAll, scale[0].large() || scale[1].large() || scale[2].large() || scale[3].large());
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t r[32];
+                if (large) {
+                    expand<FP4, true>(c[2 * h], scale[2 * h], r);
+                    expand<FP4, true>(c[2 * h + 1], scale[2 * h + 1], r + 16);
+                } else {
+                    expand<FP4, false>(c[2 * h], scale[2 * h], r);
+                    expand<FP4, false>(c[2 * h + 1], scale[2 * h + 1], r + 16);
+                }
+                if (h == 0) {   // (the slot's MMAs may take as long as half of the block)
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->code_empty[ring.s]);
+                    ok = warp_wait(&sh->empty[to_ring.s], to_ring.phase ^ 1, sh, p);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                tmem_st32(to + h * 32, r);
+            }
+            if (!ok) break;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->full[to_ring.s]);
+        }
+    } else if (warp >= kFirstEpilogue) {
         // ---- epilogue
         const int quad = warp % 4;
         int acc = 0;
@@ -458,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
                 acc_phase ^= 1u << acc;
                 tc_fence_after();
             }
-            const uint32_t from = tmem + acc * kColMax + ((uint32_t)(quad * 32) << 16);
+            const uint32_t from = tmem + acc * p.acc_stride + ((uint32_t)(quad * 32) << 16);
             for (int c = 0; c < x.cols; c += 32) {
                 float v[32];
                 if (lo < hi) {
@@ -489,21 +497,17 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
         }
     }
     __syncthreads();
-    if (sh->abort && threadIdx.x < 128) {
-        // a wait ran out: let the copies and MMAs in flight finish (bounded) before shared and
-        // tensor memory are given up
+    // where a wait ran out, what is in flight is to finish (bounded) before shared and tensor
+    // memory are given up
+    if (sh->abort && warp == 1 && elect_one()) drain_mma(sh);
+    if (sh->abort && threadIdx.x == 0) {
         const uint64_t since = global_ns();
-        if (threadIdx.x == 0 || threadIdx.x == 96) {
-            const int slots = threadIdx.x == 0 ? p.code_slots : p.x_slots;
-            uint64_t *full = threadIdx.x == 0 ? sh->code_full : sh->x_full;
-            for (int i = max(0, issued - slots); i < issued; ++i)
-                while (!mbar_try_wait(&full[i % slots], (uint32_t)(i / slots) & 1) && global_ns() - since < 100000000ull)
-                    ;
-        } else if (threadIdx.x == 32) {
-            mma_commit<1>(&sh->drain);
-            while (!mbar_try_wait(&sh->drain, 0) && global_ns() - since < 100000000ull)
+        for (int i = max(0, issued - p.code_slots); i < issued; ++i)
+            while (!mbar_try_wait(&sh->code_full[i % p.code_slots], (uint32_t)(i / p.code_slots) & 1) &&
+                   global_ns() - since < 100000000ull)
                 ;
-        }
+        while (global_ns() - since < 1000000ull)   // x's copies, whose barriers also wait for warps that have left
+            ;
     }
     tc_fence_before();
     __syncthreads();
@@ -511,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
         // ---- a shared tile: every CTA has its sums in shared memory; each adds up its share of
         // the columns, in rank order, and finishes them
         cluster_sync();
-        if (t0 < total && warp >= 12) {
+        if (t0 < total && warp >= kFirstEpilogue) {
             const int quad = warp % 4;
             walk = Walk();
             const Tile x = find_tile(p, sh, t0, walk);
@@ -577,20 +581,19 @@ int launch_w4_tiles(const W4Params &w, bool fp4, int32_t *status, cudaStream_t s
     p.lane_step = gated ? kLanes / 2 : kLanes;
     p.lane_tiles = (int)ceil_div(w.n, p.lane_step);
     p.col_max = w.rows < kColMax ? (int)ceil_div(w.rows, 16) * 16 : kColMax;
-    p.blocks = (int)ceil_div(w.k, kBlock);
+    p.steps = (int)ceil_div(w.k, kStep);
     const long long most = (long long)p.lane_tiles * w.groups * ceil_div(w.rows, p.col_max);
     if (most >= (1LL << 30)) return EP_ERR_INVALID_ARG;   // tile numbers stay within int
     // dense products with few tiles share each one's reduction (clusters of four fill 144 SMs)
     p.split = 1;
     if (!w.counts)
-        while (p.split < kMaxSplit && most * p.split * 2 <= sms - sms / 16 && p.blocks >= 4 * p.split) p.split *= 2;
-    p.x_bytes = p.col_max * kBlock * 2;
+        while (p.split < kMaxSplit && most * p.split * 2 <= sms - sms / 16 && p.steps >= 2 * p.split) p.split *= 2;
+    p.x_bytes = p.col_max * kStep * 2;
     p.scale_bytes = kLanes * 2 * (kBlock >> w.group_shift);
-    // the rings: half of the codes' slots first, then x, then what is left
-    p.code_slots = 8;
-    p.x_slots = (int)(kRingSpace - p.code_slots * kCodeSlot) / p.x_bytes;
-    if (p.x_slots > kMaxXSlots) p.x_slots = kMaxXSlots;
-    p.code_slots = (int)(kRingSpace - (size_t)p.x_slots * p.x_bytes) / kCodeSlot;
+    p.acc_stride = (p.col_max + 31) / 32 * 32;
+    p.slots = (kTmemCols - 2 * p.acc_stride) / kACols;   // 2 for 128 columns, 3 for 64
+    p.code_slots = (int)(kRingSpace - (size_t)p.slots * p.x_bytes) / kCodeSlot;
+    p.code_slots = p.code_slots / kTurns * kTurns;   // so that a group meets the same slots in every round: 8 or 12
     if (p.code_slots > kMaxCodeSlots) p.code_slots = kMaxCodeSlots;
     const uint64_t K = w.k, N = w.n, W = w.wide, G = w.groups, parts = K >> w.group_shift;
     const uint32_t per_block = kBlock >> w.group_shift;
