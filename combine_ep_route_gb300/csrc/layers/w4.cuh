@@ -43,40 +43,52 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
     return r;
 }
 
-// A scale in both halves of a register. fp4 codes read as value * 2^-126 (below), so their scale
-// carries 2^126, which is exact and saves a product; a scale of 4 and more would overflow
-// (`large`) and takes that product.
+// A group's scale, in both halves of a register each time. A masked field is a subnormal bf16
+// (below), so the scale carries the power of two that makes up for it; where that would overflow
+// (`large`: rare for a weight, and infinity and NaN) the values are brought up first, in a product
+// more each.
+//   int4: by = scale * 2^133, by16 = scale * 2^129, off = -8 scale, for scales below 2^-5
+//   fp4:  by = scale * 2^126, for scales below 4
 template <bool FP4>
 struct W4Scale {
-    __nv_bfloat162 v;
-    __device__ __forceinline__ W4Scale() : v(bf162_of(0)) {}
-    __device__ __forceinline__ explicit W4Scale(__nv_bfloat16 scale) : v(__bfloat162bfloat162(scale)) {}
-    __device__ __forceinline__ bool large() const { return (u32_of(v) & 0x7FFFu) >= 0x4080u; }   // |scale| >= 4, or NaN
+    __nv_bfloat162 scale, by, by16, off;
+    __device__ __forceinline__ W4Scale() : scale(bf162_of(0)), by(bf162_of(0)), by16(bf162_of(0)), off(bf162_of(0)) {}
+    __device__ __forceinline__ explicit W4Scale(__nv_bfloat16 s) : scale(__bfloat162bfloat162(s)) {
+        if (FP4) {
+            by = __hmul2(scale, bf162_of(0x7E807E80u));                       // 2^126
+        } else {
+            by16 = __hmul2(__hmul2(scale, bf162_of(0x7E807E80u)), bf162_of(0x41004100u));   // 2^3 more
+            by = __hmul2(by16, bf162_of(0x41804180u));                        // 2^4 more
+            off = __hmul2(scale, bf162_of(0xC100C100u));                      // -8
+        }
+    }
+    __device__ __forceinline__ bool large() const { return (u32_of(scale) & 0x7FFFu) >= (FP4 ? 0x4080u : 0x3D00u); }
 };
 
-// The eight weights of a word, in order, as four pairs.
-//   int4 (two's complement): a field with its top bit turned is value + 8; under the exponent
-//     of 128 it reads 136 + value.
-//   fp4 (sign, two bits of exponent, one of mantissa): moved to bf16's sign, the low end of its
-//     exponent and the top of its mantissa, it reads value * 2^-126, subnormals included.
-// All steps but the scale's product are exact, so a weight is rounded once.
+// The eight weights of a word, in order, as four pairs. All steps but the last are exact, so a
+// weight is rounded once, from value * scale.
+//   int4 (two's complement): a field with its top bit turned is u = value + 8. Bits 0-7 of a bf16
+//     read as an integer times 2^-133 (its subnormals and their first normal binade), so a field there
+//     is u 2^-133 or 16 u 2^-133 as it stands, and one fused product-sum makes u scale - 8 scale of it.
+//   fp4 (sign, two bits of exponent, one of mantissa): at the low end of bf16's exponent and the top
+//     of its mantissa a code reads value * 2^-126, subnormals included. One product by 2^6 + 2^12 brings
+//     a field there and its sign to the top.
 template <bool FP4, bool LARGE>
-__device__ __forceinline__ void w4_values(uint32_t word, const W4Scale<FP4> &scale, uint32_t (&pair)[4]) {
-    if (FP4) {
-        const uint32_t s[4] = {word << 12, word << 8, word << 4, word};
-        const uint32_t m[4] = {word << 6, word << 2, word >> 2, word >> 6};
-        const __nv_bfloat162 up = bf162_of(0x7E807E80u);   // 2^126
-        const __nv_bfloat162 by = LARGE ? scale.v : __hmul2(scale.v, up);
+__device__ __forceinline__ void w4_values(uint32_t word, const W4Scale<FP4> &s, uint32_t (&pair)[4]) {
+    const uint32_t w[2] = {word, word >> 8};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 v = bf162_of(and_or(s[j], 0x80008000u, m[j] & 0x01C001C0u));
-            pair[j] = u32_of(__hmul2(LARGE ? __hmul2(v, up) : v, by));
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t v = and_xor(word >> (4 * j), 0x000F000Fu, 0x43084308u);
-            pair[j] = u32_of(__hmul2(__hsub2(bf162_of(v), bf162_of(0x43084308u)), scale.v));   // 136
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t field = (j & 1) ? 0x00F000F0u : 0x000F000Fu;
+        if (FP4) {
+            const __nv_bfloat162 v = bf162_of(((w[j / 2] & field) * ((j & 1) ? 0x104u : 0x1040u)) & 0x81C081C0u);
+            pair[j] = u32_of(LARGE ? __hmul2(__hmul2(v, bf162_of(0x7E807E80u)), s.scale) : __hmul2(v, s.by));
+        } else if (LARGE) {
+            // under the exponent of 128 the field reads 136 + value
+            const __nv_bfloat162 v = bf162_of(and_xor(word >> (4 * j), 0x000F000Fu, 0x43084308u));
+            pair[j] = u32_of(__hmul2(__hsub2(v, bf162_of(0x43084308u)), s.scale));
+        } else {
+            const __nv_bfloat162 v = bf162_of(and_xor(w[j / 2], field, field & 0x00880088u));
+            pair[j] = u32_of(__hfma2(v, (j & 1) ? s.by16 : s.by, s.off));
         }
     }
 }

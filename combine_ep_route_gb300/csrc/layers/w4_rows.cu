@@ -59,17 +59,17 @@ __global__ void __launch_bounds__(kThreads) w4_rows_kernel(const W4Params p) {
         float acc[MT][NT][4] = {};
         for (int s0 = warp; s0 < steps; s0 += kWarps * kFlight) {
             uint4 code[kFlight][2 * MT];
-            W4Scale<FP4> scale[kFlight][2 * MT];
+            __nv_bfloat16 raw[kFlight][2 * MT];
 #pragma unroll
             for (int q = 0; q < kFlight; ++q) {
                 const int e = (s0 + q * kWarps) * kStep + t * 32;   // this lane's first element
 #pragma unroll
                 for (int i = 0; i < 2 * MT; ++i) {
                     code[q][i] = make_uint4(0, 0, 0, 0);
-                    scale[q][i] = W4Scale<FP4>();
+                    raw[q][i] = __ushort_as_bfloat16(0);
                     if (e < p.k) {
                         code[q][i] = __ldcs(reinterpret_cast<const uint4 *>(codes + (size_t)row[i] * (p.k / 2) + e / 2));
-                        scale[q][i] = W4Scale<FP4>(scales[(size_t)(e >> p.group_shift) * p.wide + row[i]]);
+                        raw[q][i] = scales[(size_t)(e >> p.group_shift) * p.wide + row[i]];
                     }
                 }
             }
@@ -77,13 +77,23 @@ __global__ void __launch_bounds__(kThreads) w4_rows_kernel(const W4Params p) {
             for (int q = 0; q < kFlight; ++q) {
                 const int e = (s0 + q * kWarps) * kStep + t * 32;
                 if (s0 + q * kWarps >= steps) break;   // the same for the whole warp
+                bool large = false;
+                W4Scale<FP4> scale[2 * MT];
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) {
+                    scale[i] = W4Scale<FP4>(raw[q][i]);
+                    large |= scale[i].large();
+                }
+                large = __any_sync(0xFFFFFFFFu, large);
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     uint32_t a[2 * MT][4];
 #pragma unroll
                     for (int i = 0; i < 2 * MT; ++i) {
                         const uint4 c = code[q][i];
-                        w4_values<FP4, true>(w == 0 ? c.x : w == 1 ? c.y : w == 2 ? c.z : c.w, scale[q][i], a[i]);
+                        const uint32_t word = w == 0 ? c.x : w == 1 ? c.y : w == 2 ? c.z : c.w;
+                        if (large) w4_values<FP4, true>(word, scale[i], a[i]);
+                        else w4_values<FP4, false>(word, scale[i], a[i]);
                     }
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {

@@ -25,19 +25,22 @@ namespace ep {
 namespace {
 
 constexpr int kTurns = 4;            // groups of four warps that expand blocks by turns
-constexpr int kThreads = 128 + kTurns * 128 + 128;
+constexpr int kEpilogueWarps = 8;    // two per quarter of the accumulator lanes
+constexpr int kThreads = 128 + kTurns * 128 + kEpilogueWarps * 32;
 constexpr int kFirstEpilogue = 4 + kTurns * 4;
 constexpr int kLanes = 128;          // weight rows of a tile
-constexpr int kBlock = 128;          // elements of k of a block of codes
-constexpr int kStep = 2 * kBlock;    // and of what the MMA thread waits for and issues at once
+constexpr int kStep = 256;           // elements of k of a block: rows of codes of 128 bytes
+constexpr int kHalf = kStep / 2;     // what one group of warps expands
 constexpr int kColMax = 128;         // rows of x of a tile, at most
-constexpr int kBoxes = kColMax / 16;
+constexpr int kBoxes = 1 + kColMax / 16;   // boxes of 8, 16, 32, ... 128 rows of x
+constexpr int kChunk = 16;           // columns that an epilogue warp takes at once
 constexpr int kACols = kStep / 2;    // tensor-memory columns of a step: two elements to one
 constexpr int kTmemCols = 512;       // two accumulators, then steps of the weight
 constexpr int kMaxSlots = (kTmemCols - 2 * 32) / kACols;
-constexpr int kCodeBytes = kLanes * kBlock / 2;
-constexpr int kCodeSlot = kCodeBytes + 1024;   // with the scales: four times 128 at most
-constexpr int kMaxCodeSlots = 12;
+constexpr int kMaxXSlots = 8;
+constexpr int kCodeBytes = kLanes * kStep / 2;
+constexpr int kCodeSlot = kCodeBytes + kLanes * (kStep / 32) * 2;   // with the scales, at most
+constexpr int kMaxCodeSlots = 8;
 constexpr int kMaxSplit = 4;
 constexpr uint32_t kSleepNs = 1000000;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -48,14 +51,15 @@ __global__ void take_status() { w4_status_taken = atomicExch(&w4_status, 0); }
 
 struct TileParams {
     CUtensorMap codes, scales;
-    CUtensorMap x[kBoxes];    // boxes of 16, 32, ... 128 rows
+    CUtensorMap x[kBoxes];
     W4Params w;
     int lane_step, lane_tiles;       // output features of a tile, tiles per group
     int col_max;                     // widest column tile
     int code_slots;                  // ring of codes and scales
-    int slots, x_bytes;              // ring of steps, expanded weight and x; bytes of an x slot
+    int slots;                       // ring of expanded steps in tensor memory
+    int x_slots, x_bytes;            // ring of x; bytes of a slot
     int acc_stride;                  // columns of an accumulator
-    int scale_bytes;                 // of a block
+    int scale_parts;                 // groups of a step
     int steps, split;                // steps of k; CTAs of a cluster that share them
     int32_t *status;
     uint64_t wait_limit_ns;
@@ -64,6 +68,7 @@ struct TileParams {
 
 struct Shared {
     uint64_t code_full[kMaxCodeSlots], code_empty[kMaxCodeSlots];
+    uint64_t x_full[kMaxXSlots], x_empty[kMaxXSlots];
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
@@ -102,12 +107,37 @@ __device__ __forceinline__ void expand(uint4 c, const W4Scale<FP4> &scale, uint3
 }
 
 // D (+)= A * B over 16 elements, A from tensor memory.
+template <int CG>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    if (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+            : "memory");
+}
+
+// 16 columns of this warp's 32 lanes; valid after tmem_ld_wait().
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+
+// An arrival on a barrier of any CTA of the cluster, after this thread's stores to tensor memory
+// (which it has waited for and fenced). At cluster scope the release would wait for all of the
+// thread's memory traffic, once per step.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // A bounded wait, cut short once any role of the CTA has given up.
@@ -131,15 +161,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Shared
 }
 
 // Waits (bounded) for the MMAs that this thread has issued.
+template <int CG>
 __device__ __forceinline__ void drain_mma(Shared *sh) {
     const uint64_t since = global_ns();
-    mma_commit<1>(&sh->drain);
+    mma_commit<CG>(&sh->drain);
     while (!mbar_try_wait(&sh->drain, 0) && global_ns() - since < 100000000ull)
         ;
 }
 
 // Columns of each of ct tiles over `all` > 0 columns: 130 rows make 80 and 50, not 128 and 2.
-__device__ __forceinline__ int tile_width(int all, int ct) { return ((all - 1) / ct + 16) / 16 * 16; }
+template <int CG>
+__device__ __forceinline__ int tile_width(int all, int ct) {
+    constexpr int kUnit = 16 * CG;
+    return ((all - 1) / ct + kUnit) / kUnit * kUnit;
+}
 
 // The groups' row counts, dearest tiles first, so that the last round is a cheap one. Ends in a barrier.
 __device__ __forceinline__ void order_groups(const TileParams &p, Shared *sh) {
@@ -183,7 +218,8 @@ struct Walk {
 
 // Column tiles innermost: the CTAs that share a lane tile's weight work at the same time, so
 // all but one find it in L2.
-__device__ __forceinline__ Tile find_tile(const TileParams &p, const Shared *sh, int t, Walk &w) {
+template <int CG>
+__device__ __forceinline__ Tile find_tile(const TileParams &p, const Shared *sh, int t, uint32_t rank, Walk &w) {
     if (t >= w.end) {
         do {
             ++w.at;
@@ -191,34 +227,34 @@ __device__ __forceinline__ Tile find_tile(const TileParams &p, const Shared *sh,
             w.end = sh->first[w.at + 1] * p.lane_tiles;
         } while (t >= w.end);
         w.ct = sh->first[w.at + 1] - sh->first[w.at];
-        w.width = tile_width(sh->count[w.at], w.ct);
+        w.width = tile_width<CG>(sh->count[w.at], w.ct);
     }
     const int r = t - w.begin, lt = w.ct == 1 ? r : r / w.ct, c = r - lt * w.ct;
     Tile x;
     x.g = sh->group[w.at];
-    x.lane0 = lt * p.lane_step;
+    x.lane0 = (CG == 1 ? lt : lt * 2 + (int)rank) * p.lane_step;
     x.col0 = c * w.width;
     x.cols = min(w.width, sh->count[w.at] - x.col0);
-    x.n_mma = (x.cols + 15) / 16 * 16;
+    x.n_mma = (x.cols + 16 * CG - 1) / (16 * CG) * (16 * CG);
     return x;
 }
 
 template <int ACT>
-__device__ __forceinline__ void act_all(float (&v)[32]) {
+__device__ __forceinline__ void act_all(float (&v)[kChunk]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = act_value(v[j], ACT);
+    for (int j = 0; j < kChunk; ++j) v[j] = act_value(v[j], ACT);
 }
 
-// 32 columns of one warp's 32 lanes: bias, activation, residual, out. n of them are rows in use.
-// Lanes first trade columns with a partner, so that each ends with 16 columns: of a gated product
+// kChunk columns of one warp's 32 lanes: bias, activation, residual, out. n of them are rows in use.
+// Lanes first trade columns with a partner, so that each ends with half of them: of a gated product
 // gate lanes (0-7, 16-23) take the even ones' ups from the lanes eight further and give the odd
 // ones' gates; otherwise neighbours end with two features of the even or the odd columns.
 template <bool GATED>
-__device__ __forceinline__ void epilogue_chunk(const TileParams &p, float (&v)[32], size_t row0, int n, int quad, int lane,
+__device__ __forceinline__ void epilogue_chunk(const TileParams &p, float (&v)[kChunk], size_t row0, int n, int quad, int lane,
                                                int lane0, float bias) {
     const W4Params &w = p.w;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] += bias;
+    for (int j = 0; j < kChunk; ++j) v[j] += bias;
     if (!GATED) {
         switch (w.act) {
             case EP_ACT_RELU: act_all<EP_ACT_RELU>(v); break;
@@ -235,7 +271,7 @@ __device__ __forceinline__ void epilogue_chunk(const TileParams &p, float (&v)[3
     __nv_bfloat16 *out = w.out + at;
     const __nv_bfloat16 *residual = w.residual ? w.residual + at : nullptr;
 #pragma unroll
-    for (int i = 0; i < 16; ++i, out += step) {
+    for (int i = 0; i < kChunk / 2; ++i, out += step) {
         const float got = __shfl_xor_sync(kAll, odd ? v[2 * i] : v[2 * i + 1], GATED ? 8 : 1);
         float lo = odd ? got : v[2 * i], hi = odd ? v[2 * i + 1] : got;
         if (GATED) {
@@ -260,28 +296,33 @@ __device__ __forceinline__ float bias_of(const TileParams &p, const Tile &x, int
     return __bfloat162float(p.w.bias[(size_t)x.g * p.w.wide + (GATED && (lane & 8) ? p.w.n : 0) + f]);
 }
 
-template <bool FP4, bool GATED>
+template <bool FP4, bool GATED, int CG>
 __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_constant__ TileParams p) {
     extern __shared__ uint8_t raw[];
     uint8_t *rings = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    uint8_t *xs = rings, *cs = rings + (size_t)p.slots * p.x_bytes;
+    uint8_t *xs = rings, *cs = rings + (size_t)p.x_slots * p.x_bytes;
     Shared *sh = reinterpret_cast<Shared *>(rings + kRingSpace);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t rank = p.split > 1 ? cluster_rank() : 0;
-    const int t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split;
+    const uint32_t rank = CG == 2 || p.split > 1 ? cluster_rank() : 0;
+    const int per_cluster = CG == 2 ? 2 : p.split;
+    const int t0 = blockIdx.x / per_cluster, t_step = gridDim.x / per_cluster;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.code_slots; ++s) {
             mbar_init(&sh->code_full[s], 1);
-            mbar_init(&sh->code_empty[s], 4);   // the four warps that expand it
+            mbar_init(&sh->code_empty[s], 8);   // the warps that expand it
         }
         for (int s = 0; s < p.slots; ++s) {
-            mbar_init(&sh->full[s], 9);   // the eight warps that expand it, and x's copies
+            mbar_init(&sh->full[s], 8 * CG);
             mbar_init(&sh->empty[s], 1);
+        }
+        for (int s = 0; s < p.x_slots; ++s) {
+            mbar_init(&sh->x_full[s], CG);
+            mbar_init(&sh->x_empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&sh->acc_full[a], 1);
-            mbar_init(&sh->acc_empty[a], 4);
+            mbar_init(&sh->acc_empty[a], kEpilogueWarps * CG);
         }
         mbar_init(&sh->drain, 1);
         sh->abort = 0;
@@ -289,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
         tma_prefetch_map(&p.codes);
         tma_prefetch_map(&p.scales);
     }
-    if (warp == 2) tmem_alloc<1>(&sh->tmem, kTmemCols);
+    if (warp == 2) tmem_alloc<CG>(&sh->tmem, kTmemCols);
     pdl_wait();   // nothing above reads or writes global memory
     pdl_launch_dependents();
     order_groups(p, sh);
@@ -310,35 +351,37 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
     }
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();   // both CTAs' barriers are ready before either signals the other's
     tc_fence_after();
     const int total = sh->first[p.w.groups] * p.lane_tiles;
     const uint32_t tmem = sh->tmem;
-    const int lo = p.steps * (int)rank / p.split, hi = p.steps * ((int)rank + 1) / p.split;
+    const int part = CG == 2 ? 0 : (int)rank;
+    const int lo = p.steps * part / p.split, hi = p.steps * (part + 1) / p.split;   // this CTA's steps of a tile
 
     Walk walk;
     Ring ring;
-    int issued = 0;   // codes' blocks so far
+    int issued = 0;   // producers: loads into their ring so far
     bool ok = true;
     if (warp == 0) {
         // ---- TMA: codes and scales
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile(p, sh, t, walk);
-            for (int kb = 2 * lo; kb < 2 * hi; ++kb, ++issued, ring.next(p.code_slots)) {
+            const Tile x = find_tile<CG>(p, sh, t, rank, walk);
+            for (int ks = lo; ks < hi; ++ks, ++issued, ring.next(p.code_slots)) {
                 ok = warp_wait(&sh->code_empty[ring.s], ring.phase ^ 1, sh, p);
                 if (!ok) break;
                 if (elect_one()) {
                     uint64_t *full = &sh->code_full[ring.s];
-                    mbar_arrive_expect_tx(full, kCodeBytes + p.scale_bytes);
+                    mbar_arrive_expect_tx(full, kCodeBytes + kLanes * 2 * p.scale_parts);
                     const uint32_t bar = smem_u32(full);
                     uint8_t *dst = cs + ring.s * kCodeSlot;
-                    const int group0 = (kb * kBlock) >> p.w.group_shift;
-                    if (GATED) {
-                        tma_load_5d<1>(dst, &p.codes, kb * (kBlock / 2), 0, 0, x.lane0 / 8, x.g, bar);
-                        tma_load_5d<1>(dst + kCodeBytes, &p.scales, 0, 0, x.lane0 / 8, group0, x.g, bar);
-                    } else {
-                        tma_load_3d<1>(dst, &p.codes, kb * (kBlock / 2), x.lane0, x.g, bar);
-                        tma_load_3d<1>(dst + kCodeBytes, &p.scales, x.lane0, group0, x.g, bar);
-                    }
+                    if (GATED) tma_load_5d<1>(dst, &p.codes, ks * (kStep / 2), 0, 0, x.lane0 / 8, x.g, bar);
+                    else tma_load_3d<1>(dst, &p.codes, ks * (kStep / 2), x.lane0, x.g, bar);
+                    // scales of 64 rows, then of 64 more: gated, of the gates and of the ups
+                    const int group0 = (ks * kStep) >> p.w.group_shift;
+                    dst += kCodeBytes;
+                    tma_load_3d<1>(dst, &p.scales, x.lane0, group0, x.g, bar);
+                    tma_load_3d<1>(dst + kLanes * p.scale_parts, &p.scales, x.lane0 + (GATED ? p.w.n : kLanes / 2), group0,
+                                   x.g, bar);
                 }
                 __syncwarp();
             }
@@ -346,18 +389,29 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
     } else if (warp == 3) {
         // ---- TMA: rows of x
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile(p, sh, t, walk);
-            for (int ks = lo; ks < hi; ++ks, ring.next(p.slots)) {
-                ok = warp_wait(&sh->empty[ring.s], ring.phase ^ 1, sh, p);
+            const Tile x = find_tile<CG>(p, sh, t, rank, walk);
+            // of a pair each CTA holds half of the MMA's columns; boxes end with the rows in use (what
+            // lies behind them in shared memory makes columns that nobody looks at)
+            const int own = x.n_mma / CG, first = x.col0 + (CG == 2 ? (int)rank * own : 0);
+            const int used = max(0, min(own, x.cols - (first - x.col0)));
+            const int rows = used <= 8 ? 8 : (used + 15) / 16 * 16;
+            const CUtensorMap *map = &p.x[used <= 8 ? 0 : rows / 16];
+            for (int ks = lo; ks < hi; ++ks, ++issued, ring.next(p.x_slots)) {
+                ok = warp_wait(&sh->x_empty[ring.s], ring.phase ^ 1, sh, p);
                 if (!ok) break;
                 if (elect_one()) {
-                    uint64_t *full = &sh->full[ring.s];
-                    const int subs = min(kStep / 64, (p.w.k - ks * kStep + 63) / 64);
-                    mbar_arrive_expect_tx(full, subs * x.n_mma * 128);
-                    const CUtensorMap *map = &p.x[x.n_mma / 16 - 1];
+                    const int subs = used ? min(kStep / 64, (p.w.k - ks * kStep + 63) / 64) : 0;
+                    uint32_t bar;
+                    if (CG == 2) {
+                        bar = map_rank(&sh->x_full[ring.s], 0);
+                        mbar_arrive_expect_tx_cluster(bar, subs * rows * 128);
+                    } else {
+                        bar = smem_u32(&sh->x_full[ring.s]);
+                        mbar_arrive_expect_tx(&sh->x_full[ring.s], subs * rows * 128);
+                    }
                     for (int i = 0; i < subs; ++i)
-                        tma_load_3d<1>(xs + (size_t)ring.s * p.x_bytes + i * x.n_mma * 128, map, ks * kStep + i * 64, x.col0,
-                                       x.g, smem_u32(full));
+                        tma_load_3d<CG>(xs + (size_t)ring.s * p.x_bytes + i * own * 128, map, ks * kStep + i * 64, first, x.g,
+                                        bar);
                 }
                 __syncwarp();
             }
@@ -365,67 +419,74 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
     } else if (warp == 1) {
         // ---- MMA: one thread waits and issues. (By the whole warp, with a vote after each wait, a
         // block took over 1100 cycles, whatever its columns: 64 experts with four rows 228 -> 181 us.)
-        if (elect_one()) {
+        if ((CG == 1 || rank == 0) && elect_one()) {
             int acc = 0;
             uint32_t acc_phase = 0;
+            Ring a_ring;
             const uint64_t base = smem_desc(smem_u32(xs), 16, 1024);
             for (int t = t0; t < total && ok; t += t_step) {
-                const Tile x = find_tile(p, sh, t, walk);
-                const uint32_t idesc = mma_idesc(kLanes, x.n_mma, false, false), d = tmem + acc * p.acc_stride;
+                const Tile x = find_tile<CG>(p, sh, t, rank, walk);
+                const uint32_t idesc = mma_idesc(kLanes * CG, x.n_mma, false, false), d = tmem + acc * p.acc_stride;
                 ok = role_wait(&sh->acc_empty[acc], ((acc_phase >> acc) & 1) ^ 1, sh, p);
                 if (!ok) break;
                 acc_phase ^= 1u << acc;
+                const int sub_bytes = x.n_mma / CG * 128;
                 bool more = false;
-                for (int ks = lo; ks < hi; ++ks, ring.next(p.slots)) {
-                    ok = role_wait(&sh->full[ring.s], ring.phase, sh, p);
+                for (int ks = lo; ks < hi; ++ks, ring.next(p.x_slots), a_ring.next(p.slots)) {
+                    ok = role_wait(&sh->x_full[ring.s], ring.phase, sh, p) &&
+                         role_wait(&sh->full[a_ring.s], a_ring.phase, sh, p);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t from = tmem + 2 * p.acc_stride + ring.s * kACols;
+                    const uint32_t from = tmem + 2 * p.acc_stride + a_ring.s * kACols;
                     uint64_t b = base + (uint32_t)(ring.s * p.x_bytes) / 16;
                     const int left = p.w.k - ks * kStep;
 #pragma unroll
-                    for (int sub = 0; sub < kStep / 64; ++sub, b += x.n_mma * 8) {
+                    for (int sub = 0; sub < kStep / 64; ++sub, b += sub_bytes / 16) {
                         if (left <= sub * 64) break;
-                        mma_ts(d, from + sub * 32, b, idesc, more);
+                        mma_ts<CG>(d, from + sub * 32, b, idesc, more);
                         more = true;
-                        mma_ts(d, from + sub * 32 + 8, b + 2, idesc, true);
+                        mma_ts<CG>(d, from + sub * 32 + 8, b + 2, idesc, true);
                         if (left <= sub * 64 + 32) break;
-                        mma_ts(d, from + sub * 32 + 16, b + 4, idesc, true);
-                        mma_ts(d, from + sub * 32 + 24, b + 6, idesc, true);
+                        mma_ts<CG>(d, from + sub * 32 + 16, b + 4, idesc, true);
+                        mma_ts<CG>(d, from + sub * 32 + 24, b + 6, idesc, true);
                     }
-                    mma_commit<1>(&sh->empty[ring.s]);
+                    mma_commit<CG>(&sh->x_empty[ring.s]);
+                    mma_commit<CG>(&sh->empty[a_ring.s]);
                 }
                 if (!ok) break;
-                mma_commit<1>(&sh->acc_full[acc]);
+                mma_commit<CG>(&sh->acc_full[acc]);
                 acc ^= 1;
             }
         }
         __syncwarp();
     } else if (warp >= 4 && warp < kFirstEpilogue) {
         // ---- codes to bf16, from shared to tensor memory; the groups take turns. What tile a block
-        // belongs to does not matter here, so a group goes from one of its blocks straight to the next.
+        // belongs to does not matter here, so a group goes from one half of a block straight to its next.
         const int turn = (warp - 4) / 4, quad = warp % 4, row = quad * 32 + lane;
         const int tiles = t0 < total ? (total - t0 - 1) / t_step + 1 : 0;
-        const long long blocks = (long long)tiles * 2 * (hi - lo);
-        ring.s = turn;
-        Ring to_ring;
-        to_ring.s = turn / 2;
-        for (long long b = turn; b < blocks; b += kTurns, ring.skip(kTurns, p.code_slots), to_ring.skip(kTurns / 2, p.slots)) {
+        const long long steps = (long long)tiles * (hi - lo);
+        // this lane's scales: of row 64 h + j, or gated of feature j, gate (h = 0) or up
+        const int sh_h = GATED ? (row >> 3) & 1 : row / 64, sh_j = GATED ? (row >> 4) * 8 + (row & 7) : row % 64;
+        const int scale_at = kCodeBytes / 2 + sh_h * (kLanes / 2) * p.scale_parts + sh_j +
+                             (turn & 1) * (kHalf >> p.w.group_shift) * (kLanes / 2);
+        ring.s = turn / 2;
+        Ring to_ring = ring;
+        for (long long b = turn / 2; b < steps;
+             b += kTurns / 2, ring.skip(kTurns / 2, p.code_slots), to_ring.skip(kTurns / 2, p.slots)) {
             ok = warp_wait(&sh->code_full[ring.s], ring.phase, sh, p);
             if (!ok) break;
             const uint8_t *slot = cs + ring.s * kCodeSlot;
             uint4 c[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)   // (the 64-byte swizzle)
-                c[i] = *reinterpret_cast<const uint4 *>(slot + row * 64 + ((i ^ ((row >> 1) & 3)) << 4));
+            for (int i = 0; i < 4; ++i)   // (the 128-byte swizzle)
+                c[i] = *reinterpret_cast<const uint4 *>(slot + row * 128 + ((((turn & 1) * 4 + i) ^ (row & 7)) << 4));
             W4Scale<FP4> scale[4];
-            const __nv_bfloat16 *sc = reinterpret_cast<const __nv_bfloat16 *>(slot + kCodeBytes) + row;
+            const __nv_bfloat16 *sc = reinterpret_cast<const __nv_bfloat16 *>(slot) + scale_at;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) scale[i] = W4Scale<FP4>(sc[((i * 32) >> p.w.group_shift) * kLanes]);
-            const uint32_t to = tmem + 2 * p.acc_stride + to_ring.s * kACols + (turn & 1) * (kBlock / 2) +
+            for (int i = 0; i < 4; ++i) scale[i] = W4Scale<FP4>(sc[((i * 32) >> p.w.group_shift) * (kLanes / 2)]);
+            const uint32_t to = tmem + 2 * p.acc_stride + to_ring.s * kACols + (turn & 1) * (kHalf / 2) +
                                 ((uint32_t)(quad * 32) << 16);
-            bool large = false;
-            if (FP4) large = __any_sync(kAll, scale[0].large() || scale[1].large() || scale[2].large() || scale[3].large());
+            const bool large = __any_sync(kAll, scale[0].large() || scale[1].large() || scale[2].large() || scale[3].large());
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t r[32];
@@ -436,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
                     expand<FP4, false>(c[2 * h], scale[2 * h], r);
                     expand<FP4, false>(c[2 * h + 1], scale[2 * h + 1], r + 16);
                 }
-                if (h == 0) {   // (the slot's MMAs may take as long as half of the block)
+                if (h == 0) {   // (the slot's MMAs may take as long as the first half)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh->code_empty[ring.s]);
                     ok = warp_wait(&sh->empty[to_ring.s], to_ring.phase ^ 1, sh, p);
@@ -449,116 +510,128 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->full[to_ring.s]);
+            if (lane == 0) {
+                if (CG == 2) mbar_arrive_remote(map_rank(&sh->full[to_ring.s], 0));
+                else mbar_arrive(&sh->full[to_ring.s]);
+            }
         }
     } else if (warp >= kFirstEpilogue) {
-        // ---- epilogue
-        const int quad = warp % 4;
+        // ---- epilogue: 32 lanes and every other kChunk columns of each accumulator
+        const int quad = warp % 4, half = (warp - kFirstEpilogue) / 4;
         int acc = 0;
         uint32_t acc_phase = 0;
+        // accumulator a may be overwritten: this warp's part is in registers
+        auto free_acc = [&](int a) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2) mbar_arrive_cluster_relaxed(map_rank(&sh->acc_empty[a], 0));
+                else mbar_arrive(&sh->acc_empty[a]);
+            }
+        };
         for (int t = t0; t < total && ok; t += t_step) {
-            const Tile x = find_tile(p, sh, t, walk);
+            const Tile x = find_tile<CG>(p, sh, t, rank, walk);
             const float bias = bias_of<GATED>(p, x, quad, lane);
             const size_t row0 = (size_t)x.g * p.w.rows + x.col0;
-            if (lo < hi) {
-                ok = warp_wait(&sh->acc_full[acc], (acc_phase >> acc) & 1, sh, p);
-                if (!ok) break;
-                acc_phase ^= 1u << acc;
-                tc_fence_after();
-            }
+            ok = warp_wait(&sh->acc_full[acc], (acc_phase >> acc) & 1, sh, p);
+            if (!ok) break;
+            acc_phase ^= 1u << acc;
+            tc_fence_after();
             const uint32_t from = tmem + acc * p.acc_stride + ((uint32_t)(quad * 32) << 16);
-            for (int c = 0; c < x.cols; c += 32) {
-                float v[32];
-                if (lo < hi) {
-                    uint32_t r[32];
-                    tmem_ld32(from + c, r);
-                    tmem_ld_wait();
+            for (int c = half * kChunk; c < x.cols; c += 2 * kChunk) {
+                uint32_t r[kChunk];
+                float v[kChunk];
+                tmem_ld16(from + c, r);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
-                }
+                for (int j = 0; j < kChunk; ++j) v[j] = __uint_as_float(r[j]);
                 if (p.split > 1) {   // to shared memory, [column][lane]; joined below
                     float *part = reinterpret_cast<float *>(rings) + quad * 32 + lane;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < kChunk; ++j)
                         if (c + j < x.cols) part[(c + j) * kLanes] = v[j];
                 } else {
-                    if (c + 32 >= x.cols) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh->acc_empty[acc]);
-                    }
-                    epilogue_chunk<GATED>(p, v, row0 + c, min(32, x.cols - c), quad, lane, x.lane0, bias);
+                    if (c + 2 * kChunk >= x.cols) free_acc(acc);
+                    epilogue_chunk<GATED>(p, v, row0 + c, min(kChunk, x.cols - c), quad, lane, x.lane0, bias);
                 }
             }
+            if (p.split == 1 && half * kChunk >= x.cols) free_acc(acc);   // a warp with no columns here
             acc ^= 1;
         }
     }
     __syncthreads();
     // where a wait ran out, what is in flight is to finish (bounded) before shared and tensor
     // memory are given up
-    if (sh->abort && warp == 1 && elect_one()) drain_mma(sh);
-    if (sh->abort && threadIdx.x == 0) {
+    if (sh->abort && warp == 1 && (CG == 1 || rank == 0) && elect_one()) drain_mma<CG>(sh);
+    if (sh->abort && (threadIdx.x == 0 || threadIdx.x == 96)) {
         const uint64_t since = global_ns();
-        for (int i = max(0, issued - p.code_slots); i < issued; ++i)
-            while (!mbar_try_wait(&sh->code_full[i % p.code_slots], (uint32_t)(i / p.code_slots) & 1) &&
-                   global_ns() - since < 100000000ull)
-                ;
-        while (global_ns() - since < 1000000ull)   // x's copies, whose barriers also wait for warps that have left
+        const int slots = threadIdx.x == 0 ? p.code_slots : p.x_slots;
+        uint64_t *full = threadIdx.x == 0 ? sh->code_full : sh->x_full;
+        if (CG == 1 || threadIdx.x == 0)
+            for (int i = max(0, issued - slots); i < issued; ++i)
+                while (!mbar_try_wait(&full[i % slots], (uint32_t)(i / slots) & 1) && global_ns() - since < 100000000ull)
+                    ;
+        while (CG == 2 && global_ns() - since < 1000000ull)   // a pair's copies of x, whose barrier counts both CTAs'
             ;
     }
     tc_fence_before();
     __syncthreads();
-    if (p.split > 1) {
+    if (CG == 1 && p.split > 1) {
         // ---- a shared tile: every CTA has its sums in shared memory; each adds up its share of
         // the columns, in rank order, and finishes them
         cluster_sync();
         if (t0 < total && warp >= kFirstEpilogue) {
-            const int quad = warp % 4;
+            const int quad = warp % 4, half = (warp - kFirstEpilogue) / 4;
             walk = Walk();
-            const Tile x = find_tile(p, sh, t0, walk);
+            const Tile x = find_tile<CG>(p, sh, t0, rank, walk);
             const float bias = bias_of<GATED>(p, x, quad, lane);
             const size_t row0 = (size_t)x.g * p.w.rows + x.col0;
             const int share = (x.cols + p.split - 1) / p.split, c1 = min(x.cols, ((int)rank + 1) * share);
-            for (int c = (int)rank * share; c < c1; c += 32) {
-                const int n = min(32, c1 - c);
-                float v[32];
+            for (int c = (int)rank * share + half * kChunk; c < c1; c += 2 * kChunk) {
+                const int n = min(kChunk, c1 - c);
+                float v[kChunk];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                for (int j = 0; j < kChunk; ++j) v[j] = 0.f;
                 for (int i = 0; i < p.split; ++i) {
                     const uint32_t part = map_rank(reinterpret_cast<float *>(rings) + c * kLanes + quad * 32 + lane, i);
-                    float got[32];   // all loads on their way before the first is used
+                    float got[kChunk];   // all loads on their way before the first is used
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) got[j] = j < n ? ld_cluster_f32(part + j * kLanes * 4) : 0.f;
+                    for (int j = 0; j < kChunk; ++j) got[j] = j < n ? ld_cluster_f32(part + j * kLanes * 4) : 0.f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] += got[j];
+                    for (int j = 0; j < kChunk; ++j) v[j] += got[j];
                 }
                 epilogue_chunk<GATED>(p, v, row0 + c, n, quad, lane, x.lane0, bias);
             }
         }
         cluster_sync();   // no CTA leaves while another reads its shared memory
     }
+    if (CG == 2) cluster_sync();
     tc_fence_after();
-    if (warp == 2) tmem_free<1>(tmem, kTmemCols);
+    if (warp == 2) tmem_free<CG>(tmem, kTmemCols);
 }
 
 constexpr long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-template <bool FP4, bool GATED>
+// Pairs of CTAs, where a tile for each pair fills the GPU.
+bool plan_pairs(const W4Params &w, long long lane_tiles, int sms) {
+    const long long pairs = ceil_div(lane_tiles, 2) * w.groups * ceil_div(w.rows, kColMax);
+    return lane_tiles > 1 && 2 * pairs >= sms;
+}
+
+template <bool FP4, bool GATED, int CG>
 cudaError_t launch(const TileParams &p, long long clusters, cudaStream_t st) {
-    const auto kernel = &w4_tiles_kernel<FP4, GATED>;
+    const auto kernel = &w4_tiles_kernel<FP4, GATED, CG>;
+    const unsigned size = CG == 2 ? 2 : (unsigned)p.split;
     cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kernel), kSmemMax);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * p.split));
+    cfg.gridDim = dim3((unsigned)clusters * size);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemMax;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.split;
+    attr[0].val.clusterDim.x = size;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -579,52 +652,54 @@ int launch_w4_tiles(const W4Params &w, bool fp4, int32_t *status, cudaStream_t s
     p.wait_limit_ns = product_wait_limit();
     p.sleep_ns = p.wait_limit_ns < kSleepNs ? (uint32_t)p.wait_limit_ns : kSleepNs;
     p.lane_step = gated ? kLanes / 2 : kLanes;
-    p.lane_tiles = (int)ceil_div(w.n, p.lane_step);
-    p.col_max = w.rows < kColMax ? (int)ceil_div(w.rows, 16) * 16 : kColMax;
+    const long long single = ceil_div(w.n, p.lane_step);
+    const int cg = plan_pairs(w, single, sms) ? 2 : 1, unit = 16 * cg;
+    p.lane_tiles = (int)ceil_div(single, cg);
+    p.col_max = w.rows < kColMax ? (int)ceil_div(w.rows, unit) * unit : kColMax;
     p.steps = (int)ceil_div(w.k, kStep);
     const long long most = (long long)p.lane_tiles * w.groups * ceil_div(w.rows, p.col_max);
     if (most >= (1LL << 30)) return EP_ERR_INVALID_ARG;   // tile numbers stay within int
     // dense products with few tiles share each one's reduction (clusters of four fill 144 SMs)
     p.split = 1;
-    if (!w.counts)
+    if (!w.counts && cg == 1)
         while (p.split < kMaxSplit && most * p.split * 2 <= sms - sms / 16 && p.steps >= 2 * p.split) p.split *= 2;
-    p.x_bytes = p.col_max * kStep * 2;
-    p.scale_bytes = kLanes * 2 * (kBlock >> w.group_shift);
+    p.x_bytes = p.col_max / cg * kStep * 2;
+    p.scale_parts = kStep >> w.group_shift;
     p.acc_stride = (p.col_max + 31) / 32 * 32;
     p.slots = (kTmemCols - 2 * p.acc_stride) / kACols;   // 2 for 128 columns, 3 for 64
-    p.code_slots = (int)(kRingSpace - (size_t)p.slots * p.x_bytes) / kCodeSlot;
-    p.code_slots = p.code_slots / kTurns * kTurns;   // so that a group meets the same slots in every round: 8 or 12
+    // The rings: x waits in its own until the MMAs take it, codes only until they are expanded, up to
+    // `slots` steps earlier, so x gets what three slots of codes leave.
+    p.x_slots = (int)(kRingSpace - 3 * kCodeSlot) / p.x_bytes;
+    if (p.x_slots > kMaxXSlots) p.x_slots = kMaxXSlots;
+    p.code_slots = (int)(kRingSpace - (size_t)p.x_slots * p.x_bytes) / kCodeSlot;
     if (p.code_slots > kMaxCodeSlots) p.code_slots = kMaxCodeSlots;
     const uint64_t K = w.k, N = w.n, W = w.wide, G = w.groups, parts = K >> w.group_shift;
-    const uint32_t per_block = kBlock >> w.group_shift;
     bool good;
     if (gated) {
         // gate and up rows by turns of eight: 8 rows x (gate, up) x n / 8
         const uint64_t dims[5] = {K / 2, 8, 2, N / 8, G}, strides[4] = {K / 2, N * K / 2, 8 * K / 2, 2 * N * K / 2};
-        const uint32_t box[5] = {kBlock / 2, 8, 2, 8, 1};
-        const uint64_t sdims[5] = {8, 2, N / 8, parts, G}, sstrides[4] = {N, 8, W, W * parts};
-        const uint32_t sbox[5] = {8, 2, 8, per_block, 1};
-        good = make_map(&p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.codes, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B) &&
-               make_map(&p.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w.scales, 5, sdims, sstrides, sbox,
-                        CU_TENSOR_MAP_SWIZZLE_NONE);
+        const uint32_t box[5] = {kStep / 2, 8, 2, 8, 1};
+        good = make_map(&p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.codes, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     } else {
         const uint64_t dims[3] = {K / 2, N, G}, strides[2] = {K / 2, N * K / 2};
-        const uint32_t box[3] = {kBlock / 2, kLanes, 1};
-        const uint64_t sdims[3] = {N, parts, G}, sstrides[2] = {N, N * parts};
-        const uint32_t sbox[3] = {kLanes, per_block, 1};
-        good = make_map(&p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.codes, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B) &&
-               make_map(&p.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w.scales, 3, sdims, sstrides, sbox,
-                        CU_TENSOR_MAP_SWIZZLE_NONE);
+        const uint32_t box[3] = {kStep / 2, kLanes, 1};
+        good = make_map(&p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w.codes, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
     }
-    for (int i = 0; good && i < p.col_max / 16; ++i)
-        good = make_map3(&p.x[i], w.x, K, w.rows, G, 16u * (i + 1));
+    const uint64_t sdims[3] = {W, parts, G}, sstrides[2] = {W, W * parts};
+    const uint32_t sbox[3] = {kLanes / 2, (uint32_t)p.scale_parts, 1};
+    good = good && make_map(&p.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w.scales, 3, sdims, sstrides, sbox,
+                            CU_TENSOR_MAP_SWIZZLE_NONE);
+    for (int i = 0; good && i <= p.col_max / cg / 16; ++i)
+        good = make_map3(&p.x[i], w.x, K, w.rows, G, i ? 16u * i : 8u);
     if (!good) return EP_ERR_CUDA;
-    const long long clusters = p.split > 1 || most < sms ? most : sms;
+    const long long room = p.split > 1 ? most : sms / cg, clusters = most < room ? most : room;
     cudaError_t e;
-    if (gated)
-        e = fp4 ? launch<true, true>(p, clusters, st) : launch<false, true>(p, clusters, st);
+    if (cg == 2)
+        e = gated ? (fp4 ? launch<true, true, 2>(p, clusters, st) : launch<false, true, 2>(p, clusters, st))
+                  : (fp4 ? launch<true, false, 2>(p, clusters, st) : launch<false, false, 2>(p, clusters, st));
     else
-        e = fp4 ? launch<true, false>(p, clusters, st) : launch<false, false>(p, clusters, st);
+        e = gated ? (fp4 ? launch<true, true, 1>(p, clusters, st) : launch<false, true, 1>(p, clusters, st))
+                  : (fp4 ? launch<true, false, 1>(p, clusters, st) : launch<false, false, 1>(p, clusters, st));
     return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
 

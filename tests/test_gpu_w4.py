@@ -106,6 +106,17 @@ def test_experts(counts, rows, act, kind, group):
     experts(counts, rows, 256, 72, act, kind, group)
 
 
+@pytest.mark.parametrize("act,n", (("none", 136), ("none", 400), ("swiglu", 72), ("swiglu", 200)))
+@pytest.mark.parametrize("rows,most", ((17, 8), (40, 40), (130, 130), (300, 300)))
+def test_many_experts(act, n, rows, most):
+    """Enough tiles for pairs of CTAs, with an odd number of tiles of the weight among them, and counts on both
+    sides of what one CTA of a pair holds."""
+    g = torch.Generator().manual_seed(rows + n)
+    counts = torch.randint(0, most + 1, (90,), generator=g).tolist()
+    counts[:8] = [0, 1, min(16, most), min(17, most), min(32, most), min(33, most), most, most]
+    experts(counts, rows, 352, n, act, "fp4" if n > 150 else "int4", 32)
+
+
 def test_experts_with_leading_dimensions():
     x, codes, scales, cnt, b, r, y = experts([3, 0, 9, 40, 1, 2], 40, 128, 64, "swiglu", "fp4", 32)
     lead = lambda t: t.view(2, 3, *t.shape[1:])  # noqa: E731
