@@ -24,15 +24,18 @@ namespace ep {
 
 namespace {
 
-constexpr int kTurns = 4;            // groups of four warps that expand blocks by turns
+// Pairs of groups of four warps that expand steps by turns, half a step to a group. No more pairs
+// than slots in tensor memory: then what a group has seen of its last step tells it that its slot's
+// last use but one is over, so that the parity it waits for is not that of an older phase.
+constexpr int kTurns = 2;
+constexpr int kExpandWarps = kTurns * 8;
 constexpr int kEpilogueWarps = 8;    // two per quarter of the accumulator lanes
-constexpr int kThreads = 128 + kTurns * 128 + kEpilogueWarps * 32;
-constexpr int kFirstEpilogue = 4 + kTurns * 4;
+constexpr int kThreads = 128 + (kExpandWarps + kEpilogueWarps) * 32;
+constexpr int kFirstEpilogue = 4 + kExpandWarps;
 constexpr int kLanes = 128;          // weight rows of a tile
 constexpr int kStep = 256;           // elements of k of a block: rows of codes of 128 bytes
-constexpr int kHalf = kStep / 2;     // what one group of warps expands
 constexpr int kColMax = 128;         // rows of x of a tile, at most
-constexpr int kBoxes = 1 + kColMax / 16;   // boxes of 8, 16, 32, ... 128 rows of x
+constexpr int kBoxes = kColMax / 16;   // boxes of 16, 32, ... 128 rows of x
 constexpr int kChunk = 16;           // columns that an epilogue warp takes at once
 constexpr int kACols = kStep / 2;    // tensor-memory columns of a step: two elements to one
 constexpr int kTmemCols = 512;       // two accumulators, then steps of the weight
@@ -51,7 +54,7 @@ __global__ void take_status() { w4_status_taken = atomicExch(&w4_status, 0); }
 
 struct TileParams {
     CUtensorMap codes, scales;
-    CUtensorMap x[kBoxes];
+    CUtensorMap x[kBoxes];    // boxes of a step (k a multiple of 64), or of one line of 64 elements
     W4Params w;
     int lane_step, lane_tiles;       // output features of a tile, tiles per group
     int col_max;                     // widest column tile
@@ -60,6 +63,7 @@ struct TileParams {
     int x_slots, x_bytes;            // ring of x; bytes of a slot
     int acc_stride;                  // columns of an accumulator
     int scale_parts;                 // groups of a step
+    int whole_lines;                 // k is a multiple of 64
     int steps, split;                // steps of k; CTAs of a cluster that share them
     int32_t *status;
     uint64_t wait_limit_ns;
@@ -87,7 +91,7 @@ struct Ring {
     __device__ __forceinline__ void next(int slots) {
         if (++s == slots) s = 0, phase ^= 1;
     }
-    __device__ __forceinline__ void skip(int n, int slots) {   // n <= slots
+    __device__ __forceinline__ void skip(int n, int slots) {   // n <= slots   // n <= slots
         s += n;
         if (s >= slots) s -= slots, phase ^= 1;
     }
@@ -120,6 +124,22 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
             "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
             "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
             "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int u, uint32_t bar) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+            "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
             : "memory");
 }
 
@@ -390,28 +410,33 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
         // ---- TMA: rows of x
         for (int t = t0; t < total && ok; t += t_step) {
             const Tile x = find_tile<CG>(p, sh, t, rank, walk);
-            // of a pair each CTA holds half of the MMA's columns; boxes end with the rows in use (what
-            // lies behind them in shared memory makes columns that nobody looks at)
+            // of a pair each CTA holds half of the MMA's columns (the second's may hold no row in use:
+            // then what lies there makes columns that nobody looks at)
             const int own = x.n_mma / CG, first = x.col0 + (CG == 2 ? (int)rank * own : 0);
-            const int used = max(0, min(own, x.cols - (first - x.col0)));
-            const int rows = used <= 8 ? 8 : (used + 15) / 16 * 16;
-            const CUtensorMap *map = &p.x[used <= 8 ? 0 : rows / 16];
+            const bool any = first < x.col0 + x.cols;
+            const CUtensorMap *map = &p.x[own / 16 - 1];
             for (int ks = lo; ks < hi; ++ks, ++issued, ring.next(p.x_slots)) {
                 ok = warp_wait(&sh->x_empty[ring.s], ring.phase ^ 1, sh, p);
                 if (!ok) break;
                 if (elect_one()) {
-                    const int subs = used ? min(kStep / 64, (p.w.k - ks * kStep + 63) / 64) : 0;
+                    uint8_t *dst = xs + (size_t)ring.s * p.x_bytes;
+                    const int subs = p.whole_lines ? kStep / 64 : min(kStep / 64, (p.w.k - ks * kStep + 63) / 64);
+                    const uint32_t bytes = any ? subs * own * 128 : 0;
                     uint32_t bar;
                     if (CG == 2) {
                         bar = map_rank(&sh->x_full[ring.s], 0);
-                        mbar_arrive_expect_tx_cluster(bar, subs * rows * 128);
+                        mbar_arrive_expect_tx_cluster(bar, bytes);
                     } else {
                         bar = smem_u32(&sh->x_full[ring.s]);
-                        mbar_arrive_expect_tx(&sh->x_full[ring.s], subs * rows * 128);
+                        mbar_arrive_expect_tx(&sh->x_full[ring.s], bytes);
                     }
-                    for (int i = 0; i < subs; ++i)
-                        tma_load_3d<CG>(xs + (size_t)ring.s * p.x_bytes + i * own * 128, map, ks * kStep + i * 64, first, x.g,
-                                        bar);
+                    if (any) {
+                        if (p.whole_lines)
+                            tma_load_4d<CG>(dst, map, 0, first, ks * (kStep / 64), x.g, bar);
+                        else
+                            for (int i = 0; i < subs; ++i)
+                                tma_load_3d<CG>(dst + i * own * 128, map, ks * kStep + i * 64, first, x.g, bar);
+                    }
                 }
                 __syncwarp();
             }
@@ -430,25 +455,22 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
                 ok = role_wait(&sh->acc_empty[acc], ((acc_phase >> acc) & 1) ^ 1, sh, p);
                 if (!ok) break;
                 acc_phase ^= 1u << acc;
-                const int sub_bytes = x.n_mma / CG * 128;
-                bool more = false;
+                const uint32_t line = x.n_mma / CG * 8;   // 64 elements of all rows, in 16 bytes
                 for (int ks = lo; ks < hi; ++ks, ring.next(p.x_slots), a_ring.next(p.slots)) {
                     ok = role_wait(&sh->x_full[ring.s], ring.phase, sh, p) &&
                          role_wait(&sh->full[a_ring.s], a_ring.phase, sh, p);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t from = tmem + 2 * p.acc_stride + a_ring.s * kACols;
-                    uint64_t b = base + (uint32_t)(ring.s * p.x_bytes) / 16;
+                    const uint64_t b = base + (uint32_t)(ring.s * p.x_bytes) / 16;
                     const int left = p.w.k - ks * kStep;
+                    if (left >= kStep) {
 #pragma unroll
-                    for (int sub = 0; sub < kStep / 64; ++sub, b += sub_bytes / 16) {
-                        if (left <= sub * 64) break;
-                        mma_ts<CG>(d, from + sub * 32, b, idesc, more);
-                        more = true;
-                        mma_ts<CG>(d, from + sub * 32 + 8, b + 2, idesc, true);
-                        if (left <= sub * 64 + 32) break;
-                        mma_ts<CG>(d, from + sub * 32 + 16, b + 4, idesc, true);
-                        mma_ts<CG>(d, from + sub * 32 + 24, b + 6, idesc, true);
+                        for (int i = 0; i < kStep / 16; ++i)
+                            mma_ts<CG>(d, from + i * 8, b + (i / 4) * line + (i % 4) * 2, idesc, i > 0 || ks > lo);
+                    } else {
+                        for (int i = 0; i * 16 < left; ++i)
+                            mma_ts<CG>(d, from + i * 8, b + (i / 4) * line + (i % 4) * 2, idesc, i > 0 || ks > lo);
                     }
                     mma_commit<CG>(&sh->x_empty[ring.s]);
                     mma_commit<CG>(&sh->empty[a_ring.s]);
@@ -460,57 +482,56 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
         }
         __syncwarp();
     } else if (warp >= 4 && warp < kFirstEpilogue) {
-        // ---- codes to bf16, from shared to tensor memory; the groups take turns. What tile a block
-        // belongs to does not matter here, so a group goes from one half of a block straight to its next.
-        const int turn = (warp - 4) / 4, quad = warp % 4, row = quad * 32 + lane;
+        // ---- codes to bf16, from shared to tensor memory; pairs of groups take turns. What tile a step
+        // belongs to does not matter here, so a group goes from one of its steps straight to the next.
+        const int turn = (warp - 4) / 8, half = (warp - 4) / 4 % 2, quad = warp % 4, row = quad * 32 + lane;
         const int tiles = t0 < total ? (total - t0 - 1) / t_step + 1 : 0;
         const long long steps = (long long)tiles * (hi - lo);
         // this lane's scales: of row 64 h + j, or gated of feature j, gate (h = 0) or up
-        const int sh_h = GATED ? (row >> 3) & 1 : row / 64, sh_j = GATED ? (row >> 4) * 8 + (row & 7) : row % 64;
-        const int scale_at = kCodeBytes / 2 + sh_h * (kLanes / 2) * p.scale_parts + sh_j +
-                             (turn & 1) * (kHalf >> p.w.group_shift) * (kLanes / 2);
-        ring.s = turn / 2;
-        Ring to_ring = ring;
-        for (long long b = turn / 2; b < steps;
-             b += kTurns / 2, ring.skip(kTurns / 2, p.code_slots), to_ring.skip(kTurns / 2, p.slots)) {
+        const int h = GATED ? (row >> 3) & 1 : row / 64, j = GATED ? (row >> 4) * 8 + (row & 7) : row % 64;
+        const uint32_t scale_at = kCodeBytes + (h * (kLanes / 2) * p.scale_parts + j) * 2;
+        const uint32_t row_at = row * 128, turned = (row & 7) << 4;   // (the 128-byte swizzle)
+        const uint32_t to0 = tmem + 2 * p.acc_stride + half * (kACols / 2) + ((uint32_t)(quad * 32) << 16);
+        ring.skip(turn, p.code_slots);
+        Ring to_ring;
+        to_ring.skip(turn, p.slots);
+        for (long long b = turn; b < steps; b += kTurns, ring.skip(kTurns, p.code_slots), to_ring.skip(kTurns, p.slots)) {
             ok = warp_wait(&sh->code_full[ring.s], ring.phase, sh, p);
             if (!ok) break;
             const uint8_t *slot = cs + ring.s * kCodeSlot;
+            const uint32_t to = to0 + to_ring.s * kACols;
             uint4 c[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)   // (the 128-byte swizzle)
-                c[i] = *reinterpret_cast<const uint4 *>(slot + row * 128 + ((((turn & 1) * 4 + i) ^ (row & 7)) << 4));
-            W4Scale<FP4> scale[4];
-            const __nv_bfloat16 *sc = reinterpret_cast<const __nv_bfloat16 *>(slot) + scale_at;
+            for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4 *>(slot + row_at + ((64 * half + 16 * i) ^ turned));
+            __nv_bfloat16 raw[4];   // of 32 elements each
 #pragma unroll
-            for (int i = 0; i < 4; ++i) scale[i] = W4Scale<FP4>(sc[((i * 32) >> p.w.group_shift) * (kLanes / 2)]);
-            const uint32_t to = tmem + 2 * p.acc_stride + to_ring.s * kACols + (turn & 1) * (kHalf / 2) +
-                                ((uint32_t)(quad * 32) << 16);
-            const bool large = __any_sync(kAll, scale[0].large() || scale[1].large() || scale[2].large() || scale[3].large());
+            for (int i = 0; i < 4; ++i)
+                raw[i] = *reinterpret_cast<const __nv_bfloat16 *>(
+                    slot + scale_at + ((half * 4 + i) >> (p.w.group_shift - 5)) * kLanes);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int i = 0; i < 2; ++i) {   // 64 elements, 32 columns of tensor memory, at a time
                 uint32_t r[32];
-                if (large) {
-                    expand<FP4, true>(c[2 * h], scale[2 * h], r);
-                    expand<FP4, true>(c[2 * h + 1], scale[2 * h + 1], r + 16);
+                const W4Scale<FP4> s0(raw[2 * i]), s1(raw[2 * i + 1]);
+                if (__any_sync(kAll, s0.large() || s1.large())) {
+                    expand<FP4, true>(c[2 * i], s0, r);
+                    expand<FP4, true>(c[2 * i + 1], s1, r + 16);
                 } else {
-                    expand<FP4, false>(c[2 * h], scale[2 * h], r);
-                    expand<FP4, false>(c[2 * h + 1], scale[2 * h + 1], r + 16);
+                    expand<FP4, false>(c[2 * i], s0, r);
+                    expand<FP4, false>(c[2 * i + 1], s1, r + 16);
                 }
-                if (h == 0) {   // (the slot's MMAs may take as long as the first half)
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh->code_empty[ring.s]);
+                if (i == 0) {   // (the slot's MMAs may take as long as the first part)
                     ok = warp_wait(&sh->empty[to_ring.s], to_ring.phase ^ 1, sh, p);
                     if (!ok) break;
                     tc_fence_after();
                 }
-                tmem_st32(to + h * 32, r);
+                tmem_st32(to + i * 32, r);
             }
             if (!ok) break;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
+                mbar_arrive(&sh->code_empty[ring.s]);
                 if (CG == 2) mbar_arrive_remote(map_rank(&sh->full[to_ring.s], 0));
                 else mbar_arrive(&sh->full[to_ring.s]);
             }
@@ -689,8 +710,17 @@ int launch_w4_tiles(const W4Params &w, bool fp4, int32_t *status, cudaStream_t s
     const uint32_t sbox[3] = {kLanes / 2, (uint32_t)p.scale_parts, 1};
     good = good && make_map(&p.scales, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, w.scales, 3, sdims, sstrides, sbox,
                             CU_TENSOR_MAP_SWIZZLE_NONE);
-    for (int i = 0; good && i <= p.col_max / cg / 16; ++i)
-        good = make_map3(&p.x[i], w.x, K, w.rows, G, i ? 16u * i : 8u);
+    p.whole_lines = w.k % 64 == 0;
+    for (int i = 0; good && i < p.col_max / cg / 16; ++i) {
+        const uint32_t rows = 16u * (i + 1);
+        if (p.whole_lines) {   // a step's lines of 64 elements, each with its rows
+            const uint64_t dims[4] = {64, (uint64_t)w.rows, K / 64, G}, strides[3] = {K, 64, K * w.rows};
+            const uint32_t box[4] = {64, rows, kStep / 64, 1};
+            good = make_map(&p.x[i], w.x, 4, dims, strides, box);
+        } else {
+            good = make_map3(&p.x[i], w.x, K, w.rows, G, rows);
+        }
+    }
     if (!good) return EP_ERR_CUDA;
     const long long room = p.split > 1 ? most : sms / cg, clusters = most < room ? most : room;
     cudaError_t e;
