@@ -19,23 +19,24 @@ _I32, _F32 = torch.int32, torch.float32
 def _args(logits: torch.Tensor, top_k: int, score: str, per_sequence: bool,
           num_tokens: Optional[torch.Tensor]) -> Tuple[L.EpBalanceC, Tuple[int, ...]]:
     """The call's arguments and the shape of counts."""
-    code, kind = _SCORES.get(score), _TYPES.get(logits.dtype)
+    code, kind, shape = _SCORES.get(score), _TYPES.get(logits.dtype), logits.shape
     if code is None:
         raise ValueError(f"score: want one of {sorted(_SCORES)}, got {score!r}")
-    if kind is None or logits.dim() < 2 or not logits.is_contiguous() or not logits.is_cuda:
+    if kind is None or len(shape) < 2 or not logits.is_contiguous() or not logits.is_cuda:
         raise ValueError(f"logits: want contiguous bfloat16 or float32 [..., T, E] on a CUDA device, got "
                          f"{logits.dtype} {tuple(logits.shape)} on {logits.device} "
                          f"(contiguous={logits.is_contiguous()})")
-    lead, (tokens, E) = logits.shape[:-2], logits.shape[-2:]
-    seqs = prod(lead)
+    lead, tokens, E = shape[:-2], shape[-2], shape[-1]
+    seqs = lead[0] if len(lead) == 1 else prod(lead)
     if not 1 <= E <= L.EP_MAX_E or not 1 <= top_k <= min(E, L.EP_MAX_TOPK) or max(seqs, tokens, seqs * tokens) > INT32_MAX:
         raise ValueError(f"want 1..{L.EP_MAX_E} experts, top_k in 1..min(E, {L.EP_MAX_TOPK}) and at most {INT32_MAX} "
                          f"tokens, got {tuple(logits.shape)}, top_k={top_k}")
+    ptr = None
     if num_tokens is not None:
-        _want(num_tokens, "num_tokens", tuple(lead) or (1,), logits.device, _I32)
-    a = L.EpBalanceC(seqs, tokens, E, top_k, code, 1 if per_sequence else 0, kind,
-                     None if num_tokens is None else num_tokens.data_ptr())
-    return a, (tuple(lead) if per_sequence else ()) + (E,)
+        _want(num_tokens, "num_tokens", lead or (1,), logits.device, _I32)
+        ptr = num_tokens.data_ptr()
+    a = L.EpBalanceC(seqs, tokens, E, top_k, code, 1 if per_sequence else 0, kind, ptr)
+    return a, (lead + (E,) if per_sequence else (E,))
 
 
 def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, *, score: str = "softmax", per_sequence: bool = False,
@@ -60,10 +61,11 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, *, score: str = "
     dev = logits.device
     _want(topk_ids, "topk_ids", logits.shape[:-1] + (a.top_k,), dev, _I32)
     size, lib = C.c_size_t(), L.lib()
-    L.check(lib.ep_balance_workspace_bytes(C.byref(a), C.byref(size)), "ep_balance_workspace_bytes")
+    args = C.byref(a)
+    L.check(lib.ep_balance_workspace_bytes(args, C.byref(size)), "ep_balance_workspace_bytes")
     losses, counts = empty((2,), _F32, dev, stream), empty(shape, _I32, dev, stream)
     work = empty((size.value,), torch.uint8, dev, stream)
-    L.check(lib.ep_balance_loss(C.byref(a), logits.data_ptr(), topk_ids.data_ptr(), losses.data_ptr(), counts.data_ptr(),
+    L.check(lib.ep_balance_loss(args, logits.data_ptr(), topk_ids.data_ptr(), losses.data_ptr(), counts.data_ptr(),
                                 work.data_ptr(), size.value, stream_of(stream, dev)), "ep_balance_loss")
     return losses, counts
 

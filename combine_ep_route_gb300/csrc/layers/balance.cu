@@ -33,7 +33,6 @@ constexpr int kMaxChunk = 4096;      // tokens of a CTA, at most: bounds the cha
 constexpr int kFinishThreads = 1024;
 constexpr int kSlice = 32;           // experts of a finishing CTA
 constexpr int kBackThreads = 256;
-constexpr float kLn2 = 0.69314718055994531f;
 
 struct BalanceParams {
     const void *logits;
@@ -44,7 +43,7 @@ struct BalanceParams {
     const float *dlosses;
     void *dlogits;
     uint32_t *ticket;
-    double *slots;    // [pools][slices]
+    float *slots;     // [pools][slices]
     float *zpart;     // [pools][chunks]
     float *part;      // [pools][chunks][E]
     int32_t *cpart;   // [pools][chunks][E]
@@ -262,7 +261,19 @@ __device__ __forceinline__ Lengths lengths(const BalanceParams &p, int pool) {
     return {all, all, all > 0};
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
+// A fp32 sum with what rounding took from it. (In 64 bits, of which this GPU does two additions a
+// cycle and SM, the second kernel and the gradient's few divisions took more time than all the rest:
+// 8 sequences of 1024 tokens, both directions, 46 us.)
+struct Sum {
+    float s = 0.f, lost = 0.f;
+    __device__ __forceinline__ void add(float v) {
+        const float sum = __fadd_rn(s, v), part = __fsub_rn(sum, s);
+        lost += __fadd_rn(__fsub_rn(s, __fsub_rn(sum, part)), __fsub_rn(v, part));
+        s = sum;
+    }
+    __device__ __forceinline__ float value() const { return s <= FLT_MAX ? s + lost : s; }   // (infinite: lost is NaN)
+};
+__device__ __forceinline__ float warp_sum(float v) {
     for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(kAll, v, d);
     return v;
 }
@@ -271,9 +282,9 @@ __device__ __forceinline__ double warp_sum(double v) {
 // slice's part of the pool's loss; the last CTA to finish adds the parts up.
 __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const BalanceParams p) {
     constexpr int kRows = kFinishThreads / kSlice;
-    __shared__ double ps[kRows][kSlice];
-    __shared__ int32_t cs[kRows][kSlice];
-    __shared__ double parts[2][kFinishThreads / 32];
+    __shared__ float ps[kRows][kSlice + 1];
+    __shared__ int32_t cs[kRows][kSlice + 1];
+    __shared__ float parts[2][kFinishThreads / 32];
     __shared__ Lengths n;
     __shared__ bool last;
     pdl_launch_dependents();
@@ -281,31 +292,37 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
     const int slices = (p.E + kSlice - 1) / kSlice;
     const int pool = blockIdx.x / slices, slice = blockIdx.x % slices;
     const int col = threadIdx.x % kSlice, row = threadIdx.x / kSlice, e = slice * kSlice + col;
-    if (row == 0) {
-        const Lengths own = lengths(p, pool);
-        if (col == 0) n = own;
-    }
-    double sum = 0;
+    Sum sum;
     int32_t count = 0;
     if (e < p.E) {
         const size_t at = (size_t)pool * p.chunks * p.E + e;
 #pragma unroll 5
         for (int c = row; c < p.chunks; c += kRows) {
-            sum += p.part[at + (size_t)c * p.E];
+            sum.add(p.part[at + (size_t)c * p.E]);
             count += p.cpart[at + (size_t)c * p.E];
         }
     }
-    ps[row][col] = sum, cs[row][col] = count;
+    ps[row][col] = sum.value(), cs[row][col] = count;
+    if (row == kRows - 1) {
+        const Lengths own = lengths(p, pool);
+        if (col == 0) n = own;
+    }
+    __syncthreads();
+    // a warp per expert adds the rows up by a tree
+    const float psum = warp_sum(ps[col][row]);
+    const int32_t csum = __reduce_add_sync(kAll, cs[col][row]);
+    const int e2 = slice * kSlice + row;
+    if (col == 0) {
+        float v = 0.f;
+        if (e2 < p.E) {
+            p.counts[(size_t)pool * p.E + e2] = csum;
+            if (n.pool > 0) v = (float)csum * p.E / ((float)p.K * n.pool) * (psum / n.pool);
+        }
+        parts[0][row] = v;
+    }
     __syncthreads();
     if (row == 0) {
-        sum = 0, count = 0;
-        for (int r = 0; r < kRows; ++r) sum += ps[r][col], count += cs[r][col];
-        double v = 0;
-        if (e < p.E) {
-            p.counts[(size_t)pool * p.E + e] = count;
-            if (n.pool > 0) v = (double)count * p.E / ((double)p.K * n.pool) * (sum / n.pool);
-        }
-        v = warp_sum(v);
+        const float v = warp_sum(parts[0][col]);
         if (col == 0) {
             p.slots[blockIdx.x] = v;
             __threadfence();
@@ -315,18 +332,18 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
     __syncthreads();
     if (!last) return;
     __threadfence();
-    double b = 0, z = 0;
-    for (int i = threadIdx.x; i < (int)gridDim.x; i += kFinishThreads) b += __ldcg(p.slots + i);
+    Sum b, z;
+    for (int i = threadIdx.x; i < (int)gridDim.x; i += kFinishThreads) b.add(__ldcg(p.slots + i));
     const long long all = (long long)p.pools * p.chunks;
-    for (long long i = threadIdx.x; i < all; i += kFinishThreads) z += p.zpart[i];
-    b = warp_sum(b), z = warp_sum(z);
-    if (threadIdx.x % 32 == 0) parts[0][threadIdx.x / 32] = b, parts[1][threadIdx.x / 32] = z;
+    for (long long i = threadIdx.x; i < all; i += kFinishThreads) z.add(p.zpart[i]);
+    const float bw = warp_sum(b.value()), zw = warp_sum(z.value());
+    if (threadIdx.x % 32 == 0) parts[0][threadIdx.x / 32] = bw, parts[1][threadIdx.x / 32] = zw;
     __syncthreads();
     if (threadIdx.x < 32) {
-        b = warp_sum(parts[0][threadIdx.x]), z = warp_sum(parts[1][threadIdx.x]);
+        const float bs = warp_sum(parts[0][threadIdx.x]), zt = warp_sum(parts[1][threadIdx.x]);
         if (threadIdx.x == 0) {
-            p.losses[0] = n.pools > 0 ? (float)(b / n.pools) : 0.f;
-            p.losses[1] = n.all > 0 ? (float)(z / n.all) : 0.f;
+            p.losses[0] = n.pools > 0 ? bs / n.pools : 0.f;
+            p.losses[1] = n.all > 0 ? zt / n.all : 0.f;
         }
     }
 }
@@ -396,12 +413,12 @@ __global__ void __launch_bounds__(kBackThreads) balance_backward_kernel(const Ba
     const Lengths n = lens;
     float g[M];
     const float d0 = p.dlosses[0], d1 = p.dlosses[1];
-    const double unit = n.pool > 0 ? (double)d0 * p.E / ((double)p.K * n.pool * n.pool * n.pools) : 0.;
-    const float zunit = n.all > 0 ? (float)(2. * d1 / n.all) : 0.f;
+    const float unit = n.pool > 0 ? d0 * p.E / ((float)p.K * n.pool) / ((float)n.pool * n.pools) : 0.f;
+    const float zunit = n.all > 0 ? 2.f * d1 / n.all : 0.f;
 #pragma unroll
     for (int j = 0; j < M; ++j) {
         const int e = expert_of<G, VEC>(lane, j);
-        g[j] = e < p.E ? (float)(unit * p.counts_in[(size_t)pool * p.E + e]) : 0.f;
+        g[j] = e < p.E ? unit * p.counts_in[(size_t)pool * p.E + e] : 0.f;
     }
     constexpr int kAtOnce = kBackThreads / G, kPerWarp = 32 / G;
     const long long lo = (long long)chunk * p.chunk;
@@ -485,8 +502,8 @@ size_t place(BalanceParams &p, uint8_t *base) {
     size_t at = 0;
     p.ticket = reinterpret_cast<uint32_t *>(base);
     at += 16;
-    p.slots = reinterpret_cast<double *>(base + at);
-    at += align16(p.pools * slices * 8);
+    p.slots = reinterpret_cast<float *>(base + at);
+    at += align16(p.pools * slices * 4);
     p.zpart = reinterpret_cast<float *>(base + at);
     at += align16(chunks * 4);
     p.part = reinterpret_cast<float *>(base + at);

@@ -51,11 +51,6 @@ struct ClipParams {
     int write_norm, copy; // whether this launch writes the norm; copy where nothing is scaled
 };
 
-__device__ __forceinline__ double warp_sum(double v) {
-    for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(kAll, v, d);
-    return v;
-}
-
 struct Piece {
     const void *in;
     void *out;
@@ -83,18 +78,35 @@ __device__ __forceinline__ Piece piece_of(const List<N> &list, uint32_t i) {
 }
 
 // mid is of the piece at hand; kept and lost are its earlier ones, as a sum and what rounding took
-// from it (sums in 64 bits would take half of what the GPU does in them).
+// from it. (This GPU does two 64-bit additions a cycle and SM, so they are few: two for a warp's sum
+// and one for each warp and CTA.)
 struct Squares {
     float mid = 0.f, low = 0.f, high = 0.f, kept = 0.f, lost = 0.f;
-    __device__ __forceinline__ void end_piece() {
-        const float sum = __fadd_rn(kept, mid), part = __fsub_rn(sum, kept);
-        lost += __fadd_rn(__fsub_rn(kept, __fsub_rn(sum, part)), __fsub_rn(mid, part));
-        kept = sum, mid = 0.f;
+    __device__ __forceinline__ void keep(float v) {
+        const float sum = __fadd_rn(kept, v), part = __fsub_rn(sum, kept);
+        lost += __fadd_rn(__fsub_rn(kept, __fsub_rn(sum, part)), __fsub_rn(v, part));
+        kept = sum;
     }
-    __device__ __forceinline__ double total() const {
+    __device__ __forceinline__ void end_piece() {
+        keep(mid);
+        mid = 0.f;
+    }
+    // The warp's sum, in all lanes.
+    __device__ __forceinline__ double warp_total() {
+        for (int d = 16; d > 0; d /= 2) {
+            const float other = __shfl_xor_sync(kAll, kept, d);
+            lost += __shfl_xor_sync(kAll, lost, d);
+            // (the same in both: the larger first)
+            const float a = fmaxf(kept, other), b = fminf(kept, other);
+            kept = kept == kept && other == other ? a : kept + other;
+            keep(kept == kept ? b : 0.f);
+            low += __shfl_xor_sync(kAll, low, d);
+            high += __shfl_xor_sync(kAll, high, d);
+        }
         // (past the largest float `lost` is NaN, and the sum infinite)
-        const double first = kept <= 3.402823466e38f ? (double)kept + lost : (double)kept;
-        return first + (double)low * 0x1p-200 + (double)high * 0x1p200;
+        double sum = kept <= 3.402823466e38f ? (double)kept + lost : (double)kept;
+        if (low != 0.f || high != 0.f) sum += (double)low * 0x1p-200 + (double)high * 0x1p200;
+        return sum;
     }
 };
 
@@ -187,29 +199,33 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
         if (x.bf16) piece_squares<true>(x, s);
         else piece_squares<false>(x, s);
     }
-    double sum = warp_sum(s.total());
+    const double sum = s.warp_total();
     if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = sum;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        sum = warp_sum(threadIdx.x < kThreads / 32 ? parts[threadIdx.x] : 0.);
-        if (threadIdx.x == 0) p.partial[p.base + blockIdx.x] = sum;
+    if (threadIdx.x == 0) {
+        double all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) all += parts[w];
+        p.partial[p.base + blockIdx.x] = all;
     }
 }
 
-// The norm from the sums, the same in every CTA.
-__device__ __forceinline__ double norm_of(const ClipParams &p) {
-    __shared__ double parts[kThreads / 32], all;
-    double sum = 0;
-    for (int i = threadIdx.x; i < p.partials; i += kThreads) sum += p.partial[i];
-    sum = warp_sum(sum);
-    if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = sum;
-    __syncthreads();
+// The norm from the sums, the same in every CTA, and the factor that it asks for (-1: none).
+__device__ __forceinline__ float factor_of(const ClipParams &p, bool write) {
+    __shared__ float factor;
     if (threadIdx.x < 32) {
-        sum = warp_sum(threadIdx.x < kThreads / 32 ? parts[threadIdx.x] : 0.);
-        if (threadIdx.x == 0) all = sqrt(sum);
+        double sum = 0;
+        for (int i = threadIdx.x; i < p.partials; i += 32) sum += p.partial[i];
+        for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(kAll, sum, d);
+        if (threadIdx.x == 0) {
+            const double norm = sqrt(sum);
+            if (write) *p.norm = (float)norm;
+            // (a NaN compares false)
+            const bool clip = norm > (double)p.max_norm && norm <= kDoubleMax;
+            factor = clip ? (float)((double)p.max_norm / norm) : -1.f;
+        }
     }
     __syncthreads();
-    return all;
+    return factor;
 }
 
 template <bool BF16>
@@ -256,12 +272,11 @@ template <int N>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ List<N> list, const ClipParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    const double norm = norm_of(p);
-    if (p.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
-    // (a NaN compares false)
-    const bool clip = norm > (double)p.max_norm && norm <= kDoubleMax;
-    if (!clip && !p.copy) return;
-    const float factor = clip ? (float)((double)p.max_norm / norm) : 1.f;
+    float factor = factor_of(p, p.write_norm && blockIdx.x == 0);
+    if (factor < 0.f) {   // nothing to scale
+        if (!p.copy) return;
+        factor = 1.f;
+    }
     const uint32_t pieces = list.first[list.n];
     for (uint32_t i = blockIdx.x; i < pieces; i += gridDim.x) {
         const Piece x = piece_of(list, pieces - 1 - i);
@@ -273,8 +288,7 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
 __global__ void __launch_bounds__(kThreads) norm_kernel(const ClipParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    const double norm = norm_of(p);
-    if (threadIdx.x == 0) *p.norm = (float)norm;
+    factor_of(p, true);
 }
 
 // The tensors [from, to) of the list, as one launch takes them.

@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes as C
+from array import array
 from typing import Optional, Sequence
 
 import torch
@@ -29,27 +30,32 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optio
         raise ValueError(f"max_norm: want a number from 0, got {max_norm}")
     if len(outs) != len(grads):
         raise ValueError(f"out: want {len(grads)} tensors, got {len(outs)}")
-    n, dev = len(grads), grads[0].device
+    n, dev, at = len(grads), grads[0].device, grads[0].get_device()
     if n > INT32_MAX:
         raise ValueError("grads: too many")
+    tracked = torch.is_grad_enabled()
+    kinds = []
     for t in grads:
-        if t.dtype not in _OUT or not t.is_cuda or t.device != dev or not t.is_contiguous():
+        kind = _OUT.get(t.dtype)
+        if kind is None or at < 0 or t.get_device() != at or not t.is_contiguous():
             raise ValueError(f"grads: want contiguous bfloat16 or float32 on one CUDA device, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
-        if t.requires_grad:
+        if tracked and t.requires_grad:
             untracked(grads=t)
+        kinds.append(kind)
+    # (arrays of 64 and 32 bits: a ctypes array of as many pointers takes several times as long to fill)
+    ptrs, to = array("Q", [t.data_ptr() for t in grads]), None
     if out is not None:
         for o, t in zip(outs, grads):
-            if o.dtype != t.dtype or o.shape != t.shape or o.device != dev or not o.is_contiguous():
+            if o.dtype is not t.dtype or o.shape != t.shape or o.get_device() != at or not o.is_contiguous():
                 raise ValueError(f"out: want contiguous {t.dtype} {tuple(t.shape)} on {dev}, got {o.dtype} "
                                  f"{tuple(o.shape)} on {o.device} (contiguous={o.is_contiguous()})")
-            if o.requires_grad:
+            if tracked and o.requires_grad:
                 untracked(out=o)
-    ptrs = (C.c_void_p * n)(*[t.data_ptr() for t in grads])
-    to = None if out is None else (C.c_void_p * n)(*[t.data_ptr() for t in outs])
-    numel = (C.c_int64 * n)(*[t.numel() for t in grads])
-    kinds = (C.c_int32 * n)(*[_OUT[t.dtype] for t in grads])
-    a = L.EpGradsC(n, C.addressof(ptrs), None if to is None else C.addressof(to), C.addressof(numel), C.addressof(kinds))
+        to = array("Q", [t.data_ptr() for t in outs])
+    numel, kinds = array("q", [t.numel() for t in grads]), array("i", kinds)
+    a = L.EpGradsC(n, ptrs.buffer_info()[0], None if to is None else to.buffer_info()[0], numel.buffer_info()[0],
+                   kinds.buffer_info()[0])
     size, lib = C.c_size_t(), L.lib()
     L.check(lib.ep_clip_workspace_bytes(C.byref(a), C.byref(size)), "ep_clip_workspace_bytes")
     norm, work = empty((), torch.float32, dev, stream), empty((size.value,), torch.uint8, dev, stream)
