@@ -55,13 +55,13 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, *, score: str = "
     """
     if topk_ids.dim() < 1:
         raise ValueError("topk_ids: want [..., T, top_k]")
-    a, shape = _args(logits, topk_ids.shape[-1], score, per_sequence, num_tokens)
+    K = topk_ids.shape[-1]
+    a, shape = _args(logits, K, score, per_sequence, num_tokens)
     if logits.requires_grad:
         untracked(logits=logits)
     dev = logits.device
-    _want(topk_ids, "topk_ids", logits.shape[:-1] + (a.top_k,), dev, _I32)
-    size, lib = C.c_size_t(), L.lib()
-    args = C.byref(a)
+    _want(topk_ids, "topk_ids", logits.shape[:-1] + (K,), dev, _I32)
+    size, lib, args = C.c_size_t(), L.lib(), C.byref(a)
     L.check(lib.ep_balance_workspace_bytes(args, C.byref(size)), "ep_balance_workspace_bytes")
     losses, counts = empty((2,), _F32, dev, stream), empty(shape, _I32, dev, stream)
     work = empty((size.value,), torch.uint8, dev, stream)

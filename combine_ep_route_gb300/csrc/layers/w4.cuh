@@ -45,7 +45,7 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
 
 // A group's scale, in both halves of a register each time. A masked field is a subnormal bf16
 // (below), so the scale carries the power of two that makes up for it; where that would overflow
-// (`large`: rare for a weight, and infinity and NaN) the values are brought up first, in a product
+// (is_large: rare for a weight) the values are brought up first, in a product
 // more each.
 //   int4: by = scale * 2^133, by16 = scale * 2^129, off = -8 scale, for scales below 2^-5
 //   fp4:  by = scale * 2^126, for scales below 4
@@ -62,8 +62,13 @@ struct W4Scale {
             off = __hmul2(scale, bf162_of(0xC100C100u));                      // -8
         }
     }
-    __device__ __forceinline__ bool large() const { return (u32_of(scale) & 0x7FFFu) >= (FP4 ? 0x4080u : 0x3D00u); }
 };
+
+// Whether a scale is too large for the powers above, infinite or NaN.
+template <bool FP4>
+__device__ __forceinline__ bool is_large(__nv_bfloat16 scale) {
+    return (__bfloat16_as_ushort(scale) & 0x7FFFu) >= (FP4 ? 0x4080u : 0x3D00u);   // 4, 2^-5
+}
 
 // The eight weights of a word, in order, as four pairs. All steps but the last are exact, so a
 // weight is rounded once, from value * scale.
@@ -93,7 +98,8 @@ __device__ __forceinline__ void w4_values(uint32_t word, const W4Scale<FP4> &s, 
     }
 }
 
-cudaError_t launch_w4_rows(const W4Params &p, bool fp4, cudaStream_t st);
+cudaError_t launch_w4_rows(const W4Params &p, bool fp4, int32_t *status, cudaStream_t st);
+int take_w4_rows_status(cudaStream_t st);
 int launch_w4_tiles(const W4Params &p, bool fp4, int32_t *status, cudaStream_t st);
 
 }  // namespace ep

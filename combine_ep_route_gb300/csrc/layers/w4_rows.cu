@@ -1,28 +1,50 @@
 // w4_rows.cu -- products with 4-bit weights for few rows of x, and the entry point.
 //
-// The weight's codes bound it. A CTA takes 16 (or 32) rows of the weight and all of k, split
-// over its warps; each lane reads 16 bytes of codes, 32 elements, of two weight rows straight
-// into registers, makes bf16 pairs of them and multiplies them with up to four tiles of eight
-// rows of x by mma.sync (m16n8k16, the weight's rows along m): an MMA's contraction may take the
+// The weight's codes bound it, and for a single small weight the latency of getting them. A CTA
+// takes 16 rows of the weight (of a gated one 8 gate rows and the 8 up rows that belong to them)
+// and all of k, which bulk copies bring to shared memory in one piece where three CTAs' pieces fit
+// an SM, else in chunks, three on their way at a time; a chunk's elements are split over the warps. Each lane takes 32 elements, 16 bytes, of two
+// weight rows at a time, makes bf16 pairs of them and multiplies them with one or two tiles of
+// eight rows of x by mma.sync (m16n8k16, the weight's rows along m): an MMA's contraction may take the
 // elements in any order that both operands share, so a lane's elements are those that lie
-// together in memory. (tcgen05.mma wants its operands in shared or tensor memory and 64 or 128
-// weight rows at once; few rows of x make no use of its rate.) The warps' sums are joined in
-// shared memory, in order.
+// together in memory. (tcgen05.mma wants 128 weight rows at once; few rows of x make no use of its
+// rate.) The warps' sums are joined in shared memory, in order.
 #include "w4.cuh"
 
 #include <nvtx3/nvToolsExt.h>
 
 #include "act.cuh"
+#include "tcgen05.cuh"
 
 namespace ep {
 
 namespace {
 
+constexpr int kFewRows = 16;   // row slots of a group that this kernel takes
+constexpr long long kFewBytes = 20 << 20;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 128;     // elements of k that a warp takes at once: 32 per lane of a row's four
-constexpr int kFewRows = 16;   // row slots of a group for which this kernel is the faster one
-constexpr int kFlight = 2;     // steps whose codes are on their way together
+constexpr int kRows = 16;      // of the weight
+constexpr int kSub = 128;      // elements of k that a warp takes at once: 32 per lane of a row's four
+constexpr int kStages = 3;
+constexpr int kWholeBytes = 74 * 1024;   // of a piece, so that three CTAs fit an SM
+constexpr int kCodePad = 64;   // bytes between rows of codes, of x: their banks differ
+constexpr int kXPad = 32;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr uint32_t kSleepNs = 1000000;
+
+struct RowsParams {
+    W4Params w;
+    int chunk;        // elements of k of a stage, a multiple of kSub * kWarps
+    int stages, stage_bytes;
+    int32_t *status;
+    uint64_t wait_limit_ns;
+    uint32_t sleep_ns;
+};
+
+__device__ int32_t rows_status, rows_status_taken;
+
+__global__ void take_status() { rows_status_taken = atomicExch(&rows_status, 0); }
 
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1) {
@@ -32,123 +54,195 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// MT tiles of 16 weight rows, up to NT tiles of 8 rows of x at once. A gated tile holds 8 gate
-// rows and the 8 up rows that belong to them, which are 8 apart in an accumulator.
-template <int MT, int NT, bool FP4, bool GATED>
-__global__ void __launch_bounds__(kThreads) w4_rows_kernel(const W4Params p) {
-    constexpr int kFeatures = MT * (GATED ? 8 : 16);   // of the output
-    constexpr int kCols = NT * 8;
-    __shared__ float sums[kWarps][MT * 16][kCols + 1];
-    pdl_launch_dependents();
-    pdl_wait();
-    const int g = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int count = p.counts ? max(0, min(p.counts[g], p.rows)) : p.rows;
-    const int f0 = blockIdx.x * kFeatures;
-    const int r = lane / 4, t = lane % 4;
-    // this lane's weight rows (past the last feature: the last, which nobody looks at)
-    int row[2 * MT];
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// 32 elements of two weight rows against NT tiles of x.
+template <int NT, bool FP4, bool LARGE>
+__device__ __forceinline__ void multiply(float (&acc)[NT][4], const uint4 (&code)[2], const __nv_bfloat16 (&raw)[2],
+                                         const uint8_t *x, uint32_t x_stride, int cols, int r) {
+    const W4Scale<FP4> s0(raw[0]), s1(raw[1]);
+    const uint32_t words[2][4] = {{code[0].x, code[0].y, code[0].z, code[0].w}, {code[1].x, code[1].y, code[1].z, code[1].w}};
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i)
-        row[i] = GATED ? min(f0 + (i / 2) * 8 + r, p.n - 1) + (i % 2) * p.n : min(f0 + i * 8 + r, p.n - 1);
-    const uint8_t *codes = p.codes + (size_t)g * p.wide * (p.k / 2);
-    const __nv_bfloat16 *scales = p.scales + (size_t)g * (p.k >> p.group_shift) * p.wide;
-    const int steps = (p.k + kStep - 1) / kStep;
-    for (int c0 = 0; c0 < count; c0 += kCols) {
-        const __nv_bfloat16 *x = p.x + ((size_t)g * p.rows + c0) * p.k;
-        const int cols = min(kCols, count - c0);
-        float acc[MT][NT][4] = {};
-        for (int s0 = warp; s0 < steps; s0 += kWarps * kFlight) {
-            uint4 code[kFlight][2 * MT];
-            __nv_bfloat16 raw[kFlight][2 * MT];
+    for (int w = 0; w < 4; ++w) {
+        uint32_t a[2][4];
+        w4_values<FP4, LARGE>(words[0][w], s0, a[0]);
+        w4_values<FP4, LARGE>(words[1][w], s1, a[1]);
 #pragma unroll
-            for (int q = 0; q < kFlight; ++q) {
-                const int e = (s0 + q * kWarps) * kStep + t * 32;   // this lane's first element
-#pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) {
-                    code[q][i] = make_uint4(0, 0, 0, 0);
-                    raw[q][i] = __ushort_as_bfloat16(0);
-                    if (e < p.k) {
-                        code[q][i] = __ldcs(reinterpret_cast<const uint4 *>(codes + (size_t)row[i] * (p.k / 2) + e / 2));
-                        raw[q][i] = scales[(size_t)(e >> p.group_shift) * p.wide + row[i]];
-                    }
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < kFlight; ++q) {
-                const int e = (s0 + q * kWarps) * kStep + t * 32;
-                if (s0 + q * kWarps >= steps) break;   // the same for the whole warp
-                bool large = false;
-                W4Scale<FP4> scale[2 * MT];
-#pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) {
-                    scale[i] = W4Scale<FP4>(raw[q][i]);
-                    large |= scale[i].large();
-                }
-                large = __any_sync(0xFFFFFFFFu, large);
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t a[2 * MT][4];
-#pragma unroll
-                    for (int i = 0; i < 2 * MT; ++i) {
-                        const uint4 c = code[q][i];
-                        const uint32_t word = w == 0 ? c.x : w == 1 ? c.y : w == 2 ? c.z : c.w;
-                        if (large) w4_values<FP4, true>(word, scale[i], a[i]);
-                        else w4_values<FP4, false>(word, scale[i], a[i]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        if (j * 8 >= cols) break;
-                        uint4 b = make_uint4(0, 0, 0, 0);
-                        if (e < p.k && j * 8 + r < cols)
-                            b = *reinterpret_cast<const uint4 *>(x + (size_t)(j * 8 + r) * p.k + e + w * 8);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            mma_16x8x16(acc[m][j], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], b.x, b.y);
-                            mma_16x8x16(acc[m][j], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], b.z, b.w);
-                        }
-                    }
-                }
-            }
-        }
-        __syncthreads();   // the last tile's sums have been read
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sums[warp][m * 16 + (i / 2) * 8 + r][j * 8 + t * 2 + i % 2] = acc[m][j][i];
-        __syncthreads();
-        for (int i = threadIdx.x; i < kFeatures * cols; i += kThreads) {
-            const int f = i % kFeatures, c = i / kFeatures;
-            if (f0 + f >= p.n) continue;
-            const int at = GATED ? f / 8 * 16 + f % 8 : f;
-            float z = 0.f, up = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                z += sums[w][at][c];
-                if (GATED) up += sums[w][at + 8][c];
-            }
-            if (p.bias) {
-                const __nv_bfloat16 *b = p.bias + (size_t)g * p.wide + f0 + f;
-                z += __bfloat162float(*b);
-                if (GATED) up += __bfloat162float(b[p.n]);
-            }
-            float y = GATED ? act_value(z, EP_ACT_SILU) * up : act_value(z, p.act);
-            const size_t o = ((size_t)g * p.rows + c0 + c) * p.n + f0 + f;
-            if (p.residual) y += __bfloat162float(p.residual[o]);
-            p.out[o] = __float2bfloat16_rn(y);
+        for (int j = 0; j < NT; ++j) {
+            uint4 b = make_uint4(0, 0, 0, 0);
+            if (j * 8 + r < cols) b = *reinterpret_cast<const uint4 *>(x + (j * 8) * x_stride + w * 16);
+            mma_16x8x16(acc[j], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+            mma_16x8x16(acc[j], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
         }
     }
 }
 
-template <int MT, int NT>
-cudaError_t launch_n(const W4Params &p, bool fp4, cudaStream_t st) {
-    const bool gated = p.act == EP_ACT_SWIGLU;
-    const int features = MT * (gated ? 8 : 16);
-    const dim3 grid((unsigned)((p.n + features - 1) / features), (unsigned)p.groups);
-    const auto kernel = gated ? (fp4 ? w4_rows_kernel<MT, NT, true, true> : w4_rows_kernel<MT, NT, false, true>)
-                              : (fp4 ? w4_rows_kernel<MT, NT, true, false> : w4_rows_kernel<MT, NT, false, false>);
-    return launch_after(kernel, grid, kThreads, st, p);
+template <int NT, bool FP4, bool GATED>
+__global__ void __launch_bounds__(kThreads) w4_rows_kernel(const RowsParams q) {
+    constexpr int kFeatures = GATED ? 8 : 16;   // of the output
+    constexpr int kCols = NT * 8;
+    const W4Params &p = q.w;
+    extern __shared__ __align__(128) uint8_t stages[];
+    __shared__ uint64_t full[kStages];
+    __shared__ int abort;
+    auto &sums = *reinterpret_cast<float(*)[kWarps][kRows][kCols + 1]>(stages);   // once the stages have been read
+    const int g = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
+        abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_launch_dependents();
+    const int f0 = blockIdx.x * kFeatures;
+    if (warp == 0 && !p.counts) {
+        // the codes on their way to L2 while the kernel before ends (no read: what that may still write to
+        // them is written to L2 as well); two rows, which are neighbours, to every fourth lane
+        const int i = lane / 4 * 2, f = f0 + (GATED ? i % 8 : i);
+        if (lane % 4 == 0 && f < p.n)
+            prefetch_l2(p.codes + ((size_t)g * p.wide + f + (GATED ? i / 8 * p.n : 0)) * (p.k / 2), p.k);
+    }
+    pdl_wait();
+    const int count = p.counts ? max(0, min(p.counts[g], p.rows)) : p.rows;
+    if (count == 0) return;
+    const int cols = min(count, kCols);   // (rows fit: the launch takes NT for them)
+    const int chunks = (p.k + q.chunk - 1) / q.chunk;
+    const uint32_t code_stride = q.chunk / 2 + kCodePad, x_stride = q.chunk * 2 + kXPad;
+    // row i of the CTA's 16 (past the last feature: the last, which nobody looks at)
+    const auto weight_row = [&](int i) {
+        return GATED ? min(f0 + i % 8, p.n - 1) + i / 8 * p.n : min(f0 + i, p.n - 1);
+    };
+    const uint8_t *codes = p.codes + (size_t)g * p.wide * (p.k / 2);
+    const uint8_t *x = reinterpret_cast<const uint8_t *>(p.x + (size_t)g * p.rows * p.k);
+
+    // A chunk's copies: a lane for each row of codes and of x.
+    const auto load = [&](int c) {
+        const int s = c % q.stages, k0 = c * q.chunk, n = min(q.chunk, p.k - k0);
+        uint8_t *stage = stages + s * q.stage_bytes;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], kRows * n / 2 + cols * n * 2);
+        __syncwarp();
+        if (lane < kRows)
+            bulk_g2s(stage + lane * code_stride, codes + (size_t)weight_row(lane) * (p.k / 2) + k0 / 2, n / 2, &full[s]);
+        else if (lane - kRows < cols)
+            bulk_g2s(stage + kRows * code_stride + (lane - kRows) * x_stride, x + ((size_t)(lane - kRows) * p.k + k0) * 2,
+                     n * 2, &full[s]);
+    };
+    if (warp == 0)
+        for (int c = 0; c < min(chunks, q.stages); ++c) load(c);
+
+    const int r = lane / 4, t = lane % 4;
+    const int row[2] = {weight_row(r), weight_row(r + 8)};
+    const __nv_bfloat16 *scales = p.scales + (size_t)g * (p.k >> p.group_shift) * p.wide;
+    const int subs = q.chunk / (kSub * kWarps);   // of a chunk, for each warp
+    const auto load_scales = [&](int e, __nv_bfloat16 (&raw)[2]) {   // of 32 elements from e on
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            raw[i] = e < p.k ? scales[(size_t)(e >> p.group_shift) * p.wide + row[i]] : __ushort_as_bfloat16(0);
+    };
+    float acc[NT][4] = {};
+    bool ok = true;
+    int c = 0;
+    for (; c < chunks; ++c) {
+        const int s = c % q.stages, k0 = c * q.chunk;
+        __nv_bfloat16 next[2];   // on their way while the copies are waited for, and a step ahead from then on
+        load_scales(k0 + warp * kSub + t * 32, next);
+        if (!mbar_try_wait_ns(&full[s], (c / q.stages) & 1, q.sleep_ns)) {
+            const uint64_t since = global_ns();
+            while (!mbar_try_wait_ns(&full[s], (c / q.stages) & 1, q.sleep_ns)) {
+                if (*(volatile int *)&abort || global_ns() - since > q.wait_limit_ns) {
+                    abort = 1;
+                    atomicCAS(q.status ? q.status : &rows_status, 0, EP_ERR_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+            }
+        }
+        if (__syncthreads_or(!ok)) break;   // (one has given up: all leave together)
+        const uint8_t *stage = stages + s * q.stage_bytes;
+        for (int u = 0; u < subs; ++u) {
+            const int at = (u * kWarps + warp) * kSub + t * 32;   // this lane's first element in the chunk
+            if (k0 + at - t * 32 >= p.k) break;                   // the same for the whole warp
+            const __nv_bfloat16 raw[2] = {next[0], next[1]};
+            if (u + 1 < subs) load_scales(k0 + at + kWarps * kSub, next);
+            uint4 code[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            const bool in = k0 + at < p.k;
+            if (in) {
+                code[0] = *reinterpret_cast<const uint4 *>(stage + r * code_stride + at / 2);
+                code[1] = *reinterpret_cast<const uint4 *>(stage + (r + 8) * code_stride + at / 2);
+            }
+            const uint8_t *xs = stage + kRows * code_stride + r * x_stride + at * 2;
+            const int use = in ? cols : 0;
+            if (__any_sync(kAll, is_large<FP4>(raw[0]) || is_large<FP4>(raw[1])))
+                multiply<NT, FP4, true>(acc, code, raw, xs, x_stride, use, r);
+            else
+                multiply<NT, FP4, false>(acc, code, raw, xs, x_stride, use, r);
+        }
+        if (c + q.stages < chunks) {
+            __syncthreads();   // the stage has been read
+            if (warp == 0) load(c + q.stages);
+        }
+    }
+    if (c < chunks) {   // a wait ran out: the copies in flight are to finish (bounded)
+        if (threadIdx.x == 0) {
+            const uint64_t since = global_ns();
+            for (int i = c; i < min(chunks, c + q.stages); ++i)
+                while (!mbar_try_wait(&full[i % q.stages], (i / q.stages) & 1) && global_ns() - since < 100000000ull)
+                    ;
+        }
+        __syncthreads();
+        return;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[warp][(i / 2) * 8 + r][j * 8 + t * 2 + i % 2] = acc[j][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kFeatures * cols; i += kThreads) {
+        const int f = i % kFeatures, col = i / kFeatures;
+        if (f0 + f >= p.n) continue;
+        float z = 0.f, up = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            z += sums[w][f][col];
+            if (GATED) up += sums[w][f + 8][col];
+        }
+        if (p.bias) {
+            const __nv_bfloat16 *b = p.bias + (size_t)g * p.wide + f0 + f;
+            z += __bfloat162float(*b);
+            if (GATED) up += __bfloat162float(b[p.n]);
+        }
+        float y = GATED ? act_value(z, EP_ACT_SILU) * up : act_value(z, p.act);
+        const size_t o = ((size_t)g * p.rows + col) * p.n + f0 + f;
+        if (p.residual) y += __bfloat162float(p.residual[o]);
+        p.out[o] = __float2bfloat16_rn(y);
+    }
+}
+
+template <int NT>
+cudaError_t launch_n(const RowsParams &q, bool fp4, cudaStream_t st) {
+    const bool gated = q.w.act == EP_ACT_SWIGLU;
+    const int features = gated ? 8 : 16;
+    const auto kernel = gated ? (fp4 ? w4_rows_kernel<NT, true, true> : w4_rows_kernel<NT, false, true>)
+                              : (fp4 ? w4_rows_kernel<NT, true, false> : w4_rows_kernel<NT, false, false>);
+    const size_t sums = (size_t)kWarps * kRows * (NT * 8 + 1) * sizeof(float), stages = (size_t)q.stages * q.stage_bytes;
+    const size_t smem = stages > sums ? stages : sums;
+    // (raised from 47 KB on: the default limit counts the kernel's own variables too)
+    cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void *>(kernel), smem + 1024);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((q.w.n + features - 1) / features), (unsigned)q.w.groups);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, q);
 }
 
 bool aligned16(const void *q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
@@ -160,10 +254,34 @@ struct Range {
 
 }  // namespace
 
-cudaError_t launch_w4_rows(const W4Params &p, bool fp4, cudaStream_t st) {
-    if (p.rows <= 8) return launch_n<1, 1>(p, fp4, st);
-    if (p.rows <= 16) return launch_n<1, 2>(p, fp4, st);
-    return launch_n<1, 4>(p, fp4, st);
+cudaError_t launch_w4_rows(const W4Params &w, bool fp4, int32_t *status, cudaStream_t st) {
+    RowsParams q = {};
+    q.w = w;
+    q.status = status;
+    q.wait_limit_ns = product_wait_limit();
+    q.sleep_ns = q.wait_limit_ns < kSleepNs ? (uint32_t)q.wait_limit_ns : kSleepNs;
+    const int rows = w.rows < kFewRows ? w.rows : kFewRows, unit = kSub * kWarps;
+    const auto bytes = [&](int chunk) {
+        return (kRows * (chunk / 2 + kCodePad) + rows * (chunk * 2 + kXPad) + 127) / 128 * 128;
+    };
+    // All of k with a copy for a row, where it fits (one row of x, 7168 x 7168, the weight in L2: 11.6 us in
+    // chunks of 2048 elements, 9.6 whole; from HBM 11.7 either way). Else three stages of 1024 elements, or
+    // of 2048 where x is small.
+    const int whole = (w.k + unit - 1) / unit * unit;
+    q.chunk = bytes(whole) <= kWholeBytes ? whole : rows <= 2 ? 2 * unit : unit;
+    q.stages = q.chunk == whole ? 1 : kStages;
+    q.stage_bytes = bytes(q.chunk);
+    return w.rows <= 8 ? launch_n<1>(q, fp4, st) : launch_n<2>(q, fp4, st);
+}
+
+int take_w4_rows_status(cudaStream_t st) {
+    int32_t status = 0;
+    take_status<<<1, 1, 0, st>>>();
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyFromSymbolAsync(&status, rows_status_taken, sizeof(status), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return EP_ERR_CUDA;
+    return status;
 }
 
 }  // namespace ep
@@ -203,6 +321,12 @@ extern "C" int ep_product_w4(const ep_w4_t *a, const void *x, const void *codes,
     p.act = a->act;
     Range range("ep:product_w4");
     const bool fp4 = a->kind == EP_W4_FP4;
-    if (a->rows > kFewRows) return launch_w4_tiles(p, fp4, a->status, static_cast<cudaStream_t>(stream));
-    return launch_w4_rows(p, fp4, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+    // A CTA for 16 weight rows reads all of x again, so beside n k / 2 bytes of codes rows / 4 times as many
+    // of x pass through L2. The tiles read x once for 128 or 256 weight rows, but begin later. Measured,
+    // rows / tiles: 4096 x 2048 with 1, 8, 12, 16 rows 4.1 / 8.0, 4.9 / 8.2, 5.5 / 8.2, 10.0 / 8.3 us; 7168 x 7168
+    // with 1, 2, 8 rows 10.8 / 14.7, 16.8 / 14.6, 25.9 / 14.7; 64 experts of 7168 x 2048 with 4 row slots 233 / 117.
+    const long long through = (long long)a->groups * p.wide * p.k / 2 * (4 + a->rows) / 4;
+    const bool few = a->rows <= kFewRows && (through <= kFewBytes || (a->rows == 1 && a->groups == 1));
+    if (!few) return launch_w4_tiles(p, fp4, a->status, static_cast<cudaStream_t>(stream));
+    return launch_w4_rows(p, fp4, a->status, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }

@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
             for (int i = 0; i < 2; ++i) {   // 64 elements, 32 columns of tensor memory, at a time
                 uint32_t r[32];
                 const W4Scale<FP4> s0(raw[2 * i]), s1(raw[2 * i + 1]);
-                if (__any_sync(kAll, s0.large() || s1.large())) {
+                if (__any_sync(kAll, is_large<FP4>(raw[2 * i]) || is_large<FP4>(raw[2 * i + 1]))) {
                     expand<FP4, true>(c[2 * i], s0, r);
                     expand<FP4, true>(c[2 * i + 1], s1, r + 16);
                 } else {
@@ -740,7 +740,8 @@ int take_w4_status(cudaStream_t st) {
         cudaMemcpyFromSymbolAsync(&status, w4_status_taken, sizeof(status), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)
         return EP_ERR_CUDA;
-    return status;
+    const int of_rows = take_w4_rows_status(st);
+    return status != EP_OK ? status : of_rows;
 }
 
 }  // namespace ep

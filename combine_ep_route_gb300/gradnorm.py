@@ -8,7 +8,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib as L
-from .product import _OUT, INT32_MAX, empty, stream_of, untracked
+from .product import _OUT, _want, INT32_MAX, empty, stream_of, untracked
 
 
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optional[Sequence[torch.Tensor]] = None,
@@ -33,25 +33,25 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optio
     n, dev, at = len(grads), grads[0].device, grads[0].get_device()
     if n > INT32_MAX:
         raise ValueError("grads: too many")
-    tracked = torch.is_grad_enabled()
-    kinds = []
-    for t in grads:
-        kind = _OUT.get(t.dtype)
-        if kind is None or at < 0 or t.get_device() != at or not t.is_contiguous():
-            raise ValueError(f"grads: want contiguous bfloat16 or float32 on one CUDA device, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
-        if tracked and t.requires_grad:
-            untracked(grads=t)
-        kinds.append(kind)
+    # (whole lists at a time, and a look at each tensor where something is wrong: there may be hundreds)
+    types = [t.dtype for t in grads]
+    kinds = [_OUT.get(d) for d in types]
+    if None in kinds or at < 0 or [t.get_device() for t in grads] != [at] * n or not all([t.is_contiguous() for t in grads]):
+        for t in grads:
+            if t.dtype not in _OUT or not t.is_cuda or t.get_device() != at or not t.is_contiguous():
+                raise ValueError(f"grads: want contiguous bfloat16 or float32 on one CUDA device, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
+    if any([t.requires_grad for t in grads]):
+        untracked(**{f"grads[{i}]": t for i, t in enumerate(grads)})
     # (arrays of 64 and 32 bits: a ctypes array of as many pointers takes several times as long to fill)
     ptrs, to = array("Q", [t.data_ptr() for t in grads]), None
     if out is not None:
-        for o, t in zip(outs, grads):
-            if o.dtype is not t.dtype or o.shape != t.shape or o.get_device() != at or not o.is_contiguous():
-                raise ValueError(f"out: want contiguous {t.dtype} {tuple(t.shape)} on {dev}, got {o.dtype} "
-                                 f"{tuple(o.shape)} on {o.device} (contiguous={o.is_contiguous()})")
-            if tracked and o.requires_grad:
-                untracked(out=o)
+        if ([o.dtype for o in outs] != types or [o.shape for o in outs] != [t.shape for t in grads]
+                or [o.get_device() for o in outs] != [at] * n or not all([o.is_contiguous() for o in outs])):
+            for o, t in zip(outs, grads):
+                _want(o, "out", t.shape, dev, t.dtype)
+        if any([o.requires_grad for o in outs]):
+            untracked(**{f"out[{i}]": o for i, o in enumerate(outs)})
         to = array("Q", [t.data_ptr() for t in outs])
     numel, kinds = array("q", [t.numel() for t in grads]), array("i", kinds)
     a = L.EpGradsC(n, ptrs.buffer_info()[0], None if to is None else to.buffer_info()[0], numel.buffer_info()[0],

@@ -10,13 +10,12 @@ codes and scales of a checkpoint, :func:`quantize_weight4` makes them from a wei
 from __future__ import annotations
 
 import ctypes as C
-from math import prod
 from typing import Optional, Tuple
 
 import torch
 
 from . import _lib as L
-from .product import BF16, I32, _NO_COUNTS, _act, _out, _ptr, _split, _want, stream_of, untracked
+from .product import BF16, I32, _NO_COUNTS, _act, _out, _ptr, _split, _want, _weight, stream_of, untracked
 
 U8 = torch.uint8
 KINDS = {"int4": L.EP_W4_INT4, "fp4": L.EP_W4_FP4}
@@ -36,7 +35,7 @@ def _kind(kind: str) -> int:
 def _group(k: int, scales: torch.Tensor, axis: int) -> int:
     """Elements that share a scale, from the scales' extent along k."""
     parts = scales.shape[axis]
-    if parts < 1 or k % parts or k // parts not in GROUPS:
+    if parts < 1 or k // parts not in GROUPS or k % parts:
         raise ValueError(f"scales: want one for each {', '.join(map(str, GROUPS))} of {k} elements, got {tuple(scales.shape)}")
     return k // parts
 
@@ -112,27 +111,25 @@ def _forward(x, codes, scales, counts, grouped, kind, bias, act, residual, out, 
     if x.dtype is not BF16 or not x.is_cuda or not x.is_contiguous():
         raise ValueError(f"x: want contiguous {BF16} on a CUDA device, got {x.dtype} {tuple(x.shape)} on {x.device} "
                          f"(contiguous={x.is_contiguous()})")
-    if (x.requires_grad or (bias is not None and bias.requires_grad)
-            or (residual is not None and residual.requires_grad) or scales.requires_grad):
+    if (x.requires_grad or scales.requires_grad or (bias is not None and bias.requires_grad)
+            or (residual is not None and residual.requires_grad)):
         untracked(x=x, scales=scales, bias=bias, residual=residual)
     groups, rows, k = _split(x, "x", grouped)
-    shape = codes.shape
-    if (len(shape) < 2 or (not grouped and len(shape) != 2) or prod(shape[:-2]) != groups or 2 * shape[-1] != k):
-        raise ValueError(f"codes: want {groups} weight(s) [rows, {k // 2}] for x {tuple(x.shape)}, got {tuple(shape)}")
-    wn = shape[-2]
+    wn, half = _weight(codes, groups, grouped)
     n = wn // 2 if code == L.EP_ACT_SWIGLU else wn
-    if n < 8 or n % 8 or n > 1 << 24 or (code == L.EP_ACT_SWIGLU and wn % 2) or k % 32 or not 32 <= k <= L.EP_W4_MAX_K:
-        raise ValueError(f"codes: want rows in multiples of 8 (of 16 with act 'swiglu') and k a multiple of 32 up to "
-                         f"{L.EP_W4_MAX_K}, got {wn} rows and k {k}")
-    if len(scales.shape) < 2:
+    if (2 * half != k or k % 32 or not 32 <= k <= L.EP_W4_MAX_K or n < 8 or n % 8 or n > 1 << 24
+            or (code == L.EP_ACT_SWIGLU and wn % 2)):
+        raise ValueError(f"codes: want [rows, k / 2] with rows in multiples of 8 (of 16 with act 'swiglu') and k a multiple "
+                         f"of 32 up to {L.EP_W4_MAX_K}, got {tuple(codes.shape)} for x {tuple(x.shape)}")
+    if scales.dim() < 2:
         raise ValueError(f"scales: want [..., k / group, rows], got {tuple(scales.shape)}")
-    group = _group(k, scales, -2)
-    _want(codes, "codes", shape, dev, U8)
-    _want(scales, "scales", shape[:-2] + (k // group, wn), dev)
-    lead = x.shape[:-1]
+    group, lead = _group(k, scales, -2), x.shape[:-1]
+    if codes.dtype is not U8 or codes.device != dev or not codes.is_contiguous():
+        _want(codes, "codes", codes.shape, dev, U8)
+    _want(scales, "scales", codes.shape[:-2] + (k // group, wn), dev)
     out = _out(out, lead + (n,), BF16, dev, stream)
     if bias is not None:
-        _want(bias, "bias", shape[:-1], dev)
+        _want(bias, "bias", codes.shape[:-1], dev)
     if residual is not None:
         _want(residual, "residual", lead + (n,), dev)
     if counts is not None and (counts.dtype != I32 or counts.numel() != groups or not counts.is_contiguous()
