@@ -33,6 +33,7 @@ constexpr int kMaxChunk = 4096;      // tokens of a CTA, at most: bounds the cha
 constexpr int kFinishThreads = 1024;
 constexpr int kSlice = 32;           // experts of a finishing CTA
 constexpr int kBackThreads = 256;
+constexpr float kLn2 = 0.69314718055994531f;
 
 struct BalanceParams {
     const void *logits;
@@ -62,6 +63,7 @@ __device__ __forceinline__ int length_of(const BalanceParams &p, int s) {
 }
 __device__ __forceinline__ Token token_of(const BalanceParams &p, int pool, long long r, int end) {
     if (r >= end) return {0, false};
+    if (!p.num_tokens) return {p.pools == p.seqs ? (long long)pool * p.T + r : r, true};
     if (p.pools == p.seqs) return {(long long)pool * p.T + r, r < length_of(p, pool)};
     const int s = (int)r / p.T;
     return {r, (int)r - s * p.T < length_of(p, s)};
@@ -74,7 +76,7 @@ __device__ __forceinline__ int expert_of(int lane, int j) {
 }
 
 // A logit as the losses use it: NaN and -inf to -inf (no part), +inf to the largest float.
-__device__ __forceinline__ float usable(float z) { return z >= -FLT_MAX ? fminf(z, FLT_MAX) : -INFINITY; }
+__device__ __forceinline__ float usable(float z) { return fminf(fmaxf(z, -INFINITY), FLT_MAX); }
 
 template <int G, int M, bool BF16, bool VEC>
 __device__ __forceinline__ void load_row(const BalanceParams &p, Token t, int lane, float (&z)[M]) {
@@ -115,15 +117,25 @@ __device__ __forceinline__ void load_row(const BalanceParams &p, Token t, int la
             }
         }
     }
-#pragma unroll
-    for (int j = 0; j < M; ++j) z[j] = usable(z[j]);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
 }
 
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
+    if constexpr (G == 32) {
+        float m;
+        asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(v));
+        return m;
+    } else {
 #pragma unroll
-    for (int d = G / 2; d > 0; d /= 2) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
-    return v;
+        for (int d = G / 2; d > 0; d /= 2) v = max_nan(v, __shfl_xor_sync(kAll, v, d));
+        return v;
+    }
 }
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
@@ -132,20 +144,63 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// exp(z - m) of every slot into e, their sum's inverse (0 for a row without a usable logit) and
-// its logarithm plus m (then 0). Exponentials by ex2.approx: right to (2 + |z - m| 1.5) 2^-23 of
-// themselves, so that what carries the sum is right to a few units of fp32.
+// A token's largest logit. Where a warp's tokens have NaN, infinite or huge ones, or none, the
+// logits become usable and the exponentials take another step (`odd`, the same for the warp):
+// looking at the maximum alone saves two instructions a logit.
+struct Top {
+    float m;
+    bool odd;
+};
+constexpr float kHuge = 1e38f;   // up to here a logit times log2(e) is finite
+
 template <int G, int M>
-__device__ __forceinline__ float softmax_of(const float (&z)[M], float m, float (&e)[M], float &lse) {
+__device__ __forceinline__ Top top_of(float (&z)[M]) {
+    float m = z[0];
+#pragma unroll
+    for (int j = 1; j < M; ++j) m = max_nan(m, z[j]);
+    m = group_max<G>(m);
+    const bool odd = __any_sync(kAll, !(fabsf(m) <= kHuge));
+    if (odd) {
+        m = -FLT_MAX;
+#pragma unroll
+        for (int j = 0; j < M; ++j) z[j] = usable(z[j]), m = fmaxf(m, z[j]);
+        m = group_max<G>(m);
+    }
+    return {m, odd};
+}
+
+__device__ __forceinline__ float log2_f(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// exp(z - m) of every slot into e, up to a factor next to 1 that all share; their sum's inverse (0
+// for a row without a usable logit) and the logits' logsumexp (then 0). Exponentials by ex2.approx:
+// right to (2 + |z - m| 1.5) 2^-23 of themselves, so that what carries the sum is right to a few
+// units of fp32; the logarithm to 2^-22.
+template <int G, int M>
+__device__ __forceinline__ float softmax_of(const float (&z)[M], Top top, float (&e)[M], float &lse) {
     float sum = 0.f;
+    const float shift = top.m * kLog2E;   // rounded: the factor
+    if (!top.odd) {
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+            e[j] = exp2_f(fmaf(z[j], kLog2E, -shift));
+            sum += e[j];
+        }
+        sum = group_sum<G>(sum);
+        lse = (shift + log2_f(sum)) * kLn2;
+        return rcp_f(sum);
+    }
 #pragma unroll
     for (int j = 0; j < M; ++j) {
-        e[j] = exp2_f((z[j] - m) * kLog2E);
+        e[j] = exp2_f((z[j] - top.m) * kLog2E);
         sum += e[j];
     }
     sum = group_sum<G>(sum);
-    lse = sum > 0.f ? m + logf(sum) : 0.f;
-    return sum > 0.f ? 1.f / sum : 0.f;
+    lse = sum > 0.f ? top.m + log2_f(sum) * kLn2 : 0.f;
+    return sum > 0.f ? rcp_f(sum) : 0.f;
 }
 
 // Sigmoids up to a common factor (exp(-mu), mu the largest logit where that is negative: the
@@ -163,7 +218,7 @@ __device__ __forceinline__ float sigmoid_of(const float (&z)[M], float m, float 
         sum += s[j];
     }
     sum = group_sum<G>(sum);
-    return sum > 0.f ? 1.f / sum : 0.f;
+    return sum > 0.f ? rcp_f(sum) : 0.f;
 }
 
 template <int M>
@@ -191,7 +246,7 @@ __global__ void __launch_bounds__(kSumThreads<M>) balance_sums_kernel(const Bala
     constexpr int kAtOnce = kSumThreads<M> / G, kPerWarp = 32 / G;
     for (long long r0 = lo + warp * kPerWarp; r0 < end; r0 += kAtOnce) {
         const Token t = token_of(p, pool, r0 + sub, end);
-        float z[M], e[M];
+        float z[M], e[M], lse;
         load_row<G, M, BF16, VEC>(p, t, lane, z);
         if (t.used) {
             for (int k = lane; k < p.K; k += G) {
@@ -199,15 +254,12 @@ __global__ void __launch_bounds__(kSumThreads<M>) balance_sums_kernel(const Bala
                 if (id >= 0 && id < p.E) atomicAdd(&count[id], 1);
             }
         }
-        float m = z[0], lse;
-#pragma unroll
-        for (int j = 1; j < M; ++j) m = fmaxf(m, z[j]);
-        m = fmaxf(group_max<G>(m), -FLT_MAX);
-        float inv = softmax_of<G, M>(z, m, e, lse);
+        const Top top = top_of<G, M>(z);
+        float inv = softmax_of<G, M>(z, top, e, lse);
         z2 += lse * lse;
         if (p.sigmoid) {
             float rest[M];
-            inv = sigmoid_of<G, M, false>(z, m, e, rest);
+            inv = sigmoid_of<G, M, false>(z, top.m, e, rest);
         }
 #pragma unroll
         for (int j = 0; j < M; ++j) acc[j] = fmaf(e[j], inv, acc[j]);
@@ -426,37 +478,33 @@ __global__ void __launch_bounds__(kBackThreads) balance_backward_kernel(const Ba
     for (long long r0 = lo + warp * kPerWarp; r0 < end; r0 += kAtOnce) {
         const long long r = r0 + sub;
         const Token t = token_of(p, pool, r, end);
-        float z[M], e[M], d[M];
+        float z[M], e[M], lse;
         load_row<G, M, BF16, VEC>(p, t, lane, z);
-        float m = z[0], lse;
-#pragma unroll
-        for (int j = 1; j < M; ++j) m = fmaxf(m, z[j]);
-        m = fmaxf(group_max<G>(m), -FLT_MAX);
-        const float inv = softmax_of<G, M>(z, m, e, lse);
+        const Top top = top_of<G, M>(z);
+        const float inv = softmax_of<G, M>(z, top, e, lse);
         const float zc = zunit != 0.f ? zunit * lse : 0.f;   // (no part where the z loss has none)
         float dot = 0.f;
         if (p.sigmoid) {
             float s[M], rest[M];
-            const float sinv = sigmoid_of<G, M, true>(z, m, s, rest);
+            const float sinv = sigmoid_of<G, M, true>(z, top.m, s, rest);
 #pragma unroll
             for (int j = 0; j < M; ++j) s[j] *= sinv, dot = fmaf(g[j], s[j], dot);
             dot = group_sum<G>(dot);
 #pragma unroll
-            for (int j = 0; j < M; ++j) d[j] = fmaf(s[j] * rest[j], g[j] - dot, e[j] * inv * zc);
+            for (int j = 0; j < M; ++j) z[j] = fmaf(s[j] * rest[j], g[j] - dot, e[j] * inv * zc);
         } else {
 #pragma unroll
             for (int j = 0; j < M; ++j) e[j] *= inv, dot = fmaf(g[j], e[j], dot);
-            dot = group_sum<G>(dot);
+            dot = group_sum<G>(dot) - zc;
 #pragma unroll
-            for (int j = 0; j < M; ++j) d[j] = e[j] * (g[j] - dot + zc);
+            for (int j = 0; j < M; ++j) z[j] = e[j] * (g[j] - dot);
         }
         if (r >= end || (p.accumulate && !t.used)) continue;   // a group's lanes agree
         if (!t.used) {
 #pragma unroll
-            for (int j = 0; j < M; ++j) d[j] = 0.f;
+            for (int j = 0; j < M; ++j) z[j] = 0.f;
         }
-        const long long row = p.pools == p.seqs ? (long long)pool * p.T + r : r;
-        store_row<G, M, BF16, VEC>(p, row, lane, d);
+        store_row<G, M, BF16, VEC>(p, p.pools == p.seqs ? (long long)pool * p.T + r : r, lane, z);
     }
 }
 
