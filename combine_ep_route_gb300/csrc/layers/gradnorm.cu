@@ -3,7 +3,7 @@
 //   norm = sqrt(sum over all tensors and elements of g^2)
 //   out  = g * max_norm / norm where norm is finite and above max_norm, else g
 //
-// Two kernels over the same list of pieces (runs of up to kPiece elements of a tensor): one
+// Two kernels over the same list of pieces (runs of up to 16384 elements of a tensor): one
 // adds squares up, a double per CTA in a fixed place; the other adds those up, again in a
 // fixed order, and scales. HBM bounds both: the second walks the pieces backwards, so that
 // what the first read last is still in L2, and is over at once where nothing is to be changed.
@@ -25,9 +25,14 @@ namespace ep {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kPiece = 16384;        // elements of a piece
-constexpr int kMaxCtas = 456;        // three per SM: of the sums' kernel
+constexpr int kThreads = 512;        // of the sums' kernel,
+constexpr int kMaxCtas = 456;        // whose CTAs are three per SM
+// And of the scaling one, which reads and writes: fewer threads on their way do better (1.4 G elements
+// with 2, 3, 4, 6 CTAs of 256 per SM: 1757, 1661, 1786, 1812 us in all; three of 512: 1775).
+constexpr int kScaleThreads = 256, kMaxScaleCtas = 456;
+// Elements of a piece: small ones where all tensors together would leave SMs idle otherwise.
+constexpr int kPiece = 16384, kSmallPiece = 2048;
+constexpr long long kSmallTotal = 4 << 20;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr double kDoubleMax = 1.7976931348623157e308;
 
@@ -40,7 +45,7 @@ struct List {
     long long numel[N];
     uint32_t first[N + 1];   // pieces before it
     uint32_t bf16[(N + 31) / 32];
-    int n;
+    int n, piece;
 };
 
 struct ClipParams {
@@ -68,8 +73,8 @@ __device__ __forceinline__ Piece piece_of(const List<N> &list, uint32_t i) {
         else hi = mid;
     }
     Piece x;
-    x.begin = (long long)(i - list.first[lo]) * kPiece;
-    x.count = (int)min((long long)kPiece, list.numel[lo] - x.begin);
+    x.begin = (long long)(i - list.first[lo]) * list.piece;
+    x.count = (int)min((long long)list.piece, list.numel[lo] - x.begin);
     x.bf16 = (list.bf16[lo / 32] >> (lo % 32)) & 1;
     const size_t at = (size_t)x.begin * (x.bf16 ? 2 : 4);
     x.in = static_cast<const uint8_t *>(list.in[lo]) + at;
@@ -234,18 +239,19 @@ __device__ __forceinline__ void scale_piece(const Piece &x, float factor) {
     const bool wide = (reinterpret_cast<uintptr_t>(x.in) - reinterpret_cast<uintptr_t>(x.out)) % 16 == 0;
     const int head = wide ? head_of(x.in, kSize, x.count) : x.count;
     const int vecs = (x.count - head) / kVec, tail = head + vecs * kVec;
+    // (plain loads and stores: streaming ones took 3 % longer)
     const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(x.in) + head * kSize);
     uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(x.out) + head * kSize);
-    for (int i0 = threadIdx.x; i0 < vecs; i0 += kThreads * kFlight) {
+    for (int i0 = threadIdx.x; i0 < vecs; i0 += kScaleThreads * kFlight) {
         uint4 u[kFlight];
 #pragma unroll
         for (int q = 0; q < kFlight; ++q) {
-            const int i = i0 + q * kThreads;
-            if (i < vecs) u[q] = __ldcs(p + i);
+            const int i = i0 + q * kScaleThreads;
+            if (i < vecs) u[q] = p[i];
         }
 #pragma unroll
         for (int q = 0; q < kFlight; ++q) {
-            const int i = i0 + q * kThreads;
+            const int i = i0 + q * kScaleThreads;
             if (i >= vecs) continue;
             float v[kVec];
             unpack<BF16>(u[q], v);
@@ -256,11 +262,11 @@ __device__ __forceinline__ void scale_piece(const Piece &x, float factor) {
             else
                 r = make_uint4(__float_as_uint(v[0] * factor), __float_as_uint(v[1] * factor),
                                __float_as_uint(v[2] * factor), __float_as_uint(v[3] * factor));
-            __stcs(o + i, r);
+            o[i] = r;
         }
     }
     const int rest = head + (x.count - tail);   // all of it where the two are not alike aligned
-    for (int j = threadIdx.x; j < rest; j += kThreads) {
+    for (int j = threadIdx.x; j < rest; j += kScaleThreads) {
         const int i = j < head ? j : tail + j - head;
         const float v = element<BF16>(x.in, i) * factor;
         if (BF16) static_cast<__nv_bfloat16 *>(x.out)[i] = __float2bfloat16_rn(v);
@@ -269,7 +275,7 @@ __device__ __forceinline__ void scale_piece(const Piece &x, float factor) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ List<N> list, const ClipParams p) {
+__global__ void __launch_bounds__(kScaleThreads) scale_kernel(const __grid_constant__ List<N> list, const ClipParams p) {
     pdl_launch_dependents();
     pdl_wait();
     float factor = factor_of(p, p.write_norm && blockIdx.x == 0);
@@ -295,22 +301,29 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const ClipParams p) {
 struct Part {
     int from, to;
     uint32_t pieces;
-    int ctas, base;
+    int ctas, base;   // of the sums' kernel, and those of the parts before
 };
 
 constexpr int kMost = 512;                     // tensors of a launch
 constexpr uint32_t kMostPieces = 1u << 31;     // pieces of a launch
 
-long long pieces_of(long long numel) { return (numel + kPiece - 1) / kPiece; }
+long long pieces_of(long long numel, int piece) { return (numel + piece - 1) / piece; }
+
+int piece_size(const ep_grads_t *a) {
+    long long total = 0;
+    for (int i = 0; i < a->n && total < kSmallTotal; ++i) total += a->numel[i];
+    return total < kSmallTotal ? kSmallPiece : kPiece;
+}
 
 // False where a tensor alone has too many pieces.
 bool cut(const ep_grads_t *a, std::vector<Part> &parts) {
+    const int piece = piece_size(a);
     int base = 0;
     for (int i = 0; i < a->n;) {
         Part x = {i, i, 0, 0, base};
         long long pieces = 0;
-        while (x.to < a->n && x.to - x.from < kMost && pieces + pieces_of(a->numel[x.to]) < (long long)kMostPieces)
-            pieces += pieces_of(a->numel[x.to++]);
+        while (x.to < a->n && x.to - x.from < kMost && pieces + pieces_of(a->numel[x.to], piece) < (long long)kMostPieces)
+            pieces += pieces_of(a->numel[x.to++], piece);
         if (x.to == x.from) return false;
         x.pieces = (uint32_t)pieces;
         x.ctas = (int)(pieces < kMaxCtas ? pieces : kMaxCtas);
@@ -324,6 +337,7 @@ bool cut(const ep_grads_t *a, std::vector<Part> &parts) {
 template <int N>
 void fill(const ep_grads_t *a, const Part &x, List<N> &list) {
     list.n = 0;
+    list.piece = piece_size(a);
     for (uint32_t &w : list.bf16) w = 0;
     uint32_t first = 0;
     for (int i = x.from; i < x.to; ++i) {
@@ -334,7 +348,7 @@ void fill(const ep_grads_t *a, const Part &x, List<N> &list) {
         list.numel[at] = a->numel[i];
         list.first[at] = first;
         if (a->dtypes[i] == EP_BF16) list.bf16[at / 32] |= 1u << (at % 32);
-        first += (uint32_t)pieces_of(a->numel[i]);
+        first += (uint32_t)pieces_of(a->numel[i], list.piece);
     }
     list.first[list.n] = first;
 }
@@ -344,7 +358,8 @@ cudaError_t launch_n(const ep_grads_t *a, const Part &x, const ClipParams &p, bo
     List<N> list;
     fill(a, x, list);
     if (!scale) return launch_after(squares_kernel<N>, dim3((unsigned)x.ctas), kThreads, st, list, p);
-    return launch_after(scale_kernel<N>, dim3((unsigned)x.ctas), kThreads, st, list, p);
+    const uint32_t ctas = x.pieces < (uint32_t)kMaxScaleCtas ? x.pieces : (uint32_t)kMaxScaleCtas;
+    return launch_after(scale_kernel<N>, dim3(ctas), kScaleThreads, st, list, p);
 }
 
 cudaError_t launch_part(const ep_grads_t *a, const Part &x, const ClipParams &p, bool scale, cudaStream_t st) {

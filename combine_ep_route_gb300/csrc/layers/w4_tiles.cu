@@ -44,6 +44,7 @@ constexpr int kMaxXSlots = 8;
 constexpr int kCodeBytes = kLanes * kStep / 2;
 constexpr int kCodeSlot = kCodeBytes + kLanes * (kStep / 32) * 2;   // with the scales, at most
 constexpr int kMaxCodeSlots = 8;
+static_assert(kMaxCodeSlots % kTurns == 0, "a slot's uses are one pair of groups'");
 constexpr int kMaxSplit = 4;
 constexpr uint32_t kSleepNs = 1000000;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -689,10 +690,13 @@ int launch_w4_tiles(const W4Params &w, bool fp4, int32_t *status, cudaStream_t s
     p.acc_stride = (p.col_max + 31) / 32 * 32;
     p.slots = (kTmemCols - 2 * p.acc_stride) / kACols;   // 2 for 128 columns, 3 for 64
     // The rings: x waits in its own until the MMAs take it, codes only until they are expanded, up to
-    // `slots` steps earlier, so x gets what three slots of codes leave.
-    p.x_slots = (int)(kRingSpace - 3 * kCodeSlot) / p.x_bytes;
+    // `slots` steps earlier, so x gets what four slots of codes leave. Slots of codes are a multiple of
+    // kTurns: then a slot's uses are all of one pair of groups, and the parity that it waits for is not
+    // that of an older phase. (With three, copies that arrive out of order let a pair see the phase before
+    // the one of the other pair's step, read what was not there yet and upset the barriers' counts.)
+    p.x_slots = (int)(kRingSpace - 4 * kCodeSlot) / p.x_bytes;
     if (p.x_slots > kMaxXSlots) p.x_slots = kMaxXSlots;
-    p.code_slots = (int)(kRingSpace - (size_t)p.x_slots * p.x_bytes) / kCodeSlot;
+    p.code_slots = (int)(kRingSpace - (size_t)p.x_slots * p.x_bytes) / kCodeSlot / kTurns * kTurns;
     if (p.code_slots > kMaxCodeSlots) p.code_slots = kMaxCodeSlots;
     const uint64_t K = w.k, N = w.n, W = w.wide, G = w.groups, parts = K >> w.group_shift;
     bool good;

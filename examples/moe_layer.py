@@ -8,12 +8,17 @@ sum as its residual. Tokens are held as [W, T, h], one block per simulated rank.
 
 The backward pass goes the same way back: the output's gradient is dispatched to the
 rows the experts wrote, and the gradients of the rows the experts read are combined
-with unit weights.
+with unit weights. The balance and z losses of the router join its gradient there, and
+clip() bounds the norm of all gradients together.
 
-    python examples/moe_layer.py            # times a forward and a backward pass
+To serve the layer, quantize() makes 4-bit weights of the experts and the shared expert, and
+forward_w4() runs on them; the router keeps its bf16 weight.
+
+    python examples/moe_layer.py            # times a training step's parts and a served forward pass
 """
 import os
 import sys
+from typing import Optional
 
 import torch
 
@@ -45,6 +50,8 @@ class MoeLayer:
         self.x = x
         self.logits = ep.linear(x, self.router, out_dtype=torch.float32, status=st)
         self.ids, weights = ep.route_topk(self.logits, c.top_k)
+        # the balance and z losses, and how often each expert was chosen
+        self.losses, self.load = ep.balance_loss(self.logits, self.ids)
         d = self.ctx.dispatch(x, self.ids, weights)
         self.rows, self.counts = d.b_a1, d.expert_num_tokens
         self.z = torch.empty(*d.b_a1.shape[:-1], self.w13.shape[-2], dtype=BF16, device=self.device)
@@ -58,7 +65,23 @@ class MoeLayer:
         self.shared = ep.linear(x, self.s1, bias=self.b1, act="gelu", preact=self.zs, status=st)
         return ep.linear(self.shared, self.s2, residual=routed, status=st)
 
-    def backward(self, dout: torch.Tensor) -> dict:
+    def quantize(self, group: int = 32, kind: str = "int4") -> None:
+        """4-bit weights for forward_w4 (once, when the layer is loaded)."""
+        self.kind = kind
+        self.q = {name: ep.quantize_weight4(getattr(self, name), group, kind) for name in ("w13", "w2", "s1", "s2")}
+
+    def forward_w4(self, x: torch.Tensor) -> torch.Tensor:
+        c, kw = self.cfg, dict(kind=self.kind, status=self.status)
+        logits = ep.linear(x, self.router, out_dtype=torch.float32, status=self.status)
+        ids, weights = ep.route_topk(logits, c.top_k)
+        d = self.ctx.dispatch(x, ids, weights)
+        hidden = ep.experts_product_w4(d.b_a1, *self.q["w13"], d.expert_num_tokens, act="swiglu", **kw)
+        routed = self.ctx.combine(ep.experts_product_w4(hidden, *self.q["w2"], d.expert_num_tokens, **kw))
+        shared = ep.linear_w4(x, *self.q["s1"], bias=self.b1, act="gelu", **kw)
+        return ep.linear_w4(shared, *self.q["s2"], residual=routed, **kw)
+
+    def backward(self, dout: torch.Tensor, dlosses: Optional[torch.Tensor] = None) -> dict:
+        """The gradients for the output's gradient and that of the losses (float32 [2])."""
         c, st, grads = self.cfg, self.status, {}
         # the shared expert
         grads["s2"] = ep.linear_wgrad(dout, self.shared, status=st)
@@ -80,11 +103,18 @@ class MoeLayer:
         # the router: each weight's gradient is its expert's output along dout
         picked = self.y.view(-1, c.hidden)[self.pair_row.clamp(min=0)]
         dw = (picked.float() * dout[..., None, :].float()).sum(-1) * kept
-        dlogits = ep.route_topk_backward(dw, self.logits, self.ids).to(BF16)
+        dlogits = ep.route_topk_backward(dw, self.logits, self.ids)
+        if dlosses is not None:
+            ep.balance_loss_backward(dlosses, self.logits, self.load, c.top_k, out=dlogits, accumulate=True)
+        dlogits = dlogits.to(BF16)
         grads["router"] = ep.linear_wgrad(dlogits, self.x, status=st)
         dx += ep.linear_dgrad(dlogits, self.router, out_dtype=torch.float32, status=st)
         grads["x"] = dx
         return grads
+
+    def clip(self, grads: dict, max_norm: float) -> torch.Tensor:
+        """Scales the weights' gradients down to a norm of max_norm together; returns their norm before."""
+        return ep.clip_grad_norm([g for name, g in grads.items() if name != "x"], max_norm)
 
     def check(self) -> None:
         """Raises what the kernels reported (synchronises)."""
@@ -111,7 +141,12 @@ def main() -> None:
         print(f"{name}: {a.elapsed_time(b) / 20 * 1e3:.0f} us for {cfg.W * cfg.max_tokens} tokens")
 
     timed("forward", lambda: layer.forward(x))
-    timed("backward", lambda: layer.backward(dout))
+    dlosses = torch.tensor([1e-2, 1e-3], device=layer.device)
+    timed("backward with the router's losses", lambda: layer.backward(dout, dlosses))
+    grads = layer.backward(dout, dlosses)
+    timed("clipping", lambda: layer.clip(grads, 1.0))
+    layer.quantize()
+    timed("forward with 4-bit weights", lambda: layer.forward_w4(x))
     layer.check()
 
 

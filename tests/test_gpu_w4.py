@@ -126,6 +126,21 @@ def test_experts_with_leading_dimensions():
         assert torch.equal(z.view(y.shape)[e, :c], y[e, :c])
 
 
+@pytest.mark.parametrize("rows,counts", ((7, (7, 0, 3)), (40, (40, 1, 17)), (140, (140, 0, 129))))
+@pytest.mark.parametrize("act", ("none", "swiglu"))
+def test_what_lies_around_stays(rows, counts, act):
+    """Results are written to the rows in use alone, whatever lies before and behind the output."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    n = 72
+    x, (codes, scales) = rand(g, 3, rows, 160), weight(g, 3, 2 * n if act == "swiglu" else n, 160, 32)
+    flat = torch.full((3 * rows * n + 4096,), 5.0, dtype=BF16, device="cuda")
+    out = flat[2048:2048 + 3 * rows * n].view(3, rows, n)
+    ep.experts_product_w4(x, codes, scales, torch.tensor(counts, dtype=I32, device="cuda"), act=act, out=out)
+    assert (flat[:2048] == 5.0).all() and (flat[-2048:] == 5.0).all()
+    for e, c in enumerate(counts):
+        assert (out[e, c:] == 5.0).all() and not (out[e, :c] == 5.0).all(dim=-1).any()
+
+
 def test_residual_in_place_and_nothing_to_do():
     g = torch.Generator(device="cuda").manual_seed(1)
     for rows in (5, 100):
@@ -147,6 +162,31 @@ def test_rows_do_not_touch_one_another_and_give_the_same_bits(rows):
     z = ep.linear_w4(x2, codes[0], scales[0])
     keep = torch.arange(rows, device="cuda") != rows // 2
     assert torch.equal(y[keep], z[keep]) and z[rows // 2].isnan().all()
+
+
+@pytest.mark.parametrize("rows,n,groups", ((64, 256, 1), (130, 512, 40), (128, 512, 8), (1, 4096, 1)))
+def test_long_reductions_agree_each_time(rows, n, groups):
+    """Copies of a long reduction arrive in no fixed order (rows of codes 16 KB apart, other traffic between
+    the calls): the result is the same to the bit each time, and right."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    k = 32768 if groups == 1 else 8192
+    x, (codes, scales) = rand(g, groups, rows, k), weight(g, groups, n, k, 64)
+    cnt = torch.full((groups,), rows, dtype=I32, device="cuda")
+    other = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+
+    def call():
+        if groups == 1:
+            return ep.linear_w4(x[0], codes[0], scales[0])[None]
+        return ep.experts_product_w4(x, codes, scales, cnt)
+
+    first = call()
+    want, off, _, _ = R.forward(x[-1], ep.dequantize_weight4(codes[-1], scales[-1]), None, "none", None, BF16)
+    assert ((first[-1].double() - want).abs() <= off).all()
+    for i in range(30):
+        if i % 2:
+            other.fill_(i)
+        assert torch.equal(call(), first), i
+    ep.check_products()
 
 
 def test_scales_of_any_size():
