@@ -15,6 +15,10 @@
 // tokens; a CTA's sums go to the workspace and a second, small kernel adds the CTAs' up in
 // order, so that nothing depends on the order of atomics (counts, whole numbers, are added
 // atomically in shared memory).
+//
+// Instructions and their latency bound it: 64000 tokens of 256 fp32 logits (66 MB) take 48 us in both
+// directions (about 20 for the sums, 5 to join them, 22 for the gradient; 20 would be the bytes'), 8
+// sequences of 1024 19 us, 128 tokens of 64 experts 7 for the losses alone.
 #include "launch.cuh"
 
 #include <cfloat>

@@ -7,6 +7,8 @@
 // adds squares up, a double per CTA in a fixed place; the other adds those up, again in a
 // fixed order, and scales. HBM bounds both: the second walks the pieces backwards, so that
 // what the first read last is still in L2, and is over at once where nothing is to be changed.
+// 1.44 G elements in 160 tensors (3.26 GB, read twice and written once) take 1509 us, 6.5 TB/s; 200 M in
+// 50 tensors 216, 5.9 TB/s; 0.3 M in 12 tensors 8.7 us on the device and 38 with the call's lists.
 //
 // A square of a fp32 (or bf16) number overflows from 1.8e19 and loses digits below 1e-19, so
 // a vector of 16 bytes whose largest magnitude lies outside 2^-50 .. 2^50 is scaled by 2^100

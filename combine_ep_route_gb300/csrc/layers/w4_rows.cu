@@ -8,7 +8,8 @@
 // eight rows of x by mma.sync (m16n8k16, the weight's rows along m): an MMA's contraction may take the
 // elements in any order that both operands share, so a lane's elements are those that lie
 // together in memory. (tcgen05.mma wants 128 weight rows at once; few rows of x make no use of its
-// rate.) The warps' sums are joined in shared memory, in order.
+// rate.) The warps' sums are joined in shared memory, in order. One row, 7168 x 7168: 9.5 us with the
+// weight in L2, 11.7 from HBM (2.2 TB/s; 3.8 us at the copy's rate), of which about 7 are start and end.
 #include "w4.cuh"
 
 #include <nvtx3/nvToolsExt.h>

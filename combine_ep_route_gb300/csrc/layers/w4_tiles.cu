@@ -2,16 +2,28 @@
 //
 // D[lane][col] = sum_k w[lane][k] x[col][k]: 128 rows of the weight on the accumulator's lanes,
 // up to 128 rows of x on its columns. The weight is the operand that sits in tensor memory:
-// TMA brings blocks of 128 elements of 4-bit codes and their scales, eight warps make bf16 of
+// TMA brings steps of 256 elements of 4-bit codes and their scales, sixteen warps make bf16 of
 // them (a lane its own row, 64 bytes of codes at a time) and store them to tensor memory, from
 // where the MMAs read them; x goes by TMA to shared memory with the 128-byte swizzle. So the
 // expanded weight never passes through shared memory, whose bandwidth the MMAs' other operand
-// needs. A gated product's gate and up rows are interleaved by eights by the tensor maps alone.
+// needs (an MMA of 128 columns takes 65-74 cycles that way, 107 with both operands in shared
+// memory). A gated product's gate and up rows are interleaved by eights by the tensor maps alone.
 //
-// One persistent CTA per SM: a TMA warp for the codes and scales, one for x, an MMA warp, two
-// groups of four warps that expand every other block each, and four epilogue warps that drain
-// one accumulator while the next fills. Dense products with few tiles let up to four CTAs of a
-// cluster share a tile's reduction and join their sums through distributed shared memory.
+// One persistent CTA per SM: a TMA warp for the codes and scales, one for x, an MMA warp, two pairs
+// of groups of four warps that expand a step each, half a step to a group, and eight epilogue warps
+// that drain one accumulator while the next fills. Where tiles are many, pairs of CTAs share an MMA
+// of 256 weight rows (cta_group::2): each holds half of x, which is what most of the bytes from L2 are.
+// Dense products with few tiles let up to four CTAs of a cluster share a tile's reduction and join
+// their sums through distributed shared memory.
+//
+// What bounds it: with few rows of x an SM's instructions (a step of the expanding warps takes 2400
+// cycles, 10 to an instruction with 28 warps on the SM; two are under way) and, not far below, the
+// codes' stream (64 experts of 7168 x 2048 with four rows each: 113 us, 4.4 TB/s; the copies alone 97);
+// with about 120 rows the same and the gated epilogue (64 experts of 2 x 1024 x 2048: 70 us, 920 TFLOP/s);
+// with more the tensor cores (64 experts of 2 x 2048 x 4096 under Zipf: 315 us, 1.2 PFLOP/s). What each
+// step gave (us, the three): the first kernel 228 / 111 / 476; one thread waits and issues 181 / 95 / 396;
+// steps of 256 158 / 93 / 347; warps that skip to their own steps 130 / 87 / 323; pairs of CTAs, x in a
+// ring of its own 134 / 76 / 304; x by one copy a step 120 / 76 / 289.
 #include "w4.cuh"
 
 #include <nvtx3/nvToolsExt.h>
@@ -443,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tiles_kernel(const __grid_cons
             }
         }
     } else if (warp == 1) {
-        // ---- MMA: one thread waits and issues. (By the whole warp, with a vote after each wait, a
-        // block took over 1100 cycles, whatever its columns: 64 experts with four rows 228 -> 181 us.)
+        // ---- MMA: one thread waits and issues (by the whole warp, with a vote after each wait, a step of 128
+        // took over 1100 cycles, whatever its columns)
         if ((CG == 1 || rank == 0) && elect_one()) {
             int acc = 0;
             uint32_t acc_phase = 0;

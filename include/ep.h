@@ -560,7 +560,7 @@ int ep_act_grad(const ep_product_t *args, const void *dy, const void *preact, vo
 
 /*
  * ep_product_status -- wait for the work queued on `stream`, then return what the products
- * without a status word of their own have reported on the current device since the last call
+ * (ep_product_w4 too) without a status word of their own have reported on the current device since the last call
  * (EP_OK or EP_ERR_TIMEOUT), and clear it. EP_ERR_CUDA if the stream cannot be waited for.
  */
 int ep_product_status(void *stream);
