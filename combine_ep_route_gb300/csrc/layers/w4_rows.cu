@@ -326,8 +326,8 @@ extern "C" int ep_product_w4(const ep_w4_t *a, const void *x, const void *codes,
     // of x pass through L2. The tiles read x once for 128 or 256 weight rows, but begin later. Measured,
     // rows / tiles: 4096 x 2048 with 1, 8, 12, 16 rows 4.1 / 8.0, 4.9 / 8.2, 5.5 / 8.2, 10.0 / 8.3 us; 7168 x 7168
     // with 1, 2, 8 rows 10.8 / 14.7, 16.8 / 14.6, 25.9 / 14.7; 64 experts of 7168 x 2048 with 4 row slots 233 / 117.
-    const long long through = (long long)a->groups * p.wide * p.k / 2 * (4 + a->rows) / 4;
-    const bool few = a->rows <= kFewRows && (through <= kFewBytes || (a->rows == 1 && a->groups == 1));
+    const long long codes_bytes = (long long)a->groups * p.wide * p.k / 2;   // below 2^50
+    const bool few = a->rows <= kFewRows && (codes_bytes * (4 + a->rows) / 4 <= kFewBytes || (a->rows == 1 && a->groups == 1));
     if (!few) return launch_w4_tiles(p, fp4, a->status, static_cast<cudaStream_t>(stream));
     return launch_w4_rows(p, fp4, a->status, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
