@@ -3,8 +3,8 @@
 // The weight's codes bound it, and for a single small weight the latency of getting them. A CTA
 // takes 16 rows of the weight (of a gated one 8 gate rows and the 8 up rows that belong to them)
 // and all of k, which bulk copies bring to shared memory in one piece where three CTAs' pieces fit
-// an SM, else in chunks, three on their way at a time; a chunk's elements are split over the warps. Each lane takes 32 elements, 16 bytes, of two
-// weight rows at a time, makes bf16 pairs of them and multiplies them with one or two tiles of
+// an SM, else in chunks, three on their way at a time; a chunk's elements are split over the warps.
+// Each lane takes 32 elements, 16 bytes, of two weight rows at a time, makes bf16 pairs of them and multiplies them with one or two tiles of
 // eight rows of x by mma.sync (m16n8k16, the weight's rows along m): an MMA's contraction may take the
 // elements in any order that both operands share, so a lane's elements are those that lie
 // together in memory. (tcgen05.mma wants 128 weight rows at once; few rows of x make no use of its
@@ -16,18 +16,20 @@
 
 #include "act.cuh"
 #include "tcgen05.cuh"
+#include "tensor_map.cuh"
 
 namespace ep {
 
 namespace {
 
 constexpr int kFewRows = 16;   // row slots of a group that this kernel takes
-constexpr long long kFewBytes = 20 << 20;
+constexpr long long kFewBytes = 28 << 20;   // through L2, for up to eight rows whole
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;      // of the weight
 constexpr int kSub = 128;      // elements of k that a warp takes at once: 32 per lane of a row's four
 constexpr int kStages = 3;
+constexpr int kSmBytes = 228 * 1024;     // shared memory of an SM
 constexpr int kWholeBytes = 74 * 1024;   // of a piece, so that three CTAs fit an SM
 constexpr int kCodePad = 64;   // bytes between rows of codes, of x: their banks differ
 constexpr int kXPad = 32;
@@ -253,14 +255,8 @@ struct Range {
     ~Range() { nvtxRangePop(); }
 };
 
-}  // namespace
-
-cudaError_t launch_w4_rows(const W4Params &w, bool fp4, int32_t *status, cudaStream_t st) {
-    RowsParams q = {};
-    q.w = w;
-    q.status = status;
-    q.wait_limit_ns = product_wait_limit();
-    q.sleep_ns = q.wait_limit_ns < kSleepNs ? (uint32_t)q.wait_limit_ns : kSleepNs;
+// How a call is cut: the elements of a piece, and the pieces a CTA holds.
+void cut_rows(const W4Params &w, RowsParams &q) {
     const int rows = w.rows < kFewRows ? w.rows : kFewRows, unit = kSub * kWarps;
     const auto bytes = [&](int chunk) {
         return (kRows * (chunk / 2 + kCodePad) + rows * (chunk * 2 + kXPad) + 127) / 128 * 128;
@@ -272,6 +268,42 @@ cudaError_t launch_w4_rows(const W4Params &w, bool fp4, int32_t *status, cudaStr
     q.chunk = bytes(whole) <= kWholeBytes ? whole : rows <= 2 ? 2 * unit : unit;
     q.stages = q.chunk == whole ? 1 : kStages;
     q.stage_bytes = bytes(q.chunk);
+}
+
+// Whether this kernel takes a call (of 16 row slots at most), or the tiles. A CTA for 16 weight rows reads
+// all of x again, so beside n k / 2 bytes of codes rows / 4 times as many of x pass through L2; the tiles
+// read x once for 128 or 256 weight rows, but begin later. Measured, in us, here / the tiles:
+// 1. up to 8 rows held whole: 4096 x 2048 with 1, 8 rows 4.8 / 8.1, 5.1 / 8.2; at 24 MiB through L2 8 x 2048 x
+//    1024 7.7 / 8.1; at 35, 28672 x 1024 with 6 rows 11.2 / 11.5, and past that even or slower (64 experts of
+//    7168 x 2048 with 4 row slots 192 / 115). One row alone, held whole, wins at any n: 7168 x 7168 11.5 / 14.6;
+// 2. while all CTAs find room at once, three an SM or what their shared memory allows, more rows win too:
+//    7168 x 2048 with 14 rows 5.8 / 9.1. A second round costs as much again: 4096 x 2048 with 14, 15 rows (in
+//    chunks, one CTA an SM) 5.4 / 8.3, 10.0 / 8.3; 1024 CTAs of 32 x 512 x 512 with 12 rows 10.5 / 7.3;
+// 3. each chunk of k costs 2.2 us, and the tiles share a long k among CTAs where no counts are given: 1024 x
+//    7168 with 8 rows 13.3 / 9.8 without, 13.3 / 19.3 with counts; one row, 2048 x 16384, 20.6 / 15.1.
+// Over 252 calls of 1 to 16 rows (both kernels timed on each) the one taken is within 8 % of the better but for
+// eight, which lose 1.6 us at most.
+bool few_rows_here(const W4Params &w, int sms) {
+    RowsParams q = {};
+    cut_rows(w, q);
+    const bool whole = q.stages == 1;
+    if (whole && w.groups == 1 && w.rows == 1) return true;
+    const long long codes = (long long)w.groups * w.wide * w.k / 2;   // below 2^50
+    if (whole && w.rows <= 8 && codes * (4 + w.rows) / 4 <= kFewBytes) return true;
+    const int held = kSmBytes / (q.stages * q.stage_bytes + 1024);
+    const bool at_once = (long long)w.groups * ((w.wide + kRows - 1) / kRows) <= (long long)sms * (held < 3 ? held : 3);
+    return at_once && (whole || w.counts || w.k <= 2 * q.chunk);
+}
+
+}  // namespace
+
+cudaError_t launch_w4_rows(const W4Params &w, bool fp4, int32_t *status, cudaStream_t st) {
+    RowsParams q = {};
+    q.w = w;
+    q.status = status;
+    q.wait_limit_ns = product_wait_limit();
+    q.sleep_ns = q.wait_limit_ns < kSleepNs ? (uint32_t)q.wait_limit_ns : kSleepNs;
+    cut_rows(w, q);
     return w.rows <= 8 ? launch_n<1>(q, fp4, st) : launch_n<2>(q, fp4, st);
 }
 
@@ -322,12 +354,12 @@ extern "C" int ep_product_w4(const ep_w4_t *a, const void *x, const void *codes,
     p.act = a->act;
     Range range("ep:product_w4");
     const bool fp4 = a->kind == EP_W4_FP4;
-    // A CTA for 16 weight rows reads all of x again, so beside n k / 2 bytes of codes rows / 4 times as many
-    // of x pass through L2. The tiles read x once for 128 or 256 weight rows, but begin later. Measured,
-    // rows / tiles: 4096 x 2048 with 1, 8, 12, 16 rows 4.1 / 8.0, 4.9 / 8.2, 5.5 / 8.2, 10.0 / 8.3 us; 7168 x 7168
-    // with 1, 2, 8 rows 10.8 / 14.7, 16.8 / 14.6, 25.9 / 14.7; 64 experts of 7168 x 2048 with 4 row slots 233 / 117.
-    const long long codes_bytes = (long long)a->groups * p.wide * p.k / 2;   // below 2^50
-    const bool few = a->rows <= kFewRows && (codes_bytes * (4 + a->rows) / 4 <= kFewBytes || (a->rows == 1 && a->groups == 1));
+    bool few = a->rows <= kFewRows;
+    if (few) {
+        int sms;
+        if (sm_count(&sms) != cudaSuccess) return EP_ERR_CUDA;
+        few = few_rows_here(p, sms);
+    }
     if (!few) return launch_w4_tiles(p, fp4, a->status, static_cast<cudaStream_t>(stream));
     return launch_w4_rows(p, fp4, a->status, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }
