@@ -148,14 +148,15 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// A token's largest logit. Where a warp's tokens have NaN, infinite or huge ones, or none, the
+// A token's largest logit. Where a warp's tokens have NaN, infinite or large ones, or none, the
 // logits become usable and the exponentials take another step (`odd`, the same for the warp):
 // looking at the maximum alone saves two instructions a logit.
 struct Top {
     float m;
     bool odd;
 };
-constexpr float kHuge = 1e38f;   // up to here a logit times log2(e) is finite
+// Up to here the short way's rounding of the maximum times log2(e) (half a unit of 2^17) is 2^-8 at most.
+constexpr float kLarge = 65536.f;
 
 template <int G, int M>
 __device__ __forceinline__ Top top_of(float (&z)[M]) {
@@ -163,7 +164,7 @@ __device__ __forceinline__ Top top_of(float (&z)[M]) {
 #pragma unroll
     for (int j = 1; j < M; ++j) m = max_nan(m, z[j]);
     m = group_max<G>(m);
-    const bool odd = __any_sync(kAll, !(fabsf(m) <= kHuge));
+    const bool odd = __any_sync(kAll, !(fabsf(m) <= kLarge));
     if (odd) {
         m = -FLT_MAX;
 #pragma unroll
@@ -179,10 +180,12 @@ __device__ __forceinline__ float log2_f(float x) {
     return y;
 }
 
-// exp(z - m) of every slot into e, up to a factor next to 1 that all share; their sum's inverse (0
-// for a row without a usable logit) and the logits' logsumexp (then 0). Exponentials by ex2.approx:
-// right to (2 + |z - m| 1.5) 2^-23 of themselves, so that what carries the sum is right to a few
-// units of fp32; the logarithm to 2^-22.
+// exp(z - m) of every slot into e, up to a factor that all share; their sum's inverse (0 for a row
+// without a usable logit) and the logits' logsumexp (then 0). The factor is 2 to the power of what
+// rounding takes from m log2(e): the logsumexp takes it back, and within 2^-8 of 0 that power overflows
+// nothing. Past kLarge it would (|m| = 1e10: a power of 440), so there z - m is formed first.
+// Exponentials by ex2.approx: right to (2 + |z - m| 1.5) 2^-23 of themselves, so that what carries the
+// sum is right to a few units of fp32; the logarithm to 2^-22.
 template <int G, int M>
 __device__ __forceinline__ float softmax_of(const float (&z)[M], Top top, float (&e)[M], float &lse) {
     float sum = 0.f;
