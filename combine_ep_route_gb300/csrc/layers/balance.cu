@@ -489,7 +489,9 @@ __global__ void __launch_bounds__(kBackThreads) balance_backward_kernel(const Ba
         load_row<G, M, BF16, VEC>(p, t, lane, z);
         const Top top = top_of<G, M>(z);
         const float inv = softmax_of<G, M>(z, top, e, lse);
-        const float zc = zunit != 0.f ? zunit * lse : 0.f;   // (no part where the z loss has none)
+        // The z loss's part. The logsumexp of large logits times its unit may pass the largest float where its
+        // share for an expert does not (and then meet a probability of 0): there the share comes first.
+        const float zc = zunit != 0.f && !top.odd ? zunit * lse : 0.f;   // (no part where the z loss has none)
         float dot = 0.f;
         if (p.sigmoid) {
             float s[M], rest[M];
@@ -498,13 +500,17 @@ __global__ void __launch_bounds__(kBackThreads) balance_backward_kernel(const Ba
             for (int j = 0; j < M; ++j) s[j] *= sinv, dot = fmaf(g[j], s[j], dot);
             dot = group_sum<G>(dot);
 #pragma unroll
-            for (int j = 0; j < M; ++j) z[j] = fmaf(s[j] * rest[j], g[j] - dot, e[j] * inv * zc);
+            for (int j = 0; j < M; ++j) e[j] *= inv, z[j] = fmaf(s[j] * rest[j], g[j] - dot, e[j] * zc);
         } else {
 #pragma unroll
             for (int j = 0; j < M; ++j) e[j] *= inv, dot = fmaf(g[j], e[j], dot);
             dot = group_sum<G>(dot) - zc;
 #pragma unroll
             for (int j = 0; j < M; ++j) z[j] = e[j] * (g[j] - dot);
+        }
+        if (top.odd && zunit != 0.f) {
+#pragma unroll
+            for (int j = 0; j < M; ++j) z[j] = fmaf(e[j] * lse, zunit, z[j]);
         }
         if (r >= end || (p.accumulate && !t.used)) continue;   // a group's lanes agree
         if (!t.used) {
