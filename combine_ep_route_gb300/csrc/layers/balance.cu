@@ -37,6 +37,7 @@ constexpr int kMaxChunk = 4096;      // tokens of a CTA, at most: bounds the cha
 constexpr int kFinishThreads = 1024;
 constexpr int kSlice = 32;           // experts of a finishing CTA
 constexpr int kBackThreads = 256;
+constexpr unsigned kMaxBackCtas = 4 * kMaxChunks;   // eight per SM
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct BalanceParams {
@@ -299,25 +300,43 @@ __global__ void __launch_bounds__(kSumThreads<M>) balance_sums_kernel(const Bala
     }
 }
 
-// Tokens in use: of a pool, of all, and the number of pools that have any. Called by one warp.
+// Tokens in use of all sequences, and how many sequences have any. A warp, or the warps of a block with a
+// part each, walk the sequences. (When every CTA did, and CTAs were as many as the sequences, the time
+// grew with their square: 16384 of one token took 10 ms.)
 struct Lengths {
-    long long pool, all;
-    int pools;
+    long long all;
+    int some;
 };
-__device__ __forceinline__ Lengths lengths(const BalanceParams &p, int pool) {
-    const int lane = threadIdx.x % 32;
-    long long all = 0;
-    int some = 0;
-    for (int s = lane; s < p.seqs; s += 32) {
-        const int n = length_of(p, s);
-        all += n, some += n > 0;
-    }
+__device__ __forceinline__ Lengths warp_lengths(Lengths n) {
     for (int d = 16; d > 0; d /= 2) {
-        all += __shfl_xor_sync(kAll, all, d);
-        some += __shfl_xor_sync(kAll, some, d);
+        n.all += __shfl_xor_sync(kAll, n.all, d);
+        n.some += __shfl_xor_sync(kAll, n.some, d);
     }
-    if (p.pools == p.seqs) return {length_of(p, pool), all, some};
-    return {all, all, all > 0};
+    return n;
+}
+// Of the sequences first, first + step, ... of each thread, for a whole warp.
+__device__ __forceinline__ void put_lengths(const BalanceParams &p, int first, int step, Lengths &out) {
+    Lengths n = {0, 0};
+    if (p.num_tokens) {
+#pragma unroll 4
+        for (long long s = first; s < p.seqs; s += step) {
+            const int own = length_of(p, (int)s);
+            n.all += own, n.some += own > 0;
+        }
+        n = warp_lengths(n);
+    } else if (first < 32) {
+        n = {(long long)p.seqs * p.T, p.seqs};
+    }
+    if (threadIdx.x % 32 == 0) out = n;
+}
+template <int WARPS>
+__device__ __forceinline__ Lengths total_lengths(const Lengths (&parts)[WARPS]) {
+    const int lane = threadIdx.x % 32;
+    return warp_lengths(lane < WARPS ? parts[lane] : Lengths{0, 0});
+}
+// Pools that have tokens.
+__device__ __forceinline__ int pools_in_use(const BalanceParams &p, Lengths n) {
+    return p.pools == p.seqs ? n.some : n.all > 0;
 }
 
 // A fp32 sum with what rounding took from it. (In 64 bits, of which this GPU does two additions a
@@ -344,13 +363,16 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
     __shared__ float ps[kRows][kSlice + 1];
     __shared__ int32_t cs[kRows][kSlice + 1];
     __shared__ float parts[2][kFinishThreads / 32];
-    __shared__ Lengths n;
+    __shared__ Lengths lens[kFinishThreads / 32];
     __shared__ bool last;
     pdl_launch_dependents();
     pdl_wait();
     const int slices = (p.E + kSlice - 1) / kSlice;
     const int pool = blockIdx.x / slices, slice = blockIdx.x % slices;
     const int col = threadIdx.x % kSlice, row = threadIdx.x / kSlice, e = slice * kSlice + col;
+    const bool own = p.pools == p.seqs;   // a pool is a sequence
+    const bool few = !p.num_tokens || p.seqs <= kFinishThreads;   // one warp walks them while the others add up
+    const int length = own ? length_of(p, pool) : 0;
     Sum sum;
     int32_t count = 0;
     if (e < p.E) {
@@ -362,11 +384,13 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
         }
     }
     ps[row][col] = sum.value(), cs[row][col] = count;
-    if (row == kRows - 1) {
-        const Lengths own = lengths(p, pool);
-        if (col == 0) n = own;
+    if (few) {
+        if (row == kRows - 1) put_lengths(p, col, 32, lens[0]);
+    } else if (!own) {
+        put_lengths(p, threadIdx.x, kFinishThreads, lens[row]);
     }
     __syncthreads();
+    const long long tokens = own ? length : few ? lens[0].all : total_lengths(lens).all;
     // a warp per expert adds the rows up by a tree
     const float psum = warp_sum(ps[col][row]);
     const int32_t csum = __reduce_add_sync(kAll, cs[col][row]);
@@ -375,7 +399,7 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
         float v = 0.f;
         if (e2 < p.E) {
             p.counts[(size_t)pool * p.E + e2] = csum;
-            if (n.pool > 0) v = (float)csum * p.E / ((float)p.K * n.pool) * (psum / n.pool);
+            if (tokens > 0) v = (float)csum * p.E / ((float)p.K * tokens) * (psum / tokens);
         }
         parts[0][row] = v;
     }
@@ -391,6 +415,7 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
     __syncthreads();
     if (!last) return;
     __threadfence();
+    if (own && !few) put_lengths(p, threadIdx.x, kFinishThreads, lens[row]);
     Sum b, z;
     for (int i = threadIdx.x; i < (int)gridDim.x; i += kFinishThreads) b.add(__ldcg(p.slots + i));
     const long long all = (long long)p.pools * p.chunks;
@@ -400,8 +425,10 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
     __syncthreads();
     if (threadIdx.x < 32) {
         const float bs = warp_sum(parts[0][threadIdx.x]), zt = warp_sum(parts[1][threadIdx.x]);
+        const Lengths n = few ? lens[0] : total_lengths(lens);
+        const int pools = pools_in_use(p, n);
         if (threadIdx.x == 0) {
-            p.losses[0] = n.pools > 0 ? bs / n.pools : 0.f;
+            p.losses[0] = pools > 0 ? bs / pools : 0.f;
             p.losses[1] = n.all > 0 ? zt / n.all : 0.f;
         }
     }
@@ -458,28 +485,20 @@ __device__ __forceinline__ void store_row(const BalanceParams &p, long long row,
 }
 
 template <int G, int M, bool BF16, bool VEC>
-__global__ void __launch_bounds__(kBackThreads) balance_backward_kernel(const BalanceParams p) {
-    __shared__ Lengths lens;
-    pdl_launch_dependents();
-    pdl_wait();
+__device__ __forceinline__ void backward_chunk(const BalanceParams &p, Lengths n, int pool, int chunk) {
+    constexpr int kAtOnce = kBackThreads / G, kPerWarp = 32 / G;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % G, sub = threadIdx.x % 32 / G;
-    const int pool = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
-    if (warp == 0) {
-        const Lengths own = lengths(p, pool);
-        if (threadIdx.x == 0) lens = own;
-    }
-    __syncthreads();
-    const Lengths n = lens;
-    float g[M];
+    const int pools = pools_in_use(p, n);
     const float d0 = p.dlosses[0], d1 = p.dlosses[1];
-    const float unit = n.pool > 0 ? d0 * p.E / ((float)p.K * n.pool) / ((float)n.pool * n.pools) : 0.f;
     const float zunit = n.all > 0 ? 2.f * d1 / n.all : 0.f;
+    const long long tokens = p.pools == p.seqs ? length_of(p, pool) : n.all;
+    const float unit = tokens > 0 ? d0 * p.E / ((float)p.K * tokens) / ((float)tokens * pools) : 0.f;
+    float g[M];
 #pragma unroll
     for (int j = 0; j < M; ++j) {
         const int e = expert_of<G, VEC>(lane, j);
         g[j] = e < p.E ? unit * p.counts_in[(size_t)pool * p.E + e] : 0.f;
     }
-    constexpr int kAtOnce = kBackThreads / G, kPerWarp = 32 / G;
     const long long lo = (long long)chunk * p.chunk;
     const int end = (int)min((long long)p.rows, lo + p.chunk);
     for (long long r0 = lo + warp * kPerWarp; r0 < end; r0 += kAtOnce) {
@@ -508,7 +527,7 @@ __global__ void __launch_bounds__(kBackThreads) balance_backward_kernel(const Ba
 #pragma unroll
             for (int j = 0; j < M; ++j) z[j] = e[j] * (g[j] - dot);
         }
-        if (top.odd && zunit != 0.f) {
+        if (top.odd && zunit != 0.f && lse != 0.f) {
 #pragma unroll
             for (int j = 0; j < M; ++j) z[j] = fmaf(e[j] * lse, zunit, z[j]);
         }
@@ -519,6 +538,24 @@ __global__ void __launch_bounds__(kBackThreads) balance_backward_kernel(const Ba
         }
         store_row<G, M, BF16, VEC>(p, p.pools == p.seqs ? (long long)pool * p.T + r : r, lane, z);
     }
+}
+
+// A CTA for each chunk; with MANY a CTA takes several, so that the sequences are not walked as often as there
+// are chunks. (A loop around all cases takes registers from the tokens: 64000 of 256, 26.2 us without, 28.6 with.
+// Five CTAs an SM hold the registers of narrow groups at 48, from 59 to 62 otherwise.)
+template <int G, int M, bool BF16, bool VEC, bool MANY>
+__global__ void __launch_bounds__(kBackThreads, VEC && G < 32 && !MANY ? 5 : 0) balance_backward_kernel(const BalanceParams p) {
+    __shared__ Lengths lens[kBackThreads / 32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const bool few = !p.num_tokens || p.seqs <= kBackThreads;
+    if (!few) put_lengths(p, threadIdx.x, kBackThreads, lens[threadIdx.x / 32]);
+    else if (threadIdx.x < 32) put_lengths(p, threadIdx.x, 32, lens[0]);
+    __syncthreads();
+    const Lengths n = few ? lens[0] : total_lengths(lens);
+    if (!MANY) return backward_chunk<G, M, BF16, VEC>(p, n, blockIdx.x / p.chunks, blockIdx.x % p.chunks);
+    for (unsigned at = blockIdx.x; at < (unsigned)p.pools * (unsigned)p.chunks; at += gridDim.x)
+        backward_chunk<G, M, BF16, VEC>(p, n, at / p.chunks, at % p.chunks);
 }
 
 constexpr long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -575,15 +612,24 @@ size_t place(BalanceParams &p, uint8_t *base) {
 
 bool aligned_to(const void *q, size_t n) { return q && reinterpret_cast<uintptr_t>(q) % n == 0; }
 
+template <int G, int M, bool MANY>
+cudaError_t launch_backward(const BalanceParams &p, bool bf16, bool vec, unsigned ctas, cudaStream_t st) {
+    const auto kernel = bf16 ? (vec ? balance_backward_kernel<G, M, true, true, MANY> : balance_backward_kernel<G, M, true, false, MANY>)
+                             : (vec ? balance_backward_kernel<G, M, false, true, MANY> : balance_backward_kernel<G, M, false, false, MANY>);
+    return launch_after(kernel, dim3(ctas), kBackThreads, st, p);
+}
+
 template <bool BACKWARD, int G, int M>
 cudaError_t launch_n(const BalanceParams &p, bool bf16, bool vec, cudaStream_t st) {
-    const auto kernel =
-        BACKWARD ? (bf16 ? (vec ? balance_backward_kernel<G, M, true, true> : balance_backward_kernel<G, M, true, false>)
-                         : (vec ? balance_backward_kernel<G, M, false, true> : balance_backward_kernel<G, M, false, false>))
-                 : (bf16 ? (vec ? balance_sums_kernel<G, M, true, true> : balance_sums_kernel<G, M, true, false>)
-                         : (vec ? balance_sums_kernel<G, M, false, true> : balance_sums_kernel<G, M, false, false>));
-    return launch_after(kernel, dim3((unsigned)(p.pools * (long long)p.chunks)), BACKWARD ? kBackThreads : kSumThreads<M>,
-                        st, p);
+    const unsigned ctas = (unsigned)(p.pools * (long long)p.chunks);
+    if (BACKWARD) {
+        // (without lengths there is nothing to walk)
+        if (p.num_tokens && ctas > kMaxBackCtas) return launch_backward<G, M, true>(p, bf16, vec, kMaxBackCtas, st);
+        return launch_backward<G, M, false>(p, bf16, vec, ctas, st);
+    }
+    const auto kernel = bf16 ? (vec ? balance_sums_kernel<G, M, true, true> : balance_sums_kernel<G, M, true, false>)
+                             : (vec ? balance_sums_kernel<G, M, false, true> : balance_sums_kernel<G, M, false, false>);
+    return launch_after(kernel, dim3(ctas), kSumThreads<M>, st, p);
 }
 
 // Lanes of a token: few experts leave lanes of a warp to other tokens.
@@ -659,7 +705,7 @@ extern "C" int ep_balance_loss_backward(const ep_balance_t *a, const float *dlos
         return EP_ERR_INVALID_ARG;
     // a CTA reads the counts and lengths once, so it takes several steps where tokens are many
     const int at_once = kBackThreads / (p.E <= 64 ? 8 : p.E <= 128 ? 16 : 32);
-    cut(p, at_once, 4 * kMaxChunks);
+    cut(p, at_once, kMaxBackCtas);
     if (p.pools * (long long)p.chunks > INT32_MAX) return EP_ERR_INVALID_ARG;
     p.dlosses = dlosses;
     p.logits = logits;
