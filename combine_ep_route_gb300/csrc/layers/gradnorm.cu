@@ -231,9 +231,17 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
     }
 }
 
-// The norm from the sums, the same in every CTA, and the factor that it asks for (-1: none).
-__device__ __forceinline__ float factor_of(const ClipParams &p, bool write) {
-    __shared__ float factor;
+// What elements are multiplied with: factor, then more, which is 1 unless the two's product is below the
+// smallest normal float (a norm of 1e39, or a bound of 1e-30 and elements of 1e10), where one factor would have lost
+// its last digits or all.
+struct Scale {
+    float factor, more;
+    __device__ __forceinline__ float of(float v) const { return v * factor * more; }
+};
+
+// The norm from the sums, the same in every CTA, and the scale that it asks for (factor -1: none).
+__device__ __forceinline__ Scale scale_of(const ClipParams &p, bool write) {
+    __shared__ Scale scale;
     if (threadIdx.x < 32) {
         double sum = 0;
         for (int i = threadIdx.x; i < p.partials; i += 32) sum += p.partial[i];
@@ -243,15 +251,17 @@ __device__ __forceinline__ float factor_of(const ClipParams &p, bool write) {
             if (write) *p.norm = (float)norm;
             // (a NaN compares false)
             const bool clip = norm > (double)p.max_norm && norm <= kDoubleMax;
-            factor = clip ? (float)((double)p.max_norm / norm) : -1.f;
+            const double by = clip ? (double)p.max_norm / norm : -1.;
+            const bool tiny = clip && by < 0x1p-126;
+            scale = {(float)(tiny ? by * 0x1p126 : by), tiny ? 0x1p-126f : 1.f};
         }
     }
     __syncthreads();
-    return factor;
+    return scale;
 }
 
 template <bool BF16>
-__device__ __forceinline__ void scale_piece(const Piece &x, float factor) {
+__device__ __forceinline__ void scale_piece(const Piece &x, Scale scale) {
     constexpr int kVec = BF16 ? 8 : 4, kFlight = 4, kSize = BF16 ? 2 : 4;
     const bool wide = (reinterpret_cast<uintptr_t>(x.in) - reinterpret_cast<uintptr_t>(x.out)) % 16 == 0;
     const int head = wide ? head_of(x.in, kSize, x.count) : x.count;
@@ -274,18 +284,18 @@ __device__ __forceinline__ void scale_piece(const Piece &x, float factor) {
             unpack<BF16>(u[q], v);
             uint4 r;
             if constexpr (BF16)
-                r = make_uint4(pack_bf16x2_rn(v[0] * factor, v[1] * factor), pack_bf16x2_rn(v[2] * factor, v[3] * factor),
-                               pack_bf16x2_rn(v[4] * factor, v[5] * factor), pack_bf16x2_rn(v[6] * factor, v[7] * factor));
+                r = make_uint4(pack_bf16x2_rn(scale.of(v[0]), scale.of(v[1])), pack_bf16x2_rn(scale.of(v[2]), scale.of(v[3])),
+                               pack_bf16x2_rn(scale.of(v[4]), scale.of(v[5])), pack_bf16x2_rn(scale.of(v[6]), scale.of(v[7])));
             else
-                r = make_uint4(__float_as_uint(v[0] * factor), __float_as_uint(v[1] * factor),
-                               __float_as_uint(v[2] * factor), __float_as_uint(v[3] * factor));
+                r = make_uint4(__float_as_uint(scale.of(v[0])), __float_as_uint(scale.of(v[1])),
+                               __float_as_uint(scale.of(v[2])), __float_as_uint(scale.of(v[3])));
             o[i] = r;
         }
     }
     const int rest = head + (x.count - tail);   // all of it where the two are not alike aligned
     for (int j = threadIdx.x; j < rest; j += kScaleThreads) {
         const int i = j < head ? j : tail + j - head;
-        const float v = element<BF16>(x.in, i) * factor;
+        const float v = scale.of(element<BF16>(x.in, i));
         if (BF16) static_cast<__nv_bfloat16 *>(x.out)[i] = __float2bfloat16_rn(v);
         else static_cast<float *>(x.out)[i] = v;
     }
@@ -295,23 +305,23 @@ template <int N>
 __global__ void __launch_bounds__(kScaleThreads) scale_kernel(const __grid_constant__ List<N> list, const ClipParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    float factor = factor_of(p, p.write_norm && blockIdx.x == 0);
-    if (factor < 0.f) {   // nothing to scale
+    Scale scale = scale_of(p, p.write_norm && blockIdx.x == 0);
+    if (scale.factor < 0.f) {   // nothing to scale
         if (!p.copy) return;
-        factor = 1.f;
+        scale.factor = 1.f;
     }
     const uint32_t pieces = list.first[list.n];
     for (uint32_t i = blockIdx.x; i < pieces; i += gridDim.x) {
         const Piece x = piece_of(list, pieces - 1 - i);
-        if (x.bf16) scale_piece<true>(x, factor);
-        else scale_piece<false>(x, factor);
+        if (x.bf16) scale_piece<true>(x, scale);
+        else scale_piece<false>(x, scale);
     }
 }
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const ClipParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    factor_of(p, true);
+    scale_of(p, true);
 }
 
 // The tensors [from, to) of the list, as one launch takes them.
