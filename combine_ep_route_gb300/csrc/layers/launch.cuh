@@ -28,8 +28,7 @@ cudaError_t launch_row_sums(const void *src, const int32_t *counts, int groups, 
 // The bound of a product's device-side waits, ns (ep_product_wait_limit).
 uint64_t product_wait_limit();
 
-// What the products with 4-bit weights without a status word have reported on the current
-// device, cleared; waits for the stream.
-int take_w4_status(cudaStream_t st);
+// The word of the current device in which products without one of their own report (ep_product_status).
+cudaError_t product_status_word(int32_t **word);
 
 }  // namespace ep

@@ -1145,6 +1145,20 @@ struct Range {
 
 }  // namespace
 
+cudaError_t product_status_word(int32_t **word) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int32_t *> cached[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices && (*word = cached[dev].load(std::memory_order_relaxed))) return cudaSuccess;
+    void *at = nullptr;
+    e = cudaGetSymbolAddress(&at, device_status);
+    *word = static_cast<int32_t *>(at);
+    if (e == cudaSuccess && dev < kMaxDevices) cached[dev].store(*word, std::memory_order_relaxed);
+    return e;
+}
+
 uint64_t product_wait_limit() { return wait_limit_ns.load(std::memory_order_relaxed); }
 
 }  // namespace ep
@@ -1223,8 +1237,7 @@ extern "C" int ep_product_status(void *stream) {
         cudaMemcpyFromSymbolAsync(&status, status_taken, sizeof(status), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
         cudaStreamSynchronize(st) != cudaSuccess)
         return EP_ERR_CUDA;
-    const int of_w4 = take_w4_status(st);
-    return status != EP_OK ? status : of_w4;
+    return status;
 }
 
 extern "C" int ep_product_wait_limit(int64_t ns) {

@@ -99,7 +99,6 @@ __device__ __forceinline__ void w4_values(uint32_t word, const W4Scale<FP4> &s, 
 }
 
 cudaError_t launch_w4_rows(const W4Params &p, bool fp4, int32_t *status, cudaStream_t st);
-int take_w4_rows_status(cudaStream_t st);
 int launch_w4_tiles(const W4Params &p, bool fp4, int32_t *status, cudaStream_t st);
 
 }  // namespace ep

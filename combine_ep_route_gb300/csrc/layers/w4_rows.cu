@@ -45,10 +45,6 @@ struct RowsParams {
     uint32_t sleep_ns;
 };
 
-__device__ int32_t rows_status, rows_status_taken;
-
-__global__ void take_status() { rows_status_taken = atomicExch(&rows_status, 0); }
-
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                             uint32_t b1) {
     asm volatile(
@@ -156,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) w4_rows_kernel(const RowsParams q) {
             while (!mbar_try_wait_ns(&full[s], (c / q.stages) & 1, q.sleep_ns)) {
                 if (*(volatile int *)&abort || global_ns() - since > q.wait_limit_ns) {
                     abort = 1;
-                    atomicCAS(q.status ? q.status : &rows_status, 0, EP_ERR_TIMEOUT);
+                    atomicCAS(q.status, 0, EP_ERR_TIMEOUT);
                     ok = false;
                     break;
                 }
@@ -307,16 +303,6 @@ cudaError_t launch_w4_rows(const W4Params &w, bool fp4, int32_t *status, cudaStr
     return w.rows <= 8 ? launch_n<1>(q, fp4, st) : launch_n<2>(q, fp4, st);
 }
 
-int take_w4_rows_status(cudaStream_t st) {
-    int32_t status = 0;
-    take_status<<<1, 1, 0, st>>>();
-    if (cudaGetLastError() != cudaSuccess ||
-        cudaMemcpyFromSymbolAsync(&status, rows_status_taken, sizeof(status), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-        cudaStreamSynchronize(st) != cudaSuccess)
-        return EP_ERR_CUDA;
-    return status;
-}
-
 }  // namespace ep
 
 using namespace ep;
@@ -360,6 +346,8 @@ extern "C" int ep_product_w4(const ep_w4_t *a, const void *x, const void *codes,
         if (sm_count(&sms) != cudaSuccess) return EP_ERR_CUDA;
         few = few_rows_here(p, sms);
     }
-    if (!few) return launch_w4_tiles(p, fp4, a->status, static_cast<cudaStream_t>(stream));
-    return launch_w4_rows(p, fp4, a->status, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
+    int32_t *status = a->status;
+    if (!status && product_status_word(&status) != cudaSuccess) return EP_ERR_CUDA;
+    if (!few) return launch_w4_tiles(p, fp4, status, static_cast<cudaStream_t>(stream));
+    return launch_w4_rows(p, fp4, status, static_cast<cudaStream_t>(stream)) == cudaSuccess ? EP_OK : EP_ERR_CUDA;
 }

@@ -61,10 +61,6 @@ constexpr int kMaxSplit = 4;
 constexpr uint32_t kSleepNs = 1000000;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
-__device__ int32_t w4_status, w4_status_taken;
-
-__global__ void take_status() { w4_status_taken = atomicExch(&w4_status, 0); }
-
 struct TileParams {
     CUtensorMap codes, scales;
     CUtensorMap x[kBoxes];    // boxes of a step (k a multiple of 64), or of one line of 64 elements
@@ -182,7 +178,7 @@ __device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity, Shared
         if (*abort) return false;
         if (global_ns() - t0 > p.wait_limit_ns) {
             *abort = 1;
-            atomicCAS(p.status ? p.status : &w4_status, 0, EP_ERR_TIMEOUT);
+            atomicCAS(p.status, 0, EP_ERR_TIMEOUT);
             return false;
         }
     }
@@ -747,17 +743,6 @@ int launch_w4_tiles(const W4Params &w, bool fp4, int32_t *status, cudaStream_t s
         e = gated ? (fp4 ? launch<true, true, 1>(p, clusters, st) : launch<false, true, 1>(p, clusters, st))
                   : (fp4 ? launch<true, false, 1>(p, clusters, st) : launch<false, false, 1>(p, clusters, st));
     return e == cudaSuccess ? EP_OK : EP_ERR_CUDA;
-}
-
-int take_w4_status(cudaStream_t st) {
-    int32_t status = 0;
-    take_status<<<1, 1, 0, st>>>();
-    if (cudaGetLastError() != cudaSuccess ||
-        cudaMemcpyFromSymbolAsync(&status, w4_status_taken, sizeof(status), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-        cudaStreamSynchronize(st) != cudaSuccess)
-        return EP_ERR_CUDA;
-    const int of_rows = take_w4_rows_status(st);
-    return status != EP_OK ? status : of_rows;
 }
 
 }  // namespace ep
