@@ -35,6 +35,7 @@ constexpr int kCodePad = 64;   // bytes between rows of codes, of x: their banks
 constexpr int kXPad = 32;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr uint32_t kSleepNs = 1000000;
+constexpr uint64_t kPollNs = 100000;     // limits below are kept by polling: a suspended try may last 20 us
 
 struct RowsParams {
     W4Params w;
@@ -42,7 +43,7 @@ struct RowsParams {
     int stages, stage_bytes;
     int32_t *status;
     uint64_t wait_limit_ns;
-    uint32_t sleep_ns;
+    uint32_t sleep_ns;   // of a try at a wait, at most; 0: polled
 };
 
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -51,6 +52,20 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Whether a stage is there: after a suspended try, or at once.
+__device__ __forceinline__ bool try_stage(uint64_t *bar, uint32_t parity, uint32_t sleep_ns) {
+    if (sleep_ns > 0) return mbar_try_wait_ns(bar, parity, sleep_ns);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
@@ -147,9 +162,9 @@ __global__ void __launch_bounds__(kThreads) w4_rows_kernel(const RowsParams q) {
         const int s = c % q.stages, k0 = c * q.chunk;
         __nv_bfloat16 next[2];   // on their way while the copies are waited for, and a step ahead from then on
         load_scales(k0 + warp * kSub + t * 32, next);
-        if (!mbar_try_wait_ns(&full[s], (c / q.stages) & 1, q.sleep_ns)) {
+        if (!try_stage(&full[s], (c / q.stages) & 1, q.sleep_ns)) {
             const uint64_t since = global_ns();
-            while (!mbar_try_wait_ns(&full[s], (c / q.stages) & 1, q.sleep_ns)) {
+            while (!try_stage(&full[s], (c / q.stages) & 1, q.sleep_ns)) {
                 if (*(volatile int *)&abort || global_ns() - since > q.wait_limit_ns) {
                     abort = 1;
                     atomicCAS(q.status, 0, EP_ERR_TIMEOUT);
@@ -298,7 +313,7 @@ cudaError_t launch_w4_rows(const W4Params &w, bool fp4, int32_t *status, cudaStr
     q.w = w;
     q.status = status;
     q.wait_limit_ns = product_wait_limit();
-    q.sleep_ns = q.wait_limit_ns < kSleepNs ? (uint32_t)q.wait_limit_ns : kSleepNs;
+    q.sleep_ns = q.wait_limit_ns < kPollNs ? 0 : q.wait_limit_ns < kSleepNs ? (uint32_t)q.wait_limit_ns : kSleepNs;
     cut_rows(w, q);
     return w.rows <= 8 ? launch_n<1>(q, fp4, st) : launch_n<2>(q, fp4, st);
 }

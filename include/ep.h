@@ -567,7 +567,8 @@ int ep_product_status(void *stream);
 
 /* ep_product_wait_limit -- bound of every device-side wait of later products of the process, ns
  * (1000..6e10, default 2e9; host only). A wait is looked at when a suspended try of it ends, after
- * 10 to 20 us as measured, so a limit below that acts after it. EP_ERR_INVALID_ARG outside. */
+ * 10 to 20 us as measured, so a limit below that acts after it; only ep_product_w4's kernel for few rows
+ * keeps limits below 100 us by polling. EP_ERR_INVALID_ARG outside. */
 int ep_product_wait_limit(int64_t ns);
 
 /* -------------------------------------------------- products with 4-bit weights
