@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const Ba
     __threadfence();
     if (own && !few) put_lengths(p, threadIdx.x, kFinishThreads, lens[row]);
     Sum b, z;
-    for (int i = threadIdx.x; i < (int)gridDim.x; i += kFinishThreads) b.add(__ldcg(p.slots + i));
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kFinishThreads) b.add(__ldcg(p.slots + i));
     const long long all = (long long)p.pools * p.chunks;
     for (long long i = threadIdx.x; i < all; i += kFinishThreads) z.add(p.zpart[i]);
     const float bw = warp_sum(b.value()), zw = warp_sum(z.value());

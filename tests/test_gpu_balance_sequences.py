@@ -64,3 +64,19 @@ def test_time_grows_with_the_number_of_sequences(ragged):
         return min(took)
 
     assert least(32768) < 8 * least(8192)
+
+
+def test_as_many_sequences_as_there_may_be():
+    """2^31 - 1 of one token: the CTAs' numbers and the last one's walk over them stay in range (as a signed number
+    that walk passed 2^31). Half a minute: every pool has a CTA of its own. Sums of ones with what rounding takes
+    from them, one division: 2^-22."""
+    if torch.cuda.get_device_properties(0).total_memory < 100e9:
+        pytest.skip("needs the memory")
+    S = (1 << 31) - 1
+    z = torch.ones(S, 1, 1, dtype=BF16, device="cuda")
+    ids = torch.zeros(S, 1, 1, dtype=I32, device="cuda")
+    losses, counts = ep.balance_loss(z, ids, per_sequence=True)
+    assert ((losses - 1).abs() <= 2.0 ** -22).all()     # one expert, chosen by all; its logit's square is 1
+    assert bool((counts[::1 << 20] == 1).all()) and bool((counts[-4096:] == 1).all())
+    del losses, counts, z, ids
+    torch.cuda.empty_cache()
