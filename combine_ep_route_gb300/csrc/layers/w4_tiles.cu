@@ -16,12 +16,13 @@
 // Dense products with few tiles let up to four CTAs of a cluster share a tile's reduction and join
 // their sums through distributed shared memory.
 //
-// What bounds it: with few rows of x an SM's instructions (a step of the expanding warps takes 2400
-// cycles, 10 to an instruction with 28 warps on the SM; two are under way) and, not far below, the
-// codes' stream (64 experts of 7168 x 2048 with four rows each: 113 us, 4.4 TB/s; the copies alone 97);
-// with about 120 rows the same and the gated epilogue (64 experts of 2 x 1024 x 2048: 70 us, 920 TFLOP/s);
-// with more the tensor cores (64 experts of 2 x 2048 x 4096 under Zipf: 315 us, 1.2 PFLOP/s). What each
-// step gave (us, the three): the first kernel 228 / 111 / 476; one thread waits and issues 181 / 95 / 396;
+// What bounds it: no one unit is full. With few rows of x, the codes' stream with its waits and the expanding
+// instructions (64 experts of 7168 x 2048 with four rows each, int4: 115 us, 4.4 TB/s, the copies alone 97; issue
+// slots 66 % used, and warps wait for barriers and copies more than for anything else; yet fp4, whose decode takes
+// 17 instructions a word instead of 9, takes 133, and groups of 32 or 128 the same). With about 120 rows the same
+// and the gated epilogue (64 experts of 2 x 1024 x 2048: int4 63 us, fp4 68 to 70, 920 TFLOP/s; tensor pipe 49 %
+// busy). With more, each 128 rows expand their weight again, which keeps the tensor pipe at 68 % (64 experts of
+// 2 x 2048 x 4096 under Zipf: 309 to 315 us, 1.2 PFLOP/s). What each step gave (us, the three): the first kernel 228 / 111 / 476; one thread waits and issues 181 / 95 / 396;
 // steps of 256 158 / 93 / 347; warps that skip to their own steps 130 / 87 / 323; pairs of CTAs, x in a
 // ring of its own 134 / 76 / 304; x by one copy a step 120 / 76 / 289.
 #include "w4.cuh"
@@ -100,7 +101,7 @@ struct Ring {
     __device__ __forceinline__ void next(int slots) {
         if (++s == slots) s = 0, phase ^= 1;
     }
-    __device__ __forceinline__ void skip(int n, int slots) {   // n <= slots   // n <= slots
+    __device__ __forceinline__ void skip(int n, int slots) {   // n <= slots
         s += n;
         if (s >= slots) s -= slots, phase ^= 1;
     }

@@ -15,7 +15,8 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *, out: Optio
                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The norm of all ``grads`` together (float32, no dimensions), which are scaled in place by ``max_norm / norm``
     where it is finite and above ``max_norm``, and otherwise left as they are; a norm that is not finite is the
-    caller's to handle.
+    caller's to handle. (Finite elements have a finite norm in the 64 bits that decide: one past the largest float is
+    returned as infinity, and clipped.)
 
     ``grads`` are contiguous bf16 and float32 tensors of any shape on one CUDA device, of which no two overlap;
     ``max_norm`` of infinity gives the norm alone. With ``out`` (tensors of the same shapes and types) the

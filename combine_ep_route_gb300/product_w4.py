@@ -44,7 +44,8 @@ def _group(k: int, scales: torch.Tensor, axis: int) -> int:
 
 def pack_weight4(codes: torch.Tensor, scales: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """The layout that the products read: ``codes`` of any integer type ``[..., n, k]`` (a code in the low four
-    bits: 0..15, or -8..7 of an int8 tensor) and ``scales`` ``[..., n, k / group]`` as a checkpoint has them."""
+    bits: 0..15, or -8..7 of an int8 tensor) and ``scales`` ``[..., n, k / group]`` as a checkpoint has them, rounded to
+    bf16 (an fp16 scale loses up to three bits, 2^-8 of itself and of its weights). Codes have no zero point."""
     if codes.dim() < 2 or codes.is_floating_point() or codes.shape[-1] % 32 or codes.shape[-1] == 0:
         raise ValueError(f"codes: want integers [..., n, k] with k a multiple of 32, got {codes.dtype} {tuple(codes.shape)}")
     if scales.shape[:-1] != codes.shape[:-1]:

@@ -665,7 +665,8 @@ int ep_topk_route_backward(const ep_topk_t *args, const float *dweights, const v
  *   losses[0] = mean over the pools with tokens of sum_e E c_e / (top_k N) * (sum of p_e) / N,
  *               1 where choices and probabilities are even
  *   losses[1] = mean over all tokens of (log of the sum of exp(logit))^2, whatever the score
- * (0 without tokens). A logit of minus infinity or NaN takes no part in its token's
+ * (0 without tokens; losses[1] is infinite where the tokens' sum passes the largest float). A logit of minus
+ * infinity or NaN takes no part in its token's
  * probabilities, a token without any other adds nothing to either sum; ids outside 0..E-1 are
  * not counted. Sums do not depend on the order of execution.
  */
@@ -679,7 +680,8 @@ typedef struct ep_balance {
     const int32_t *num_tokens; /* device [seqs] or NULL */
 } ep_balance_t;
 
-/* ep_balance_workspace_bytes -- device workspace of ep_balance_loss (host only). */
+/* ep_balance_workspace_bytes -- device workspace of ep_balance_loss (host only): about 8 E bytes for each of
+ * up to 304 chunks of tokens, or of as many as there are pools or runs of 4096 tokens, if those are more. */
 int ep_balance_workspace_bytes(const ep_balance_t *args, size_t *bytes);
 
 /*
@@ -719,7 +721,8 @@ int ep_clip_workspace_bytes(const ep_grads_t *args, size_t *bytes);
  * and out[i] = grads[i] * max_norm / norm where norm is finite and above max_norm (>= 0; infinity:
  * the norm alone), else grads[i] unchanged. In place nothing is written then. The sum neither
  * overflows nor underflows where the elements do not, and does not depend on the order of
- * execution. out[i] may be grads[i]; nothing that is written may overlap another tensor
+ * execution. It is the norm in 64 bits that decides: of finite elements it is finite, and one past the
+ * largest float is written to *norm as infinity and clipped all the same. out[i] may be grads[i]; nothing that is written may overlap another tensor
  * (refused). The arrays are read before the call returns. The workspace is 16-byte aligned
  * and of the call alone until its kernels are done. Tensors whose grads[i] and out[i] differ in their address modulo 16
  * take several times as long.
