@@ -9,22 +9,36 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("score", ("softmax", "sigmoid"))
-@pytest.mark.parametrize("size", [(1217, 2, 24, 3), (2500, 1, 60, 4), (2433, 9, 8, 1), (1300, 3, 257, 8)])
+@pytest.mark.parametrize("size", [(1217, 2, 24, 3), (2500, 1, 60, 4), (2433, 9, 8, 1), (1300, 3, 257, 8), (1400, 2, 128, 4), (1250, 2, 256, 8),
+                                  (1250, 2, 512, 8), (1300, 2, 1024, 16), (1219, 1, 1001, 16)])
 @pytest.mark.parametrize("ragged", (False, True))
 @pytest.mark.parametrize("per_sequence", (False, True))
-def test_more_sequences_than_work_at_a_time(per_sequence, ragged, size, score):
-    z, ids, lengths = inputs(*size, F32, 3, ragged)
-    check(z, ids, lengths, score, per_sequence)
+@pytest.mark.parametrize("dtype", (F32, BF16))
+def test_more_sequences_than_work_at_a_time(dtype, per_sequence, ragged, size, score):
+    z, ids, lengths = inputs(*size, dtype, 3, ragged)
+    zc, _, _, counts, grad, kw, dl = check(z, ids, lengths, score, per_sequence)
+    # added to what is there: the gradient and one more rounding, rows without a token left alone
+    out = torch.ones_like(zc)
+    ep.balance_loss_backward(dl, zc, counts, size[3], out=out, accumulate=True, **kw)
+    used = torch.ones(size[:2], dtype=torch.bool, device="cuda") if lengths is None else \
+        torch.arange(size[1], device="cuda") < lengths.cuda()[:, None]
+    assert (out[~used] == 1).all()
+    want = 1 + grad[used].double()
+    # (in bf16 the gradient compared with is rounded too)
+    off = want.abs() * (2.0 ** -8 if dtype is BF16 else 2.0 ** -24) + (grad[used].double().abs() * 2.0 ** -8 if dtype is BF16 else 0)
+    assert ((out[used].double() - want).abs() <= off).all()
 
 
-def test_more_tokens_than_work_at_a_time():
-    """Chunks of 4096 tokens, the most there are, and more of them than CTAs."""
+@pytest.mark.parametrize("lengths", (False, True))
+def test_more_tokens_than_work_at_a_time(lengths):
+    """Chunks of 4096 tokens, the most there are, and more of them than a gradient with lengths has CTAs."""
     T, E = 4096 * 1216 + 4097, 8
     z = torch.randn(1, T, E, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(BF16)
     ids = torch.zeros(1, T, 1, dtype=I32, device="cuda")
-    _, counts = ep.balance_loss(z, ids)
+    kw = dict(num_tokens=torch.tensor([T], dtype=I32, device="cuda")) if lengths else {}
+    _, counts = ep.balance_loss(z, ids, **kw)
     d = torch.tensor([0.0, float(T)], device="cuda")
-    grad = ep.balance_loss_backward(d, z, counts, 1)
+    grad = ep.balance_loss_backward(d, z, counts, 1, **kw)
     for at in (0, T // 2, 4096 * 1216 - 2048, 4096 * 1216 + 2048, T - 2048):
         own = z[0, at:at + 2048].double()
         want = 2 * torch.logsumexp(own, -1, keepdim=True) * torch.softmax(own, -1)
